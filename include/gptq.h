@@ -47,9 +47,10 @@ typedef enum {
   GPTQ_ERR_NULL_POINTER = 1,    /* a required pointer is NULL            */
   GPTQ_ERR_BAD_SIZE = 2,        /* a size is negative or zero             */
   GPTQ_ERR_BAD_LEADING_DIM = 3, /* ld_* smaller than the row width        */
-  GPTQ_ERR_BAD_DTYPE = 4,       /* element type not GPTQ_F32 / GPTQ_F16   */
+  GPTQ_ERR_BAD_DTYPE = 4,       /* element type that the call does not take */
   GPTQ_ERR_BAD_BITS = 5,        /* bits outside [2, 8]                    */
   GPTQ_ERR_BAD_BLOCK = 6,       /* block_size not one of 16, 32, 64, 128  */
+                                /* (block_rows of fp8 codes: not 1 or 128) */
   GPTQ_ERR_BAD_GROUP = 7,       /* group_size not 0 / 16k aligned with B  */
   GPTQ_ERR_WORKSPACE = 8,       /* ws NULL or smaller than the query      */
   GPTQ_ERR_BAD_DAMP = 9,        /* percdamp negative or not finite        */
@@ -61,7 +62,8 @@ typedef enum {
 
 typedef enum {
   GPTQ_F32 = 0, /* IEEE binary32 */
-  GPTQ_F16 = 1  /* IEEE binary16 */
+  GPTQ_F16 = 1, /* IEEE binary16 */
+  GPTQ_BF16 = 2 /* bfloat16: the gptq_fp8_* and gptq_token_logprobs calls only */
 } gptq_dtype;
 
 /*
@@ -310,6 +312,70 @@ size_t gptq2d_quantize_workspace_size(int64_t m, int64_t n);
 gptq_status gptq2d_quantize(const void* X, int32_t x_dtype, int64_t m, int64_t n, int64_t ldx, const float* U_Q,
                             const float* U_P, int32_t bits, uint8_t* codes, int64_t ld_codes, float* scale,
                             int32_t* zero, double* out_err, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * 8-bit floating-point layers: e4m3 codes (4 exponent bits, bias 7, 3 fraction
+ * bits, largest value 448, no infinities, NaN = 0x7F / 0xFF) with one fp32 scale
+ * per block of 128 columns.  Nothing is calibrated: a layer's weights are coded
+ * once, its inputs on every call, and the product runs on the 8-bit matrix cores.
+ *
+ * gptq_fp8_quantize: X [device] [m x k] (x_dtype GPTQ_F32, GPTQ_F16 or GPTQ_BF16,
+ *   leading dimension ld_x >= k) -> codes [device] uint8 [m x ld_codes] (ld_codes >=
+ *   k; bytes past column k are left as they are) and scales [device] float, with
+ *   X ~ scale * code.  m == 0 is a no-op.
+ *   block_rows 1:   one scale per row and block of 128 columns (activations), stored
+ *                   block by block: scales[b * ld_scales + i], ld_scales >= m.
+ *   block_rows 128: one scale per tile of 128 rows x 128 columns (weights):
+ *                   scales[(i / 128) * ld_scales + b], ld_scales >= ceil(k / 128).
+ *   Per block: a = the largest finite |x|; scale = 2^e with e the smallest integer
+ *   >= -126 such that a <= 448 * 2^e (scale 1 if a == 0); code = x / scale (exact)
+ *   rounded once to nearest even.  Elements that are NaN or infinite become NaN
+ *   codes (0x7F) and take no part in a.
+ *
+ * gptq_fp8_matmul: Y [device] [m x n] (y_dtype GPTQ_F32, GPTQ_F16 or GPTQ_BF16,
+ *   leading dimension ld_y >= n) with
+ *     Y[i][j] = bias[j] + sum_b x_scales[b * ld_xs + i] * w_scales[(j / 128) * ld_ws + b]
+ *                         * sum_{c = 128 b}^{min(128 b + 128, k) - 1} x_codes[i][c] w_codes[j][c]
+ *   in fp32, rounded once to y_dtype.  x_codes [device] [m x ld_x], x_scales [device]
+ *   float [ceil(k / 128) x ld_xs], ld_xs >= m; w_codes [device] [n x ld_w], w_scales
+ *   [device] float [ceil(n / 128) x ld_ws], ld_ws >= ceil(k / 128): the outputs of
+ *   gptq_fp8_quantize with block_rows 1 and 128, or any codes and fp32 scales in that
+ *   layout.  bias: NULL or [device] n values of y_dtype.  Code rows may start at any
+ *   address; with ld_x, ld_w and both base addresses multiples of 16 the wide loads
+ *   are used.  m == 0 is a no-op.  Results are bitwise reproducible for a given shape
+ *   and alignment.  ws: >= gptq_fp8_matmul_workspace_size() bytes (may be 0).
+ */
+gptq_status gptq_fp8_quantize(const void* X, int32_t x_dtype, int64_t m, int64_t k, int64_t ld_x, int64_t block_rows,
+                              uint8_t* codes, int64_t ld_codes, float* scales, int64_t ld_scales, void* stream);
+size_t gptq_fp8_matmul_workspace_size(int64_t m, int64_t n, int64_t k);
+gptq_status gptq_fp8_matmul(const uint8_t* x_codes, int64_t ld_x, const float* x_scales, int64_t ld_xs,
+                            const uint8_t* w_codes, int64_t ld_w, const float* w_scales, int64_t ld_ws, int64_t m,
+                            int64_t n, int64_t k, const void* bias, void* Y, int32_t y_dtype, int64_t ld_y, void* ws,
+                            size_t ws_bytes, void* stream);
+
+/*
+ * What a (quantized) model says about a text: per row of logits the log probability
+ * of the given token, the entropy, and the most probable tokens.
+ *
+ * gptq_token_logprobs: logits [device] [n x v] (dtype GPTQ_F32, GPTQ_F16 or GPTQ_BF16,
+ *   leading dimension ld >= v), tokens [device] int64 [n]; with p = softmax of a row:
+ *   logprobs     [device] float [n]: log p(tokens[i]); 0 where tokens[i] < 0 (no token
+ *                there), NaN where tokens[i] >= v.
+ *   entropy      [device] float [n]: -sum p log p, in nats.
+ *   top_ids      [device] int32 [n x top_k], top_logprobs [device] float [n x top_k]: the
+ *                top_k largest logits, largest first, equal ones by lower index.
+ *                0 <= top_k <= min(v, GPTQ_MAX_TOP); both may be NULL when top_k == 0.
+ *   A logit of -inf is a token of probability 0.  A row that holds a NaN or +inf, or
+ *   nothing but -inf, has no softmax: its entropy, top_logprobs and logprobs (but those
+ *   of tokens < 0) are NaN, and top_ids orders its logits with NaN above +inf.
+ *   n == 0 is a no-op.  fp32 arithmetic; bitwise reproducible for a given shape and
+ *   alignment.  ws: >= gptq_token_logprobs_workspace_size() bytes (may be 0).
+ */
+#define GPTQ_MAX_TOP 64
+size_t gptq_token_logprobs_workspace_size(int64_t n, int64_t v, int64_t top_k);
+gptq_status gptq_token_logprobs(const void* logits, int32_t dtype, int64_t n, int64_t v, int64_t ld, const int64_t* tokens,
+                                int64_t top_k, float* logprobs, float* entropy, int32_t* top_ids, float* top_logprobs,
+                                void* ws, size_t ws_bytes, void* stream);
 
 /*
  * Per-launch timing of the quantization loop -- a measurement aid, off by

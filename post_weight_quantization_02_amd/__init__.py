@@ -27,12 +27,16 @@ __all__ = [
     "gptq_act_order_perm", "gptq_prepare_hinv_perm", "gptq_quantize_layer_perm",
     "gptq_packed_words_per_row", "gptq_pack_codes", "gptq_dequant_matmul", "gptq_dequantize",
     "gptq2d_quantize", "gptq2d_quantize_workspace_size",
+    "GPTQ_BF16", "GPTQ_MAX_TOP", "gptq_fp8_quantize", "gptq_fp8_matmul", "gptq_fp8_matmul_workspace_size",
+    "gptq_token_logprobs", "gptq_token_logprobs_workspace_size",
     "gptq_launch_timing", "gptq_launch_timing_read", "TIMING_PANEL", "TIMING_PRODUCT",
     "gptq_status_string", "gptq_version", "quantize_layer",
 ]
 
 GPTQ_F32 = 0
 GPTQ_F16 = 1
+GPTQ_BF16 = 2                           # the fp8 and log-probability calls only
+GPTQ_MAX_TOP = 64                       # include/gptq.h
 GPTQ_NOALLOC_SCRATCH_BYTES = 96 << 20   # include/gptq.h
 TIMING_PANEL, TIMING_PRODUCT = 0, 1     # kinds of gptq_launch_timing_read
 
@@ -106,6 +110,16 @@ def library() -> ctypes.CDLL:
     lib.gptq2d_quantize.restype = i32
     lib.gptq_dequantize.argtypes = [vp, i64, i64, i64, vp, vp, i64, vp, vp, i32, i64, vp]
     lib.gptq_dequantize.restype = i32
+    lib.gptq_fp8_quantize.argtypes = [vp, i32, i64, i64, i64, i64, vp, i64, vp, i64, vp]
+    lib.gptq_fp8_quantize.restype = i32
+    lib.gptq_fp8_matmul_workspace_size.argtypes = [i64, i64, i64]
+    lib.gptq_fp8_matmul_workspace_size.restype = sz
+    lib.gptq_fp8_matmul.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, i64, i64, i64, vp, vp, i32, i64, vp, sz, vp]
+    lib.gptq_fp8_matmul.restype = i32
+    lib.gptq_token_logprobs_workspace_size.argtypes = [i64, i64, i64]
+    lib.gptq_token_logprobs_workspace_size.restype = sz
+    lib.gptq_token_logprobs.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, vp, vp, vp, vp, sz, vp]
+    lib.gptq_token_logprobs.restype = i32
     lib.gptq_launch_timing.argtypes = [i32]
     lib.gptq_launch_timing.restype = i32
     lib.gptq_launch_timing_read.argtypes = [i32, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(i64),
@@ -183,6 +197,62 @@ def _workspace(nbytes: int, device, ws=None):
 def _check(status: int, where: str):
     if status != 0:
         raise GPTQError(status, where)
+
+
+def _elem_code(t, name) -> int:
+    """Element type of the fp8 and log-probability calls."""
+    torch = _torch()
+    code = {torch.float32: GPTQ_F32, torch.float16: GPTQ_F16, torch.bfloat16: GPTQ_BF16}.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+    return code
+
+
+def _expect(t, name, shape, dtypes, device):
+    """A tensor of that shape and one of those dtypes on that device, its last
+    dimension contiguous and its rows not overlapping."""
+    if not isinstance(dtypes, tuple):
+        dtypes = (dtypes,)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have unit stride in its last dimension")
+    if t.dim() == 2 and t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name} has overlapping rows")
+
+
+def _no_grad(where, *tensors):
+    if _torch().is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        raise ValueError(f"{where} has no backward pass: detach its inputs or call it under torch.no_grad()")
+
+
+def _device_scope(device, stream):
+    """Makes the tensors' device the current one for a call; a given stream has to
+    belong to it."""
+    if stream is not None and stream.device != device:
+        raise ValueError(f"the stream belongs to {stream.device}, the tensors to {device}")
+    return _torch().cuda.device(device)
+
+
+def _pitch(t) -> int:
+    """Leading dimension: the row stride, also of a matrix of one row or none."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def _ws_ptr(nbytes: int, device, ws):
+    """(tensor or None, address, bytes) of a workspace that may be empty."""
+    torch = _torch()
+    if ws is None:
+        if nbytes == 0:
+            return None, None, 0
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    elif ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous tensor on {device}")
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 # --------------------------------------------------------------------------- C names
@@ -414,6 +484,115 @@ def gptq_dequant_matmul(packed, bits: int, scales, zeros, group_size: int, X, d_
                                        Y.stride(0), _stream(stream, packed, scales, zeros, perm, X, Y))
     _check(st, "gptq_dequant_matmul")
     return Y
+
+
+def gptq_fp8_quantize(X, block_rows: int = 1, codes=None, scales=None, stream=None):
+    """e4m3 codes of X [m x k] (fp32, fp16 or bf16) with one power-of-two fp32 scale
+    per row and 128 columns (``block_rows=1``, activations) or per 128 x 128 tile
+    (``block_rows=128``, weights).  Returns (codes float8_e4m3fn [m x k], scales):
+    scales [ceil(k/128) x m], or [ceil(m/128) x ceil(k/128)] for tiles.  The codes
+    made here have rows a multiple of 128 bytes apart."""
+    torch = _torch()
+    _rowmajor(X, "X")
+    _no_grad("gptq_fp8_quantize", X)
+    code = _elem_code(X, "X")
+    m, k = X.shape
+    dev = X.device
+    kb = -(-k // 128)
+    shape = (kb, m) if block_rows == 1 else (-(-m // 128), kb)
+    with _device_scope(dev, stream):
+        if codes is None:
+            codes = torch.empty(m, kb * 128, dtype=torch.float8_e4m3fn, device=dev)[:, :k]
+        if scales is None:
+            scales = torch.empty(shape, dtype=torch.float32, device=dev)
+        _expect(codes, "codes", (m, k), (torch.float8_e4m3fn, torch.uint8), dev)
+        _expect(scales, "scales", shape, torch.float32, dev)
+        st = library().gptq_fp8_quantize(X.data_ptr(), code, m, k, _pitch(X), int(block_rows), codes.data_ptr(),
+                                         _pitch(codes), scales.data_ptr(), _pitch(scales),
+                                         _stream(stream, X, codes, scales))
+    _check(st, "gptq_fp8_quantize")
+    return codes, scales
+
+
+def gptq_fp8_matmul_workspace_size(m: int, n: int, k: int) -> int:
+    return int(library().gptq_fp8_matmul_workspace_size(m, n, k))
+
+
+def gptq_fp8_matmul(x_codes, x_scales, w_codes, w_scales, bias=None, Y=None, out_dtype=None, ws=None,
+                    stream=None):
+    """Y [m x n] = X W^T (+ bias) from e4m3 codes (float8_e4m3fn or uint8 bit patterns)
+    x_codes [m x k], w_codes [n x k] and fp32 scales x_scales [ceil(k/128) x m],
+    w_scales [ceil(n/128) x ceil(k/128)]; fp32 sums, rounded once to Y's dtype
+    (``out_dtype``: fp32, fp16 or bf16; fp32 if not given).  bias: n values of that dtype."""
+    torch = _torch()
+    _rowmajor(x_codes, "x_codes")
+    m, k = x_codes.shape
+    dev = x_codes.device
+    if w_codes.dim() != 2:
+        raise ValueError("w_codes must be a 2-D tensor")
+    n, kb = w_codes.shape[0], -(-k // 128)
+    fp8 = (torch.float8_e4m3fn, torch.uint8)
+    _expect(x_codes, "x_codes", (m, k), fp8, dev)
+    _expect(w_codes, "w_codes", (n, k), fp8, dev)
+    _expect(x_scales, "x_scales", (kb, m), torch.float32, dev)
+    _expect(w_scales, "w_scales", (-(-n // 128), kb), torch.float32, dev)
+    _no_grad("gptq_fp8_matmul", x_codes, x_scales, w_codes, w_scales, bias, Y)
+    with _device_scope(dev, stream):
+        if Y is None:
+            Y = torch.empty(m, n, dtype=out_dtype or torch.float32, device=dev)
+        y_code = _elem_code(Y, "Y")
+        _expect(Y, "Y", (m, n), out_dtype or Y.dtype, dev)
+        if bias is not None:
+            _expect(bias, "bias", (n,), Y.dtype, dev)
+        ws, ws_ptr, ws_bytes = _ws_ptr(gptq_fp8_matmul_workspace_size(m, n, k), dev, ws)
+        st = library().gptq_fp8_matmul(x_codes.data_ptr(), _pitch(x_codes), x_scales.data_ptr(), _pitch(x_scales),
+                                       w_codes.data_ptr(), _pitch(w_codes), w_scales.data_ptr(), _pitch(w_scales),
+                                       m, n, k, _ptr(bias), Y.data_ptr(), y_code, _pitch(Y), ws_ptr, ws_bytes,
+                                       _stream(stream, x_codes, x_scales, w_codes, w_scales, bias, Y, ws))
+    _check(st, "gptq_fp8_matmul")
+    return Y
+
+
+def gptq_token_logprobs_workspace_size(n: int, v: int, top_k: int = 0) -> int:
+    return int(library().gptq_token_logprobs_workspace_size(n, v, top_k))
+
+
+def gptq_token_logprobs(logits, tokens, top_k: int = 0, logprobs=None, entropy=None, top_ids=None,
+                        top_logprobs=None, ws=None, stream=None):
+    """Per row of logits [n x v] (fp32, fp16 or bf16): the log probability of
+    tokens[i] (int64 [n]; 0 where the token is negative: none there), the entropy in
+    nats, and the top_k <= 64 most probable tokens (equal logits: lower index first).
+    Returns (logprobs [n], entropy [n], top_ids int32 [n x top_k], top_logprobs
+    [n x top_k]), fp32 but for the ids."""
+    torch = _torch()
+    _rowmajor(logits, "logits")
+    _no_grad("gptq_token_logprobs", logits)
+    code = _elem_code(logits, "logits")
+    n, v = logits.shape
+    dev = logits.device
+    top_k = int(top_k)
+    _expect(tokens, "tokens", (n,), torch.int64, dev)
+    with _device_scope(dev, stream):
+        def out(t, name, shape, dtype):
+            if t is None:
+                return torch.empty(shape, dtype=dtype, device=dev)
+            _expect(t, name, shape, dtype, dev)
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+            return t
+
+        logprobs = out(logprobs, "logprobs", (n,), torch.float32)
+        entropy = out(entropy, "entropy", (n,), torch.float32)
+        top_ids = out(top_ids, "top_ids", (n, max(top_k, 0)), torch.int32)
+        top_logprobs = out(top_logprobs, "top_logprobs", (n, max(top_k, 0)), torch.float32)
+        ws, ws_ptr, ws_bytes = _ws_ptr(gptq_token_logprobs_workspace_size(n, v, top_k), dev, ws)
+        st = library().gptq_token_logprobs(logits.data_ptr(), code, n, v, _pitch(logits), tokens.data_ptr(), top_k,
+                                           logprobs.data_ptr(), entropy.data_ptr(), top_ids.data_ptr(),
+                                           top_logprobs.data_ptr(), ws_ptr, ws_bytes,
+                                           _stream(stream, logits, tokens, logprobs, entropy, top_ids, top_logprobs,
+                                                   ws))
+    _check(st, "gptq_token_logprobs")
+    return logprobs, entropy, top_ids, top_logprobs
 
 
 def gptq_launch_timing(enable: bool) -> None:

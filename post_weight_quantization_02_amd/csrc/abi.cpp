@@ -298,6 +298,66 @@ gptq_status gptq_dequant_matmul(const uint32_t* packed, int64_t ld_packed, int32
                                               (hipStream_t)stream));
 }
 
+static bool elem_ok(int32_t d) { return d == GPTQ_F32 || d == GPTQ_F16 || d == GPTQ_BF16; }
+
+gptq_status gptq_fp8_quantize(const void* X, int32_t x_dtype, int64_t m, int64_t k, int64_t ld_x, int64_t block_rows,
+                              uint8_t* codes, int64_t ld_codes, float* scales, int64_t ld_scales, void* stream) {
+  if (m < 0 || k <= 0) return GPTQ_ERR_BAD_SIZE;
+  if (m > kMaxDim || k > kMaxDim) return GPTQ_ERR_TOO_LARGE;
+  if (!elem_ok(x_dtype)) return GPTQ_ERR_BAD_DTYPE;
+  if (block_rows != 1 && block_rows != 128) return GPTQ_ERR_BAD_BLOCK;
+  if (m == 0) return GPTQ_OK;
+  if (X == nullptr || codes == nullptr || scales == nullptr) return GPTQ_ERR_NULL_POINTER;
+  if (ld_x < k || ld_codes < k || ld_scales < (block_rows == 1 ? m : gptq::cdiv(k, 128)))
+    return GPTQ_ERR_BAD_LEADING_DIM;
+  return from_hip(gptq::fp8_quantize_launch(X, x_dtype, m, k, ld_x, block_rows, codes, ld_codes, scales, ld_scales,
+                                            (hipStream_t)stream));
+}
+
+size_t gptq_fp8_matmul_workspace_size(int64_t m, int64_t n, int64_t k) {
+  if (m <= 0 || n <= 0 || k <= 0 || m > kMaxDim || n > kMaxDim || k > kMaxDim) return 0;
+  return gptq::fp8_plan(m, n, k).ws_bytes;
+}
+
+gptq_status gptq_fp8_matmul(const uint8_t* x_codes, int64_t ld_x, const float* x_scales, int64_t ld_xs,
+                            const uint8_t* w_codes, int64_t ld_w, const float* w_scales, int64_t ld_ws, int64_t m,
+                            int64_t n, int64_t k, const void* bias, void* Y, int32_t y_dtype, int64_t ld_y, void* ws,
+                            size_t ws_bytes, void* stream) {
+  if (m < 0 || n <= 0 || k <= 0) return GPTQ_ERR_BAD_SIZE;
+  if (m > kMaxDim || n > kMaxDim || k > kMaxDim) return GPTQ_ERR_TOO_LARGE;
+  if (!elem_ok(y_dtype)) return GPTQ_ERR_BAD_DTYPE;
+  if (m == 0) return GPTQ_OK;
+  if (x_codes == nullptr || x_scales == nullptr || w_codes == nullptr || w_scales == nullptr || Y == nullptr)
+    return GPTQ_ERR_NULL_POINTER;
+  if (ld_x < k || ld_w < k || ld_xs < m || ld_ws < gptq::cdiv(k, 128) || ld_y < n) return GPTQ_ERR_BAD_LEADING_DIM;
+  const gptq::Fp8Plan plan = gptq::fp8_plan(m, n, k);
+  if (gptq_status st = ws_check(ws, ws_bytes, plan.ws_bytes)) return st;
+  const gptq::Fp8Args p{x_codes, ld_x, x_scales, ld_xs, w_codes, ld_w, w_scales, ld_ws, m, n, k, bias, Y, y_dtype, ld_y};
+  return from_hip(gptq::fp8_matmul_launch(plan, p, ws, (hipStream_t)stream));
+}
+
+size_t gptq_token_logprobs_workspace_size(int64_t n, int64_t v, int64_t top_k) {
+  if (n <= 0 || v <= 0 || n > kMaxDim || v > kMaxDim || top_k < 0 || top_k > GPTQ_MAX_TOP || top_k > v) return 0;
+  return gptq::logprob_plan(n, v, top_k).ws_bytes;
+}
+
+gptq_status gptq_token_logprobs(const void* logits, int32_t dtype, int64_t n, int64_t v, int64_t ld, const int64_t* tokens,
+                                int64_t top_k, float* logprobs, float* entropy, int32_t* top_ids, float* top_logprobs,
+                                void* ws, size_t ws_bytes, void* stream) {
+  if (n < 0 || v <= 0 || top_k < 0 || top_k > GPTQ_MAX_TOP || top_k > v) return GPTQ_ERR_BAD_SIZE;
+  if (n > kMaxDim || v > kMaxDim) return GPTQ_ERR_TOO_LARGE;
+  if (!elem_ok(dtype)) return GPTQ_ERR_BAD_DTYPE;
+  if (n == 0) return GPTQ_OK;
+  if (logits == nullptr || tokens == nullptr || logprobs == nullptr || entropy == nullptr ||
+      (top_k > 0 && (top_ids == nullptr || top_logprobs == nullptr)))
+    return GPTQ_ERR_NULL_POINTER;
+  if (ld < v) return GPTQ_ERR_BAD_LEADING_DIM;
+  const gptq::LogprobPlan plan = gptq::logprob_plan(n, v, top_k);
+  if (gptq_status st = ws_check(ws, ws_bytes, plan.ws_bytes)) return st;
+  const gptq::LogprobArgs p{logits, dtype, n, v, ld, tokens, (int)top_k, logprobs, entropy, top_ids, top_logprobs};
+  return from_hip(gptq::logprob_launch(plan, p, ws, (hipStream_t)stream));
+}
+
 gptq_status gptq_launch_timing(int32_t enable) {
   gptq::thread_timer().on = enable != 0;
   return GPTQ_OK;
@@ -337,7 +397,7 @@ const char* gptq_status_string(int32_t status) {
     case GPTQ_ERR_BAD_LEADING_DIM: return "leading dimension smaller than the row width";
     case GPTQ_ERR_BAD_DTYPE: return "unsupported element type";
     case GPTQ_ERR_BAD_BITS: return "bits must be in [2, 8] (2, 3, 4 or 8 for packed codes)";
-    case GPTQ_ERR_BAD_BLOCK: return "block_size must be 16, 32, 64 or 128";
+    case GPTQ_ERR_BAD_BLOCK: return "block_size must be 16, 32, 64 or 128 (block_rows of fp8 codes: 1 or 128)";
     case GPTQ_ERR_BAD_GROUP: return "group_size must be 0, or a multiple of 16 that divides or is divided by block_size";
     case GPTQ_ERR_WORKSPACE: return "workspace missing or smaller than the query";
     case GPTQ_ERR_BAD_DAMP: return "percdamp must be finite and >= 0";

@@ -69,6 +69,54 @@ hipError_t dequant_matmul_launch(const uint32_t* packed, int64_t ld_packed, int 
                                  int64_t d_col, const void* X, int x_dtype, int m, int64_t ld_x, float* Y,
                                  int64_t ld_y, hipStream_t s);
 
+// ---------------------------------------------------------------- element types of the fp8 and logits calls
+enum { kF32 = 0, kF16 = 1, kBF16 = 2 };
+
+// ---------------------------------------------------------------- fp8 codes with block scales
+hipError_t fp8_quantize_launch(const void* X, int x_dtype, int64_t m, int64_t k, int64_t ld_x, int64_t block_rows,
+                               uint8_t* codes, int64_t ld_codes, float* scales, int64_t ld_scales, hipStream_t s);
+
+struct Fp8Plan {
+  size_t ws_bytes;
+};
+Fp8Plan fp8_plan(int64_t m, int64_t n, int64_t k);
+struct Fp8Args {
+  const uint8_t* X;
+  int64_t ld_x;
+  const float* sx;        // [ceil(k / 128)][m]
+  int64_t ld_sx;
+  const uint8_t* W;
+  int64_t ld_w;
+  const float* sw;        // [ceil(n / 128)][ceil(k / 128)]
+  int64_t ld_sw;
+  int64_t m, n, k;
+  const void* bias;       // nullptr or n values of Y's type
+  void* Y;
+  int y_dtype;
+  int64_t ld_y;
+};
+hipError_t fp8_matmul_launch(const Fp8Plan& plan, const Fp8Args& p, void* ws, hipStream_t s);
+
+// ---------------------------------------------------------------- log probabilities
+struct LogprobPlan {
+  int splits;             // parts of a row, joined by a second launch when more than one
+  int64_t span;           // elements of a part
+  size_t ws_bytes;
+};
+LogprobPlan logprob_plan(int64_t n, int64_t v, int64_t top_k);
+struct LogprobArgs {
+  const void* logits;
+  int dtype;
+  int64_t n, v, ld;
+  const int64_t* tokens;
+  int top_k;
+  float* logprobs;
+  float* entropy;
+  int32_t* top_ids;
+  float* top_logprobs;
+};
+hipError_t logprob_launch(const LogprobPlan& plan, const LogprobArgs& p, void* ws, hipStream_t s);
+
 // ---------------------------------------------------------------- two-sided rounding
 struct Plan2D {
   int64_t m, n, Mb, Nb;   // matrix and 32-tile counts
