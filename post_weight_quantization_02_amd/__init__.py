@@ -199,10 +199,15 @@ def _check(status: int, where: str):
         raise GPTQError(status, where)
 
 
+_ELEM = {}
+
+
 def _elem_code(t, name) -> int:
     """Element type of the fp8 and log-probability calls."""
-    torch = _torch()
-    code = {torch.float32: GPTQ_F32, torch.float16: GPTQ_F16, torch.bfloat16: GPTQ_BF16}.get(t.dtype)
+    if not _ELEM:
+        torch = _torch()
+        _ELEM.update({torch.float32: GPTQ_F32, torch.float16: GPTQ_F16, torch.bfloat16: GPTQ_BF16})
+    code = _ELEM.get(t.dtype)
     if code is None:
         raise TypeError(f"{name}: unsupported dtype {t.dtype}")
     return code
@@ -211,18 +216,17 @@ def _elem_code(t, name) -> int:
 def _expect(t, name, shape, dtypes, device):
     """A tensor of that shape and one of those dtypes on that device, its last
     dimension contiguous and its rows not overlapping."""
-    if not isinstance(dtypes, tuple):
-        dtypes = (dtypes,)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: unsupported dtype {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
-    if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name} must have unit stride in its last dimension")
-    if t.dim() == 2 and t.shape[0] > 1 and t.stride(0) < t.shape[1]:
-        raise ValueError(f"{name} has overlapping rows")
+    if not t.is_contiguous():
+        if shape[-1] > 1 and t.stride(-1) != 1:
+            raise ValueError(f"{name} must have unit stride in its last dimension")
+        if len(shape) == 2 and shape[0] > 1 and t.stride(0) < shape[1]:
+            raise ValueError(f"{name} has overlapping rows")
 
 
 def _no_grad(where, *tensors):
@@ -230,12 +234,20 @@ def _no_grad(where, *tensors):
         raise ValueError(f"{where} has no backward pass: detach its inputs or call it under torch.no_grad()")
 
 
-def _device_scope(device, stream):
-    """Makes the tensors' device the current one for a call; a given stream has to
-    belong to it."""
+def _launch(device, stream, fn, args, tensors, where):
+    """fn(*args, stream handle) on ``device``: on its current stream, or on ``stream``,
+    which has to belong to it (ordered as in _stream)."""
+    torch = _torch()
     if stream is not None and stream.device != device:
-        raise ValueError(f"the stream belongs to {stream.device}, the tensors to {device}")
-    return _torch().cuda.device(device)
+        raise ValueError(f"{where}: the stream belongs to {stream.device}, the tensors to {device}")
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _launch(device, stream, fn, args, tensors, where)
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(device.index)     # current_stream() without the Python object
+    else:
+        handle = _stream(stream, *tensors)
+    _check(fn(*args, handle), where)
 
 
 def _pitch(t) -> int:
@@ -500,17 +512,19 @@ def gptq_fp8_quantize(X, block_rows: int = 1, codes=None, scales=None, stream=No
     dev = X.device
     kb = -(-k // 128)
     shape = (kb, m) if block_rows == 1 else (-(-m // 128), kb)
-    with _device_scope(dev, stream):
-        if codes is None:
-            codes = torch.empty(m, kb * 128, dtype=torch.float8_e4m3fn, device=dev)[:, :k]
-        if scales is None:
-            scales = torch.empty(shape, dtype=torch.float32, device=dev)
+    if codes is None:
+        codes = torch.empty((m, kb * 128), dtype=torch.float8_e4m3fn, device=dev)
+        if k != kb * 128:
+            codes = codes[:, :k]
+    else:
         _expect(codes, "codes", (m, k), (torch.float8_e4m3fn, torch.uint8), dev)
-        _expect(scales, "scales", shape, torch.float32, dev)
-        st = library().gptq_fp8_quantize(X.data_ptr(), code, m, k, _pitch(X), int(block_rows), codes.data_ptr(),
-                                         _pitch(codes), scales.data_ptr(), _pitch(scales),
-                                         _stream(stream, X, codes, scales))
-    _check(st, "gptq_fp8_quantize")
+    if scales is None:
+        scales = torch.empty(shape, dtype=torch.float32, device=dev)
+    else:
+        _expect(scales, "scales", shape, (torch.float32,), dev)
+    _launch(dev, stream, library().gptq_fp8_quantize,
+            (X.data_ptr(), code, m, k, _pitch(X), int(block_rows), codes.data_ptr(), _pitch(codes), scales.data_ptr(),
+             _pitch(scales)), (X, codes, scales), "gptq_fp8_quantize")
     return codes, scales
 
 
@@ -534,22 +548,21 @@ def gptq_fp8_matmul(x_codes, x_scales, w_codes, w_scales, bias=None, Y=None, out
     fp8 = (torch.float8_e4m3fn, torch.uint8)
     _expect(x_codes, "x_codes", (m, k), fp8, dev)
     _expect(w_codes, "w_codes", (n, k), fp8, dev)
-    _expect(x_scales, "x_scales", (kb, m), torch.float32, dev)
-    _expect(w_scales, "w_scales", (-(-n // 128), kb), torch.float32, dev)
-    _no_grad("gptq_fp8_matmul", x_codes, x_scales, w_codes, w_scales, bias, Y)
-    with _device_scope(dev, stream):
-        if Y is None:
-            Y = torch.empty(m, n, dtype=out_dtype or torch.float32, device=dev)
-        y_code = _elem_code(Y, "Y")
-        _expect(Y, "Y", (m, n), out_dtype or Y.dtype, dev)
-        if bias is not None:
-            _expect(bias, "bias", (n,), Y.dtype, dev)
-        ws, ws_ptr, ws_bytes = _ws_ptr(gptq_fp8_matmul_workspace_size(m, n, k), dev, ws)
-        st = library().gptq_fp8_matmul(x_codes.data_ptr(), _pitch(x_codes), x_scales.data_ptr(), _pitch(x_scales),
-                                       w_codes.data_ptr(), _pitch(w_codes), w_scales.data_ptr(), _pitch(w_scales),
-                                       m, n, k, _ptr(bias), Y.data_ptr(), y_code, _pitch(Y), ws_ptr, ws_bytes,
-                                       _stream(stream, x_codes, x_scales, w_codes, w_scales, bias, Y, ws))
-    _check(st, "gptq_fp8_matmul")
+    _expect(x_scales, "x_scales", (kb, m), (torch.float32,), dev)
+    _expect(w_scales, "w_scales", (-(-n // 128), kb), (torch.float32,), dev)
+    _no_grad("gptq_fp8_matmul", x_scales, w_scales, bias, Y)
+    if Y is None:
+        Y = torch.empty((m, n), dtype=out_dtype or torch.float32, device=dev)
+    else:
+        _expect(Y, "Y", (m, n), (out_dtype or Y.dtype,), dev)
+    y_code = _elem_code(Y, "Y")
+    if bias is not None:
+        _expect(bias, "bias", (n,), (Y.dtype,), dev)
+    ws, ws_ptr, ws_bytes = _ws_ptr(library().gptq_fp8_matmul_workspace_size(m, n, k), dev, ws)
+    _launch(dev, stream, library().gptq_fp8_matmul,
+            (x_codes.data_ptr(), _pitch(x_codes), x_scales.data_ptr(), _pitch(x_scales), w_codes.data_ptr(),
+             _pitch(w_codes), w_scales.data_ptr(), _pitch(w_scales), m, n, k, _ptr(bias), Y.data_ptr(), y_code,
+             _pitch(Y), ws_ptr, ws_bytes), (x_codes, x_scales, w_codes, w_scales, bias, Y, ws), "gptq_fp8_matmul")
     return Y
 
 
@@ -571,27 +584,27 @@ def gptq_token_logprobs(logits, tokens, top_k: int = 0, logprobs=None, entropy=N
     n, v = logits.shape
     dev = logits.device
     top_k = int(top_k)
-    _expect(tokens, "tokens", (n,), torch.int64, dev)
-    with _device_scope(dev, stream):
-        def out(t, name, shape, dtype):
-            if t is None:
-                return torch.empty(shape, dtype=dtype, device=dev)
-            _expect(t, name, shape, dtype, dev)
-            if not t.is_contiguous():
-                raise ValueError(f"{name} must be contiguous")
-            return t
+    _expect(tokens, "tokens", (n,), (torch.int64,), dev)
+    if not tokens.is_contiguous():
+        raise ValueError("tokens must be contiguous")
 
-        logprobs = out(logprobs, "logprobs", (n,), torch.float32)
-        entropy = out(entropy, "entropy", (n,), torch.float32)
-        top_ids = out(top_ids, "top_ids", (n, max(top_k, 0)), torch.int32)
-        top_logprobs = out(top_logprobs, "top_logprobs", (n, max(top_k, 0)), torch.float32)
-        ws, ws_ptr, ws_bytes = _ws_ptr(gptq_token_logprobs_workspace_size(n, v, top_k), dev, ws)
-        st = library().gptq_token_logprobs(logits.data_ptr(), code, n, v, _pitch(logits), tokens.data_ptr(), top_k,
-                                           logprobs.data_ptr(), entropy.data_ptr(), top_ids.data_ptr(),
-                                           top_logprobs.data_ptr(), ws_ptr, ws_bytes,
-                                           _stream(stream, logits, tokens, logprobs, entropy, top_ids, top_logprobs,
-                                                   ws))
-    _check(st, "gptq_token_logprobs")
+    def out(t, name, shape, dtype):
+        if t is None:
+            return torch.empty(shape, dtype=dtype, device=dev)
+        _expect(t, name, shape, (dtype,), dev)
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return t
+
+    logprobs = out(logprobs, "logprobs", (n,), torch.float32)
+    entropy = out(entropy, "entropy", (n,), torch.float32)
+    top_ids = out(top_ids, "top_ids", (n, max(top_k, 0)), torch.int32)
+    top_logprobs = out(top_logprobs, "top_logprobs", (n, max(top_k, 0)), torch.float32)
+    ws, ws_ptr, ws_bytes = _ws_ptr(library().gptq_token_logprobs_workspace_size(n, v, top_k), dev, ws)
+    _launch(dev, stream, library().gptq_token_logprobs,
+            (logits.data_ptr(), code, n, v, _pitch(logits), tokens.data_ptr(), top_k, logprobs.data_ptr(),
+             entropy.data_ptr(), top_ids.data_ptr(), top_logprobs.data_ptr(), ws_ptr, ws_bytes),
+            (logits, tokens, logprobs, entropy, top_ids, top_logprobs, ws), "gptq_token_logprobs")
     return logprobs, entropy, top_ids, top_logprobs
 
 

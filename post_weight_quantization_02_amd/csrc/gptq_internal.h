@@ -76,7 +76,10 @@ enum { kF32 = 0, kF16 = 1, kBF16 = 2 };
 hipError_t fp8_quantize_launch(const void* X, int x_dtype, int64_t m, int64_t k, int64_t ld_x, int64_t block_rows,
                                uint8_t* codes, int64_t ld_codes, float* scales, int64_t ld_scales, hipStream_t s);
 
+enum { kFp8Few, kFp8Medium, kFp8Large };
 struct Fp8Plan {
+  int kind;
+  int splits;             // parts of k, summed by a second launch when more than one
   size_t ws_bytes;
 };
 Fp8Plan fp8_plan(int64_t m, int64_t n, int64_t k);

@@ -128,6 +128,19 @@ def test_matmul_parity(m, n, k, out, biased):
     check(y, out, xc, sx, wc, sw, bias)
 
 
+@pytest.mark.parametrize("m,n,k,out", [(300, 24581, 200, "f16"), (260, 24580, 257, "f32"), (1025, 10001, 128, "bf16"),
+                                       (513, 16500, 384, "f32")])
+def test_matmul_parity_large(m, n, k, out):
+    """Enough outputs for the largest tiles, with ragged edges on every side."""
+    xc, sx, wc, sw = operands(m, n, k, k)
+    if out == "f16":
+        sx = sx * 1e-3
+    bias = torch.randn(n, device="cuda").to(TYPES[out])
+    y = G.gptq_fp8_matmul(xc, sx, wc, sw, bias, out_dtype=TYPES[out])
+    torch.cuda.synchronize()
+    check(y, out, xc, sx, wc, sw, bias)
+
+
 @pytest.mark.parametrize("m,n,k,pitch", [(1, 130, 200, 201), (20, 33, 129, 129), (70, 140, 300, 303), (300, 260, 1000, 1001),
                                          (130, 130, 257, 264)])
 def test_matmul_pitches_and_strided_outputs(m, n, k, pitch):
