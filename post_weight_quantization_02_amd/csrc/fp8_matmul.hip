@@ -26,11 +26,18 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
 typedef __bf16 bf16;
+typedef const __attribute__((address_space(4))) float uniform_float;   // read by scalar loads
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 
-// 16 codes of a row from column c; columns from k on read as zero
+// 16 codes of a row from column c; columns from k on read as zero.  The row's last
+// chunk is taken from its last 16 bytes and shifted.
 __device__ __forceinline__ u32x4 load_chunk(const uint8_t* __restrict__ row, int64_t c, int64_t k) {
   if (c + 16 <= k) return *(const u32x4_any*)(row + c);
+  if (c >= k) return u32x4{0u, 0u, 0u, 0u};
+  if (k >= 16) {
+    const auto v = __builtin_bit_cast(unsigned __int128, (u32x4)(*(const u32x4_any*)(row + k - 16)));
+    return __builtin_bit_cast(u32x4, v >> (8 * (int)(c + 16 - k)));
+  }
   u32x4 v = {0u, 0u, 0u, 0u};
 #pragma unroll
   for (int e = 0; e < 16; ++e)
@@ -96,111 +103,79 @@ __device__ __forceinline__ int64_t xcd_remap(int64_t bid, int64_t total) {
 template <typename T>
 __device__ __forceinline__ void store4(T* __restrict__ Y, int64_t ld_y, const T* __restrict__ bias, int64_t i, int64_t j,
                                        int64_t m, int64_t n, f32x4 v) {
-  if (i >= m) return;
+  typedef T T4 __attribute__((ext_vector_type(4), aligned(2)));     // at any element
+  if (i >= m || j >= n) return;
+  T* y = Y + i * ld_y + j;
+  if (j + 4 <= n) {
+    if (bias) {
+      const T4 b = *(const T4*)(bias + j);
 #pragma unroll
-  for (int r = 0; r < 4; ++r)
-    if (j + r < n) Y[i * ld_y + j + r] = (T)(v[r] + (bias ? (float)bias[j + r] : 0.f));
+      for (int r = 0; r < 4; ++r) v[r] += (float)b[r];
+    }
+    *(T4*)y = T4{(T)v[0], (T)v[1], (T)v[2], (T)v[3]};
+  } else {
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (j + r < n) y[r] = (T)(v[r] + (bias ? (float)bias[j + r] : 0.f));
+  }
+}
+
+// A wave's 16 rows x 64 outputs of four neighbouring tiles: v[a] holds outputs 16 a +
+// 4 q .. + 3 of the lane's row.  For 16-bit types the four lanes of a row swap parts
+// (registers only), so that each holds 16 outputs in a row and stores 32 bytes.
+template <typename T>
+__device__ __forceinline__ void store_row64(T* __restrict__ Y, int64_t ld_y, const T* __restrict__ bias, int64_t i, int64_t j0,
+                                            int q, int64_t m, int64_t n, const f32x4 (&v)[4]) {
+  if constexpr (sizeof(T) == 2) {
+    typedef T T4 __attribute__((ext_vector_type(4)));
+    typedef T T4_any __attribute__((ext_vector_type(4), aligned(2)));
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    typedef uint32_t u32x4_at2 __attribute__((ext_vector_type(4), aligned(2)));
+    if (j0 + 64 <= n) {         // the same for the whole wave
+      uint32_t u[4][2];
+#pragma unroll
+      for (int a = 0; a < 4; ++a) {
+        f32x4 f = v[a];
+        if (bias) {
+          const T4_any b = *(const T4_any*)(bias + j0 + 16 * a + 4 * q);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) f[r] += (float)b[r];
+        }
+        const u32x2 w = __builtin_bit_cast(u32x2, T4{(T)f[0], (T)f[1], (T)f[2], (T)f[3]});
+        u[a][0] = w[0];
+        u[a][1] = w[1];
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+          const auto r = __builtin_amdgcn_permlane32_swap(u[a][h], u[a + 2][h], false, false);
+          u[a][h] = r[0];
+          u[a + 2][h] = r[1];
+        }
+#pragma unroll
+        for (int a = 0; a < 4; a += 2) {
+          const auto r = __builtin_amdgcn_permlane16_swap(u[a][h], u[a + 1][h], false, false);
+          u[a][h] = r[0];
+          u[a + 1][h] = r[1];
+        }
+      }
+      if (i < m) {
+        T* y = Y + i * ld_y + j0 + 16 * q;
+        *(u32x4_at2*)y = u32x4_at2{u[0][0], u[0][1], u[1][0], u[1][1]};
+        *(u32x4_at2*)(y + 8) = u32x4_at2{u[2][0], u[2][1], u[3][0], u[3][1]};
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int a = 0; a < 4; ++a) store4<T>(Y, ld_y, bias, i, j0 + 16 * a + 4 * q, m, n, v[a]);
 }
 
 // sum v (+ bias) over the parts of a split product or the waves of a work-group is
 // always taken in the same order, so results do not depend on timing.
 
-// ---------------------------------------------------------------- few rows
-// At most 16 TT rows of X: W is streamed once, straight into registers.  A work-group
-// takes 16 rows of W, its 8 waves every eighth block of 128 columns (4 blocks' loads in
-// flight each), and the waves' sums meet in LDS.  X comes from L2.  HBM-bound on W, so
-// the exact (widened) block sums cost nothing.
-constexpr int kFewWaves = 8, kFewUnroll = 4;
-
-template <typename T, int TT>
-__global__ __launch_bounds__(64 * kFewWaves) void fp8_few_kernel(Fp8Args p) {
-  __shared__ f32x4 part[kFewWaves][TT][64];
-  const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
-  const int lr = lane & 15, q = lane >> 4;
-  const int64_t j0 = (int64_t)blockIdx.x * 16;
-  const uint8_t* wr = p.W + min<int64_t>(j0 + lr, p.n - 1) * p.ld_w;
-  const float* sw = p.sw + (j0 / kBlk) * p.ld_sw;
-  const uint8_t* xr[TT];
-  const float* sx[TT];
-#pragma unroll
-  for (int c = 0; c < TT; ++c) {
-    const int64_t i = min<int64_t>(16 * c + lr, p.m - 1);
-    xr[c] = p.X + i * p.ld_x;
-    sx[c] = p.sx + i;
-  }
-  f32x4 acc[TT];
-#pragma unroll
-  for (int c = 0; c < TT; ++c) acc[c] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const auto add = [&](i32x8 wv, const i32x8 (&xv)[TT], const float (&sc)[TT], float s) {
-    const Frag<true> wf(wv);
-#pragma unroll
-    for (int c = 0; c < TT; ++c) {
-      const f32x4 d = block_product(wf, Frag<true>(xv[c]));
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[c][e] = fmaf(d[e], s * sc[c], acc[c][e]);
-    }
-  };
-  const auto whole = [&](const uint8_t* r, int64_t b) {
-    const uint8_t* a = r + b * kBlk + 16 * q;
-    return join(*(const u32x4_any*)a, *(const u32x4_any*)(a + 64));
-  };
-  const int64_t full = p.k / kBlk;
-  int64_t b = w;
-  for (; b + kFewWaves * (kFewUnroll - 1) < full; b += kFewWaves * kFewUnroll) {
-    i32x8 wv[kFewUnroll], xv[kFewUnroll][TT];
-    float sc[kFewUnroll][TT], s[kFewUnroll];
-#pragma unroll
-    for (int u = 0; u < kFewUnroll; ++u) {
-      const int64_t at = b + kFewWaves * u;
-      wv[u] = whole(wr, at);
-      s[u] = sw[at];
-#pragma unroll
-      for (int c = 0; c < TT; ++c) {
-        xv[u][c] = whole(xr[c], at);
-        sc[u][c] = sx[c][at * p.ld_sx];
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kFewUnroll; ++u) add(wv[u], xv[u], sc[u], s[u]);
-  }
-  for (; b * kBlk < p.k; b += kFewWaves) {      // what is left, the last block guarded
-    i32x8 xv[TT];
-    float sc[TT];
-    const auto any = [&](const uint8_t* r) {
-      return b < full ? whole(r, b)
-                      : join(load_chunk(r, b * kBlk + 16 * q, p.k), load_chunk(r, b * kBlk + 64 + 16 * q, p.k));
-    };
-    const i32x8 wv = any(wr);
-#pragma unroll
-    for (int c = 0; c < TT; ++c) {
-      xv[c] = any(xr[c]);
-      sc[c] = sx[c][b * p.ld_sx];
-    }
-    add(wv, xv, sc, sw[b]);
-  }
-#pragma unroll
-  for (int c = 0; c < TT; ++c) part[w][c][lane] = acc[c];
-  __syncthreads();
-  if (w < TT) {
-    f32x4 v = part[0][w][lane];
-#pragma unroll
-    for (int i = 1; i < kFewWaves; ++i) v += part[i][w][lane];
-    store4<T>((T*)p.Y, p.ld_y, (const T*)p.bias, 16 * w + lr, j0 + 4 * q, p.m, p.n, v);
-  }
-}
-
-// ---------------------------------------------------------------- tiles by LDS
-// BT rows of X by BN rows of W per work-group, WT x WN waves.  Each block of 128
-// columns goes to LDS without passing through registers (16-byte direct loads, a wave's
-// load filling 8 rows of 128 bytes), one block ahead of the products, in two buffers
-// that are variables of their own so that reading one does not wait for the other's loads.
-// Row r keeps its 16-byte chunk c at place c ^ (r & 7): the 16 rows that a fragment
-// load takes at one chunk then spread over all banks.  The rows' scales travel with the
-// block; the tile of W has one scale, fetched a block ahead.  A last block of fewer than
-// 128 columns is taken first, through registers, with zeros behind column k.  Scaling
-// lags one row of tiles behind the matrix instructions, so it runs beside them.
 typedef __attribute__((address_space(3))) void lds_void;
-typedef const __attribute__((address_space(4))) float uniform_float;
 
 // `bytes` bytes from a wave-uniform address
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* base, int64_t bytes) {
@@ -211,6 +186,13 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* base, int64_t
                                            0x00020000);
 }
 
+template <int I, int N, typename F>
+__device__ __forceinline__ void static_for(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    static_for<I + 1, N>(f);
+  }
+}
 // 16 bytes per lane from r + voffset + soffset to LDS at `to` + 16 * lane
 __device__ __forceinline__ void load16_to_lds(__amdgpu_buffer_rsrc_t r, uint8_t* to, uint32_t voffset, int soffset) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)to, 16, voffset, soffset, 0, 0);
@@ -219,23 +201,169 @@ __device__ __forceinline__ void load4_to_lds(__amdgpu_buffer_rsrc_t r, float* to
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)to, 4, voffset, 0, 0, 0);
 }
 
-template <int BT, int BN>
-struct __attribute__((aligned(16))) Stage {
+// ---------------------------------------------------------------- few rows
+// At most 16 TT rows of X.  A work-group takes 16 rows of W, its waves every fourth
+// block of 128 columns, and the waves' sums meet in LDS at the end.  Each wave streams
+// its blocks of W, and the rows of X and their scales with them, through a ring of R
+// LDS slots of its own, filled by direct loads R - 1 blocks ahead: no barriers, and
+// nothing in flight holds registers.  HBM-bound on W, so the exact (widened) block sums
+// cost nothing.  A last block of fewer than 128 columns goes through registers.
+constexpr int kFewWaves = 4;
+
+template <int TT>
+struct __attribute__((aligned(16))) Slot {
+  uint8_t w[16 * kBlk];
+  uint8_t x[16 * TT * kBlk];
+  float sx[64];
+};
+template <int TT, int I>
+__device__ __forceinline__ Slot<TT> (&slots())[kFewWaves] {
+  __shared__ Slot<TT> s[kFewWaves];
+  return s;
+}
+
+template <typename T, int TT, int R, bool DMA>
+__global__ __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_per_eu(2))) void fp8_few_kernel(Fp8Args p) {
+  __shared__ f32x4 part[kFewWaves][TT][64];
+  const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int lr = lane & 15, q = lane >> 4;
+  const int64_t j0 = (int64_t)blockIdx.x * 16;
+  uniform_float* sw = (uniform_float*)(uintptr_t)p.sw + (j0 / kBlk) * p.ld_sw;
+  const int rows_w = (int)min<int64_t>(16, p.n - j0), rows_x = (int)p.m;
+  const int full = (int)(p.k / kBlk), nblk = (int)((p.k + kBlk - 1) / kBlk);
+  f32x4 acc[TT];
+#pragma unroll
+  for (int c = 0; c < TT; ++c) acc[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+  // blocks through registers: the last one, or all of them where rows may start anywhere
+  const auto by_registers = [&](int b) {
+    const auto both = [&](const uint8_t* r) {
+      return join(load_chunk(r, (int64_t)b * kBlk + 16 * q, p.k), load_chunk(r, (int64_t)b * kBlk + 64 + 16 * q, p.k));
+    };
+    const i32x8 wv = both(p.W + (j0 + min(lr, rows_w - 1)) * p.ld_w);
+    i32x8 xv[TT];
+    float sc[TT];
+#pragma unroll
+    for (int c = 0; c < TT; ++c) {
+      const int64_t i = min(16 * c + lr, rows_x - 1);
+      xv[c] = both(p.X + i * p.ld_x);
+      sc[c] = p.sx[(int64_t)b * p.ld_sx + i];
+    }
+#pragma unroll
+    for (int c = 0; c < TT; ++c) scale_add(acc[c], block_product(Frag<true>(wv), Frag<true>(xv[c])), sc[c] * sw[b]);
+  };
+  if constexpr (!DMA) {
+    for (int b = w; b < nblk; b += kFewWaves) by_registers(b);
+  } else {
+    const int mine = full > w ? (full - w + kFewWaves - 1) / kFewWaves : 0;      // whole blocks w, w + 4, ...
+    const __amdgpu_buffer_rsrc_t wb = rsrc(p.W + j0 * p.ld_w, (rows_w - 1) * p.ld_w + p.k);
+    const __amdgpu_buffer_rsrc_t xb = rsrc(p.X, (rows_x - 1) * p.ld_x + p.k);
+    const int ch = ((lane & 7) ^ (lane >> 3)) * 16;
+    uint32_t wo[2], xo[2 * TT];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) wo[j] = (uint32_t)(min(8 * j + (lane >> 3), rows_w - 1) * p.ld_w) + ch;
+#pragma unroll
+    for (int j = 0; j < 2 * TT; ++j) xo[j] = (uint32_t)(min(8 * j + (lane >> 3), rows_x - 1) * p.ld_x) + ch;
+    const uint32_t so = 4u * (uint32_t)min(lane, rows_x - 1);
+    const auto block_of = [&](int i) { return i < mine ? w + kFewWaves * i : 0; };
+    const auto fetch = [&](Slot<TT>& s, int b) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) load16_to_lds(wb, s.w + 8 * j * kBlk, wo[j], b * kBlk);
+#pragma unroll
+      for (int j = 0; j < 2 * TT; ++j) load16_to_lds(xb, s.x + 8 * j * kBlk, xo[j], b * kBlk);
+      load4_to_lds(rsrc(p.sx + (int64_t)b * p.ld_sx, 4 * rows_x), s.sx, so);
+    };
+    constexpr int kLoads = 3 + 2 * TT;
+    static_assert((R - 1) * kLoads < 64, "counted by vmcnt");
+    const uint32_t a0 = (uint32_t)(lr * kBlk + ((q ^ (lr & 7)) * 16)), a1 = a0 ^ 64;
+    const auto use = [&](const Slot<TT>& s, float scale) {
+      const Frag<true> wf(join(*(const u32x4*)(s.w + a0), *(const u32x4*)(s.w + a1)));
+#pragma unroll
+      for (int c = 0; c < TT; ++c) {
+        const Frag<true> xf(join(*(const u32x4*)(s.x + 16 * c * kBlk + a0), *(const u32x4*)(s.x + 16 * c * kBlk + a1)));
+        scale_add(acc[c], block_product(wf, xf), s.sx[16 * c + lr] * scale);
+      }
+    };
+    if (mine > 0) {
+      float sw_next = sw[w];
+      static_for<0, R - 1>([&](auto i) { fetch(slots<TT, i.value>()[w], block_of(i.value)); });
+      int i = 0;
+      const auto one = [&](auto h) {
+        // the reads of the slot that is refilled next are done; so is this slot's block once it alone is left out
+        const float scale = sw_next;
+        sw_next = sw[block_of(i + 1)];
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        fetch(slots<TT, (h.value + R - 1) % R>()[w], block_of(i + R - 1));
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((R - 1) * kLoads) : "memory");
+        use(slots<TT, h.value>()[w], scale);
+        ++i;
+      };
+      while (i + R <= mine) static_for<0, R>(one);
+      static_for<0, R - 1>([&](auto h) {
+        if (i < mine) one(h);
+      });
+    }
+    if (full < nblk && full % kFewWaves == w) by_registers(full);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // unused fetches write LDS: not after this work-group's end
+  }
+#pragma unroll
+  for (int c = 0; c < TT; ++c) part[w][c][lane] = acc[c];
+  __syncthreads();
+  if (w < TT) {         // TT <= 4 waves
+    f32x4 v = part[0][w][lane];
+#pragma unroll
+    for (int i = 1; i < kFewWaves; ++i) v += part[i][w][lane];
+    store4<T>((T*)p.Y, p.ld_y, (const T*)p.bias, 16 * w + lr, j0 + 4 * q, p.m, p.n, v);
+  }
+}
+
+// ---------------------------------------------------------------- tiles by LDS
+// BT rows of X by BN rows of W per work-group, WT x WN waves.  Each block of 128
+// columns goes to LDS without passing through registers (16-byte direct loads, a wave's
+// load filling 8 rows of 128 bytes), S - 1 blocks ahead of the products, in S buffers
+// that are variables of their own so that reading one does not wait for the others' loads.
+// Row r keeps its 16-byte chunk c at place c ^ (r & 7): the 16 rows that a fragment
+// load takes at one chunk then spread over all banks.  The rows' scales travel with the
+// block; the tile of W has one scale, fetched a block ahead.  A last block of fewer than
+// 128 columns is taken first, through registers, with zeros behind column k.  Scaling
+// lags one row of tiles behind the matrix instructions, so it runs beside them.
+// stage I of a kernel's buffers, variables of their own
+template <int BT>
+struct __attribute__((aligned(16))) StageX {
   uint8_t x[BT * kBlk];
-  uint8_t w[BN * kBlk];
   float sx[BT + 64];      // each wave's load of the rows' scales writes 64 of them, the next wave's first ones too
 };
+template <int BT, int I>
+__device__ __forceinline__ StageX<BT>& stage_x() {
+  __shared__ StageX<BT> s;
+  return s;
+}
+template <int BN>
+struct __attribute__((aligned(16))) StageW {
+  uint8_t w[BN * kBlk];
+};
+template <int BN, int I>
+__device__ __forceinline__ StageW<BN>& stage_w() {
+  __shared__ StageW<BN> s;
+  return s;
+}
 
-template <typename T, bool WIDE, int BT, int BN, int WT, int WN, bool SPLIT>
-__global__ __launch_bounds__(64 * WT * WN) void fp8_dma_kernel(Fp8Args p, int tiles_t, int tiles_n, int blocks_per_split,
+// how a work-group keeps its buffers full
+enum Flow {
+  kBlocks,      // S buffers; one barrier per block
+  kAhead,       // S buffers; a block's codes are read into registers while the one before is multiplied
+  kCarry        // 2 buffers; the next block's first codes are read beside this one's last products
+};
+
+template <typename T, bool WIDE, int BT, int BN, int WT, int WN, int S, Flow FLOW, bool SPLIT>
+__global__ __launch_bounds__(64 * WT * WN) __attribute__((amdgpu_waves_per_eu(2))) void fp8_dma_kernel(Fp8Args p, int tiles_t, int tiles_n, int blocks_per_split,
                                                                float* __restrict__ parts) {
   constexpr int kWavesHere = WT * WN, TT = BT / WT / 16, TN = BN / WN / 16;
   constexpr int kXLoads = BT / 8 / kWavesHere, kWLoads = BN / 8 / kWavesHere;
   static_assert(kXLoads * 8 * kWavesHere == BT && kWLoads * 8 * kWavesHere == BN, "loads divide over the waves");
   static_assert(BN / WN <= kBlk && kBlk % (BN / WN) == 0, "one W scale per wave");
   constexpr int kScaleRows = BT / kWavesHere;
-  __shared__ Stage<BT, BN> s0;
-  __shared__ Stage<BT, BN> s1;
+  constexpr int kLoads = kXLoads + kWLoads + 1;        // of a wave, per block
+  static_assert((S - 2) * kLoads < 64, "counted by vmcnt");
   const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
   const int lr = lane & 15, q = lane >> 4;
   // work-groups of one XCD take neighbouring tiles: bands of 8 tiles along X, W outermost
@@ -262,14 +390,19 @@ __global__ __launch_bounds__(64 * WT * WN) void fp8_dma_kernel(Fp8Args p, int ti
     wo[j] = (uint32_t)(min((w * kWLoads + j) * 8 + (lane >> 3), rows_w - 1) * p.ld_w) + ch;
   const uint32_t so = 4u * (uint32_t)min(w * kScaleRows + lane, rows_x - 1);
   uniform_float* swp = (uniform_float*)(uintptr_t)p.sw + ((j0 + wj) / kBlk < (p.n + kBlk - 1) / kBlk ? (j0 + wj) / kBlk : 0) * p.ld_sw;
-  const auto fetch = [&](Stage<BT, BN>& s, int b) {
+  // the rows' scales are X's last load
+  const auto fetch_x = [&](StageX<BT>& s, int b, int l) {
+    if (l < kXLoads) load16_to_lds(xb, s.x + (w * kXLoads + l) * 8 * kBlk, xo[l], b * kBlk);
+    else load4_to_lds(rsrc(p.sx + (int64_t)b * p.ld_sx + i0, 4 * rows_x), s.sx + w * kScaleRows, so);
+  };
+  const auto fetch_w = [&](StageW<BN>& s, int b, int l) {
+    load16_to_lds(wb, s.w + (w * kWLoads + l) * 8 * kBlk, wo[l], b * kBlk);
+  };
+  const auto fetch = [&](auto i, int b) {
 #pragma unroll
-    for (int j = 0; j < kXLoads; ++j)
-      load16_to_lds(xb, s.x + (w * kXLoads + j) * 8 * kBlk, xo[j], b * kBlk);
+    for (int l = 0; l <= kXLoads; ++l) fetch_x(stage_x<BT, i.value>(), b, l);
 #pragma unroll
-    for (int j = 0; j < kWLoads; ++j)
-      load16_to_lds(wb, s.w + (w * kWLoads + j) * 8 * kBlk, wo[j], b * kBlk);
-    load4_to_lds(rsrc(p.sx + (int64_t)b * p.ld_sx + i0, 4 * rows_x), s.sx + w * kScaleRows, so);
+    for (int l = 0; l < kWLoads; ++l) fetch_w(stage_w<BN, i.value>(), b, l);
   };
   f32x4 acc[TT][TN];
 #pragma unroll
@@ -280,23 +413,29 @@ __global__ __launch_bounds__(64 * WT * WN) void fp8_dma_kernel(Fp8Args p, int ti
   const uint32_t x0 = (uint32_t)((wi + lr) * kBlk + ((q ^ (lr & 7)) * 16)), x1 = x0 ^ 64;
   const uint32_t w0 = (uint32_t)((wj + lr) * kBlk + ((q ^ (lr & 7)) * 16)), w1 = w0 ^ 64;
   const uint32_t sx0 = (uint32_t)(wi + lr);
-  const auto multiply = [&](const Stage<BT, BN>& s, float sw) {
-    const auto frag = [&](const uint8_t* rows, uint32_t a, uint32_t b, int tile) {
-      return Frag<WIDE>(join(*(const u32x4*)(rows + a + tile * 16 * kBlk), *(const u32x4*)(rows + b + tile * 16 * kBlk)));
-    };
+  const auto pick = [&](const uint8_t* rows, uint32_t a, uint32_t b, int tile) {
+    return join(*(const u32x4*)(rows + a + tile * 16 * kBlk), *(const u32x4*)(rows + b + tile * 16 * kBlk));
+  };
+  // acc += scale * (W tiles * X tiles): x(c) and sx(c) give tile c of X and its rows' scales,
+  // asked for one tile ahead; meanwhile(c) issues loads while tile c is multiplied (issued
+  // together they would hold the wave up before its first product)
+  const auto multiply = [&](const i32x8 (&wv)[TN], auto&& x, auto&& sx, float sw, auto&& meanwhile) {
     Frag<WIDE> wf[TN];
 #pragma unroll
-    for (int a = 0; a < TN; ++a) wf[a] = frag(s.w, w0, w1, a);
-    Frag<WIDE> xf = frag(s.x, x0, x1, 0), xn;
-    float sc = sw * s.sx[sx0], sc_last = 0.f;
+    for (int a = 0; a < TN; ++a) wf[a] = Frag<WIDE>(wv[a]);
+    i32x8 xv = x(0);
+    // a row scale is read two tiles before its use: multiplied by sw where it was read, it
+    // would hold the products up for an LDS read each tile
+    float sc = sx(0), sc_last = 0.f;
     f32x4 last[TN];
 #pragma unroll
     for (int c = 0; c < TT; ++c) {
       f32x4 d[TN];
       float sn = 0.f;
+      const Frag<WIDE> xf(xv);
       if (c + 1 < TT) {
-        xn = frag(s.x, x0, x1, c + 1);
-        sn = sw * s.sx[sx0 + 16 * (c + 1)];
+        xv = x(c + 1);
+        sn = sx(c + 1);
       }
 #pragma unroll
       for (int a = 0; a < TN; ++a) {
@@ -304,57 +443,163 @@ __global__ __launch_bounds__(64 * WT * WN) void fp8_dma_kernel(Fp8Args p, int ti
         if (c > 0) scale_add(acc[c - 1][a], last[a], sc_last);
         __builtin_amdgcn_sched_barrier(0);
       }
+      meanwhile(c);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int a = 0; a < TN; ++a) last[a] = d[a];
-      sc_last = sc;
-      xf = xn;
+      sc_last = sw * sc;
       sc = sn;
     }
 #pragma unroll
     for (int a = 0; a < TN; ++a) scale_add(acc[TT - 1][a], last[a], sc_last);
   };
   // a block of fewer than 128 columns, through registers
-  const auto fetch_tail = [&](Stage<BT, BN>& s, int b) {
+  const auto fetch_tail = [&](int b) {
+    StageX<BT>& sx = stage_x<BT, 0>();
     for (int id = t; id < (BT + BN) * 8; id += 64 * kWavesHere) {
       const bool is_x = id < BT * 8;
       const int r = is_x ? id >> 3 : (id >> 3) - BT, c = id & 7;
       const uint8_t* row = is_x ? p.X + (i0 + min(r, rows_x - 1)) * p.ld_x : p.W + (j0 + min(r, rows_w - 1)) * p.ld_w;
-      *(u32x4*)((is_x ? s.x : s.w) + r * kBlk + ((c ^ (r & 7)) * 16)) = load_chunk(row, (int64_t)b * kBlk + 16 * c, p.k);
+      const u32x4 v = load_chunk(row, (int64_t)b * kBlk + 16 * c, p.k);
+      const int at = r * kBlk + ((c ^ (r & 7)) * 16);
+      if (is_x) *(u32x4*)(sx.x + at) = v;
+      else *(u32x4*)(stage_w<BN, 0>().w + at) = v;
     }
-    if (t < BT) s.sx[t] = p.sx[(int64_t)b * p.ld_sx + i0 + min(t, rows_x - 1)];
+    if (t < BT) sx.sx[t] = p.sx[(int64_t)b * p.ld_sx + i0 + min(t, rows_x - 1)];
   };
   const bool tail = b1 == nblk && (p.k % kBlk) != 0;
   const int steps = b1 - b0;
   const auto block_of = [&](int step) { return !tail ? b0 + step : step == 0 ? nblk - 1 : b0 + step - 1; };
-  float sw_next = swp[block_of(0)];
-  if (tail) fetch_tail(s0, nblk - 1);
-  else fetch(s0, b0);
-  for (int step = 0; step < steps; step += 2) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (h == 1 && step + 1 >= steps) break;
-      Stage<BT, BN>& here = h ? s1 : s0;
-      Stage<BT, BN>& there = h ? s0 : s1;
+  // behind the last block, block 0, which is not used: with a fetch on every path the
+  // counts of outstanding loads are known, and no read waits for a later block
+  const auto next = [&](int step) { return step < steps ? block_of(step) : 0; };
+  float sw_next = swp[next(0)];
+  if (tail) fetch_tail(nblk - 1);
+  else fetch(std::integral_constant<int, 0>{}, b0);
+  int step = 0;
+  const auto run = [&](auto&& one) {
+    while (step + S <= steps) static_for<0, S>(one);
+    static_for<0, S - 1>([&](auto i) {
+      if (step < steps) one(i);
+    });
+  };
+  if constexpr (FLOW == kBlocks) {
+    static_for<1, S - 1>([&](auto i) { fetch(i, next(i.value)); });
+    run([&](auto i) {
+      constexpr int h = i.value, to = (h + S - 1) % S;
+      const StageX<BT>& s = stage_x<BT, h>();
       // this block has arrived, and every wave is done with the buffer that is filled next
-      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S - 2) * kLoads) : "memory");
       const float sw = sw_next;
-      // after the last block, a block that is not used: a fetch on every path lets the
-      // reads of `here` wait for nothing of `there`
-      const int b = step + h + 1 < steps ? block_of(step + h + 1) : 0;
-      sw_next = swp[b];
-      fetch(there, b);
-      multiply(here, sw);
+      sw_next = swp[next(step + 1)];
+      fetch(std::integral_constant<int, to>{}, next(step + S - 1));
+      i32x8 wv[TN];
+#pragma unroll
+      for (int a = 0; a < TN; ++a) wv[a] = pick(stage_w<BN, h>().w, w0, w1, a);
+      multiply(wv, [&](int c) { return pick(s.x, x0, x1, c); }, [&](int c) { return s.sx[sx0 + 16 * c]; }, sw,
+               [](int) {});
+      ++step;
+    });
+  } else if constexpr (FLOW == kCarry) {
+    static_assert(S == 2 && TT >= 2, "two buffers");
+    fetch(std::integral_constant<int, 1>{}, next(1));
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLoads) : "memory");
+    Frag<WIDE> wf[TN], xf;
+    float sc, sc_last = 0.f, sw = sw_next;      // sc: a row scale as read, multiplied by sw only when it is used
+#pragma unroll
+    for (int a = 0; a < TN; ++a) wf[a] = Frag<WIDE>(pick(stage_w<BN, 0>().w, w0, w1, a));
+    xf = Frag<WIDE>(pick(stage_x<BT, 0>().x, x0, x1, 0));
+    sc = stage_x<BT, 0>().sx[sx0];
+    run([&](auto i) {
+      constexpr int h = i.value, to = h ^ 1;
+      sw_next = swp[next(step + 1)];
+      f32x4 last[TN];
+#pragma unroll
+      for (int c = 0; c < TT; ++c) {
+        f32x4 d[TN];
+        i32x8 xn;
+        float sn;
+        if (c + 1 < TT) {
+          xn = pick(stage_x<BT, h>().x, x0, x1, c + 1);
+          sn = stage_x<BT, h>().sx[sx0 + 16 * (c + 1)];
+        } else {
+          // the next block has arrived, and every wave has read all of this one
+          asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+          xn = pick(stage_x<BT, to>().x, x0, x1, 0);
+          sn = stage_x<BT, to>().sx[sx0];
+        }
+#pragma unroll
+        for (int a = 0; a < TN; ++a) {
+          d[a] = block_product(wf[a], xf);
+          if (c + 1 == TT) wf[a] = Frag<WIDE>(pick(stage_w<BN, to>().w, w0, w1, a));
+          if (c > 0) scale_add(acc[c - 1][a], last[a], sc_last);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        if (c + 1 == TT) fetch(i, next(step + 2));
+#pragma unroll
+        for (int a = 0; a < TN; ++a) last[a] = d[a];
+        sc_last = sw * sc;
+        sc = sn;
+        xf = Frag<WIDE>(xn);
+      }
+#pragma unroll
+      for (int a = 0; a < TN; ++a) scale_add(acc[TT - 1][a], last[a], sc_last);
+      sw = sw_next;
+      ++step;
+    });
+  } else {
+    static_assert(S % 2 == 0, "two sets of registers in turn");
+    static_for<1, S>([&](auto i) { fetch(i, next(i.value)); });
+    i32x8 wv[2][TN], xv[2][TT];
+    float sxv[2][TT];
+    constexpr int kReads = TN + TT;
+    const auto read_one = [&](int set, const StageX<BT>& x, const StageW<BN>& w, int l) {
+      if (l < TN) wv[set][l] = pick(w.w, w0, w1, l);
+      else {
+        xv[set][l - TN] = pick(x.x, x0, x1, l - TN);
+        sxv[set][l - TN] = x.sx[sx0 + 16 * (l - TN)];
+      }
+    };
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S - 1) * kLoads) : "memory");
+#pragma unroll
+    for (int l = 0; l < kReads; ++l) read_one(0, stage_x<BT, 0>(), stage_w<BN, 0>(), l);
+    run([&](auto i) {
+      constexpr int h = i.value, set = h & 1, nx = (h + 1) % S;
+      // the next block has arrived, and every wave has read this one
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S - 2) * kLoads) : "memory");
+      const float sw = sw_next;
+      sw_next = swp[next(step + 1)];
+      const int b = next(step + S);
+      multiply(wv[set], [&](int c) { return xv[set][c]; }, [&](int c) { return sxv[set][c]; }, sw, [&](int c) {
+#pragma unroll
+        for (int l = 0; l < kReads; ++l)
+          if (l * TT / kReads == c) read_one(set ^ 1, stage_x<BT, nx>(), stage_w<BN, nx>(), l);
+#pragma unroll
+        for (int l = 0; l < kLoads; ++l)
+          if (l * TT / kLoads == c) {
+            if (l <= kXLoads) fetch_x(stage_x<BT, h>(), b, l);
+            else fetch_w(stage_w<BN, h>(), b, l - kXLoads - 1);
+          }
+      });
+      ++step;
+    });
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // unused fetches write LDS: not after this work-group's end
+#pragma unroll
+  for (int c = 0; c < TT; ++c) {
+    const int64_t i = i0 + wi + 16 * c + lr, j = j0 + wj;
+    float* part_y = parts + (int64_t)part * p.m * p.n;
+    if constexpr (TN == 4) {
+      if constexpr (SPLIT) store_row64<float>(part_y, p.n, nullptr, i, j, q, p.m, p.n, acc[c]);
+      else store_row64<T>((T*)p.Y, p.ld_y, (const T*)p.bias, i, j, q, p.m, p.n, acc[c]);
+    } else {
+#pragma unroll
+      for (int a = 0; a < TN; ++a) {
+        if constexpr (SPLIT) store4<float>(part_y, p.n, nullptr, i, j + 16 * a + 4 * q, p.m, p.n, acc[c][a]);
+        else store4<T>((T*)p.Y, p.ld_y, (const T*)p.bias, i, j + 16 * a + 4 * q, p.m, p.n, acc[c][a]);
+      }
     }
   }
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the unused fetch writes LDS: not after this work-group's end
-#pragma unroll
-  for (int c = 0; c < TT; ++c)
-#pragma unroll
-    for (int a = 0; a < TN; ++a) {
-      const int64_t i = i0 + wi + 16 * c + lr, j = j0 + wj + 16 * a + 4 * q;
-      if constexpr (SPLIT) store4<float>(parts + (int64_t)part * p.m * p.n, p.n, nullptr, i, j, p.m, p.n, acc[c][a]);
-      else store4<T>((T*)p.Y, p.ld_y, (const T*)p.bias, i, j, p.m, p.n, acc[c][a]);
-    }
 }
 
 // Y from the parts of a product split over k
@@ -429,14 +674,14 @@ __global__ __launch_bounds__(256) void fp8_tile_kernel(const uint8_t* __restrict
       store4<T>(Y, ld_y, bias, i0 + wi + 16 * c + lr, j0 + wj + 16 * a + 4 * q, m, n, acc[c][a]);
 }
 
-template <typename T, bool WIDE, int BT, int BN, int WT, int WN>
+template <typename T, bool WIDE, int BT, int BN, int WT, int WN, int S, Flow FLOW>
 hipError_t launch_dma(const Fp8Plan& plan, const Fp8Args& p, float* ws, hipStream_t s) {
   const int tt = (int)cdiv(p.m, BT), tn = (int)cdiv(p.n, BN);
   const int per = (int)cdiv(cdiv(p.k, kBlk), plan.splits);
   if (plan.splits == 1) {
-    fp8_dma_kernel<T, WIDE, BT, BN, WT, WN, false><<<tt * tn, 64 * WT * WN, 0, s>>>(p, tt, tn, per, nullptr);
+    fp8_dma_kernel<T, WIDE, BT, BN, WT, WN, S, FLOW, false><<<tt * tn, 64 * WT * WN, 0, s>>>(p, tt, tn, per, nullptr);
   } else {
-    fp8_dma_kernel<T, WIDE, BT, BN, WT, WN, true><<<tt * tn * plan.splits, 64 * WT * WN, 0, s>>>(p, tt, tn, per, ws);
+    fp8_dma_kernel<T, WIDE, BT, BN, WT, WN, S, FLOW, true><<<tt * tn * plan.splits, 64 * WT * WN, 0, s>>>(p, tt, tn, per, ws);
     fp8_sum_kernel<T><<<(unsigned)std::min<int64_t>(cdiv(p.m * p.n, 256), 2048), 256, 0, s>>>(p, plan.splits, ws);
   }
   return hipGetLastError();
@@ -445,16 +690,22 @@ hipError_t launch_dma(const Fp8Plan& plan, const Fp8Args& p, float* ws, hipStrea
 template <typename T>
 hipError_t launch(const Fp8Plan& plan, const Fp8Args& p, float* ws, hipStream_t s) {
   constexpr bool WIDE = std::is_same<T, float>::value;
-  const unsigned few = (unsigned)cdiv(p.n, 16);
-  if (plan.kind == kFp8Few) {
-    if (p.m <= 16) fp8_few_kernel<T, 1><<<few, 64 * kFewWaves, 0, s>>>(p);
-    else if (p.m <= 32) fp8_few_kernel<T, 2><<<few, 64 * kFewWaves, 0, s>>>(p);
-    else fp8_few_kernel<T, 4><<<few, 64 * kFewWaves, 0, s>>>(p);
-    return hipGetLastError();
-  }
   // the direct loads need 16-byte rows, 32-bit offsets inside a tile and a whole block
   const bool dma = p.k >= kBlk && (((uintptr_t)p.X | (uintptr_t)p.W | (uint64_t)p.ld_x | (uint64_t)p.ld_w) & 15) == 0 &&
                    std::max(p.ld_x, p.ld_w) <= (int64_t(1) << 22);
+  const unsigned few = (unsigned)cdiv(p.n, 16);
+  if (plan.kind == kFp8Few) {
+    if (!dma) {
+      if (p.m <= 16) fp8_few_kernel<T, 1, 1, false><<<few, 64 * kFewWaves, 0, s>>>(p);
+      else if (p.m <= 32) fp8_few_kernel<T, 2, 1, false><<<few, 64 * kFewWaves, 0, s>>>(p);
+      else fp8_few_kernel<T, 4, 1, false><<<few, 64 * kFewWaves, 0, s>>>(p);
+    } else {
+      if (p.m <= 16) fp8_few_kernel<T, 1, 2, true><<<few, 64 * kFewWaves, 0, s>>>(p);
+      else if (p.m <= 32) fp8_few_kernel<T, 2, 2, true><<<few, 64 * kFewWaves, 0, s>>>(p);
+      else fp8_few_kernel<T, 4, 2, true><<<few, 64 * kFewWaves, 0, s>>>(p);
+    }
+    return hipGetLastError();
+  }
   if (!dma) {
     const dim3 grid((unsigned)cdiv(p.n, kTile), (unsigned)cdiv(p.m, kTile));
     fp8_tile_kernel<T><<<grid, 256, 0, s>>>(p.X, p.ld_x, p.sx, p.ld_sx, p.W, p.ld_w, p.sw, p.ld_sw, p.m, p.n, p.k,
@@ -462,10 +713,10 @@ hipError_t launch(const Fp8Plan& plan, const Fp8Args& p, float* ws, hipStream_t 
     return hipGetLastError();
   }
   if (plan.kind == kFp8Large) {
-    if constexpr (WIDE) return launch_dma<T, WIDE, 128, 256, 2, 4>(plan, p, ws, s);
-    else return launch_dma<T, WIDE, 256, 256, 2, 4>(plan, p, ws, s);
+    if constexpr (WIDE) return launch_dma<T, WIDE, 128, 128, 2, 2, 2, kBlocks>(plan, p, ws, s);
+    else return launch_dma<T, WIDE, 256, 256, 2, 4, 2, kBlocks>(plan, p, ws, s);
   }
-  return launch_dma<T, WIDE, 128, 128, 2, 2>(plan, p, ws, s);
+  return launch_dma<T, WIDE, 128, 64, 4, 2, 6, kAhead>(plan, p, ws, s);
 }
 
 }  // namespace
@@ -478,8 +729,8 @@ Fp8Plan fp8_plan(int64_t m, int64_t n, int64_t k) {
     return p;
   }
   p.kind = kFp8Medium;
-  const int64_t tiles = cdiv(m, kTile) * cdiv(n, kTile), nblk = cdiv(k, kBlk);
-  const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(512 / tiles, nblk / 4));
+  const int64_t tiles = cdiv(m, 128) * cdiv(n, 64), nblk = cdiv(k, kBlk);
+  const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(256 / tiles, nblk / 8));
   p.splits = (int)cdiv(nblk, cdiv(nblk, splits));     // none empty
   if (p.splits > 1) p.ws_bytes = (size_t)p.splits * m * n * sizeof(float);
   return p;
