@@ -122,8 +122,9 @@ __device__ __forceinline__ void store4(T* __restrict__ Y, int64_t ld_y, const T*
 
 // A wave's 16 rows x 64 outputs of four neighbouring tiles: v[a] holds outputs 16 a +
 // 4 q .. + 3 of the lane's row.  For 16-bit types the four lanes of a row swap parts
-// (registers only), so that each holds 16 outputs in a row and stores 32 bytes.
-template <typename T>
+// (registers only), so that each holds 16 outputs in a row and stores 32 bytes; STREAM:
+// past the caches' keeping, for outputs larger than they hold.
+template <bool STREAM, typename T>
 __device__ __forceinline__ void store_row64(T* __restrict__ Y, int64_t ld_y, const T* __restrict__ bias, int64_t i, int64_t j0,
                                             int q, int64_t m, int64_t n, const f32x4 (&v)[4]) {
   if constexpr (sizeof(T) == 2) {
@@ -162,8 +163,14 @@ __device__ __forceinline__ void store_row64(T* __restrict__ Y, int64_t ld_y, con
       }
       if (i < m) {
         T* y = Y + i * ld_y + j0 + 16 * q;
-        *(u32x4_at2*)y = u32x4_at2{u[0][0], u[0][1], u[1][0], u[1][1]};
-        *(u32x4_at2*)(y + 8) = u32x4_at2{u[2][0], u[2][1], u[3][0], u[3][1]};
+        const u32x4_at2 lo = {u[0][0], u[0][1], u[1][0], u[1][1]}, hi = {u[2][0], u[2][1], u[3][0], u[3][1]};
+        if constexpr (STREAM) {
+          __builtin_nontemporal_store(lo, (u32x4_at2*)y);
+          __builtin_nontemporal_store(hi, (u32x4_at2*)(y + 8));
+        } else {
+          *(u32x4_at2*)y = lo;
+          *(u32x4_at2*)(y + 8) = hi;
+        }
       }
       return;
     }
@@ -326,36 +333,35 @@ __global__ __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_per_eu(
 // block; the tile of W has one scale, fetched a block ahead.  A last block of fewer than
 // 128 columns is taken first, through registers, with zeros behind column k.  Scaling
 // lags one row of tiles behind the matrix instructions, so it runs beside them.
-// stage I of a kernel's buffers, variables of their own
+// stage I of a kernel's buffers, variables of their own: one for each group of waves
 template <int BT>
 struct __attribute__((aligned(16))) StageX {
   uint8_t x[BT * kBlk];
   float sx[BT + 64];      // each wave's load of the rows' scales writes 64 of them, the next wave's first ones too
 };
-template <int BT, int I>
-__device__ __forceinline__ StageX<BT>& stage_x() {
-  __shared__ StageX<BT> s;
+template <int BT, int WK, int I>
+__device__ __forceinline__ StageX<BT> (&stage_x())[WK] {
+  __shared__ StageX<BT> s[WK];
   return s;
 }
 template <int BN>
 struct __attribute__((aligned(16))) StageW {
   uint8_t w[BN * kBlk];
 };
-template <int BN, int I>
-__device__ __forceinline__ StageW<BN>& stage_w() {
-  __shared__ StageW<BN> s;
+template <int BN, int WK, int I>
+__device__ __forceinline__ StageW<BN> (&stage_w())[WK] {
+  __shared__ StageW<BN> s[WK];
   return s;
 }
 
 // how a work-group keeps its buffers full
 enum Flow {
   kBlocks,      // S buffers; one barrier per block
-  kAhead,       // S buffers; a block's codes are read into registers while the one before is multiplied
-  kCarry        // 2 buffers; the next block's first codes are read beside this one's last products
+  kAhead        // S buffers; a block's codes are read into registers while the one before is multiplied
 };
 
-template <typename T, bool WIDE, int BT, int BN, int WT, int WN, int S, Flow FLOW, bool SPLIT>
-__global__ __launch_bounds__(64 * WT * WN) __attribute__((amdgpu_waves_per_eu(2))) void fp8_dma_kernel(Fp8Args p, int tiles_t, int tiles_n, int blocks_per_split,
+template <typename T, bool WIDE, int BT, int BN, int WT, int WN, int WK, int S, Flow FLOW, bool SPLIT>
+__global__ __launch_bounds__(64 * WT * WN * WK) __attribute__((amdgpu_waves_per_eu(2))) void fp8_dma_kernel(Fp8Args p, int tiles_t, int tiles_n, int blocks_per_split,
                                                                float* __restrict__ parts) {
   constexpr int kWavesHere = WT * WN, TT = BT / WT / 16, TN = BN / WN / 16;
   constexpr int kXLoads = BT / 8 / kWavesHere, kWLoads = BN / 8 / kWavesHere;
@@ -364,7 +370,8 @@ __global__ __launch_bounds__(64 * WT * WN) __attribute__((amdgpu_waves_per_eu(2)
   constexpr int kScaleRows = BT / kWavesHere;
   constexpr int kLoads = kXLoads + kWLoads + 1;        // of a wave, per block
   static_assert((S - 2) * kLoads < 64, "counted by vmcnt");
-  const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane((t >> 6) % kWavesHere);
+  const int g = __builtin_amdgcn_readfirstlane((t >> 6) / kWavesHere);      // the wave's group
   const int lr = lane & 15, q = lane >> 4;
   // work-groups of one XCD take neighbouring tiles: bands of 8 tiles along X, W outermost
   const int tiles = tiles_t * tiles_n;
@@ -400,9 +407,9 @@ __global__ __launch_bounds__(64 * WT * WN) __attribute__((amdgpu_waves_per_eu(2)
   };
   const auto fetch = [&](auto i, int b) {
 #pragma unroll
-    for (int l = 0; l <= kXLoads; ++l) fetch_x(stage_x<BT, i.value>(), b, l);
+    for (int l = 0; l <= kXLoads; ++l) fetch_x(stage_x<BT, WK, i.value>()[g], b, l);
 #pragma unroll
-    for (int l = 0; l < kWLoads; ++l) fetch_w(stage_w<BN, i.value>(), b, l);
+    for (int l = 0; l < kWLoads; ++l) fetch_w(stage_w<BN, WK, i.value>()[g], b, l);
   };
   f32x4 acc[TT][TN];
 #pragma unroll
@@ -455,97 +462,53 @@ __global__ __launch_bounds__(64 * WT * WN) __attribute__((amdgpu_waves_per_eu(2)
   };
   // a block of fewer than 128 columns, through registers
   const auto fetch_tail = [&](int b) {
-    StageX<BT>& sx = stage_x<BT, 0>();
-    for (int id = t; id < (BT + BN) * 8; id += 64 * kWavesHere) {
+    StageX<BT>& sx = stage_x<BT, WK, 0>()[0];
+    for (int id = t; id < (BT + BN) * 8; id += 64 * kWavesHere * WK) {
       const bool is_x = id < BT * 8;
       const int r = is_x ? id >> 3 : (id >> 3) - BT, c = id & 7;
       const uint8_t* row = is_x ? p.X + (i0 + min(r, rows_x - 1)) * p.ld_x : p.W + (j0 + min(r, rows_w - 1)) * p.ld_w;
       const u32x4 v = load_chunk(row, (int64_t)b * kBlk + 16 * c, p.k);
       const int at = r * kBlk + ((c ^ (r & 7)) * 16);
       if (is_x) *(u32x4*)(sx.x + at) = v;
-      else *(u32x4*)(stage_w<BN, 0>().w + at) = v;
+      else *(u32x4*)(stage_w<BN, WK, 0>()[0].w + at) = v;
     }
     if (t < BT) sx.sx[t] = p.sx[(int64_t)b * p.ld_sx + i0 + min(t, rows_x - 1)];
   };
   const bool tail = b1 == nblk && (p.k % kBlk) != 0;
-  const int steps = b1 - b0;
-  const auto block_of = [&](int step) { return !tail ? b0 + step : step == 0 ? nblk - 1 : b0 + step - 1; };
+  // the groups take the blocks in turn
+  const int count = b1 - b0, steps = (count + WK - 1) / WK;
+  const auto block_of = [&](int at) { return !tail ? b0 + at : at == 0 ? nblk - 1 : b0 + at - 1; };
   // behind the last block, block 0, which is not used: with a fetch on every path the
   // counts of outstanding loads are known, and no read waits for a later block
-  const auto next = [&](int step) { return step < steps ? block_of(step) : 0; };
+  const auto next = [&](int step) { return step * WK + g < count ? block_of(step * WK + g) : 0; };
   float sw_next = swp[next(0)];
   if (tail) fetch_tail(nblk - 1);
-  else fetch(std::integral_constant<int, 0>{}, b0);
+  if (!tail || g > 0) fetch(std::integral_constant<int, 0>{}, next(0));
   int step = 0;
+  // one(stage, whether the group has a block): only in the last step may it have none
   const auto run = [&](auto&& one) {
-    while (step + S <= steps) static_for<0, S>(one);
-    static_for<0, S - 1>([&](auto i) {
-      if (step < steps) one(i);
+    while (step + S < steps) static_for<0, S>([&](auto i) { one(i, true); });
+    static_for<0, S>([&](auto i) {
+      if (step < steps) one(i, WK == 1 || step * WK + g < count);
     });
   };
   if constexpr (FLOW == kBlocks) {
     static_for<1, S - 1>([&](auto i) { fetch(i, next(i.value)); });
-    run([&](auto i) {
+    run([&](auto i, bool has) {
       constexpr int h = i.value, to = (h + S - 1) % S;
-      const StageX<BT>& s = stage_x<BT, h>();
+      const StageX<BT>& s = stage_x<BT, WK, h>()[g];
       // this block has arrived, and every wave is done with the buffer that is filled next
       asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S - 2) * kLoads) : "memory");
       const float sw = sw_next;
       sw_next = swp[next(step + 1)];
       fetch(std::integral_constant<int, to>{}, next(step + S - 1));
+      ++step;
+      if (!has) return;
       i32x8 wv[TN];
 #pragma unroll
-      for (int a = 0; a < TN; ++a) wv[a] = pick(stage_w<BN, h>().w, w0, w1, a);
+      for (int a = 0; a < TN; ++a) wv[a] = pick(stage_w<BN, WK, h>()[g].w, w0, w1, a);
       multiply(wv, [&](int c) { return pick(s.x, x0, x1, c); }, [&](int c) { return s.sx[sx0 + 16 * c]; }, sw,
                [](int) {});
-      ++step;
-    });
-  } else if constexpr (FLOW == kCarry) {
-    static_assert(S == 2 && TT >= 2, "two buffers");
-    fetch(std::integral_constant<int, 1>{}, next(1));
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLoads) : "memory");
-    Frag<WIDE> wf[TN], xf;
-    float sc, sc_last = 0.f, sw = sw_next;      // sc: a row scale as read, multiplied by sw only when it is used
-#pragma unroll
-    for (int a = 0; a < TN; ++a) wf[a] = Frag<WIDE>(pick(stage_w<BN, 0>().w, w0, w1, a));
-    xf = Frag<WIDE>(pick(stage_x<BT, 0>().x, x0, x1, 0));
-    sc = stage_x<BT, 0>().sx[sx0];
-    run([&](auto i) {
-      constexpr int h = i.value, to = h ^ 1;
-      sw_next = swp[next(step + 1)];
-      f32x4 last[TN];
-#pragma unroll
-      for (int c = 0; c < TT; ++c) {
-        f32x4 d[TN];
-        i32x8 xn;
-        float sn;
-        if (c + 1 < TT) {
-          xn = pick(stage_x<BT, h>().x, x0, x1, c + 1);
-          sn = stage_x<BT, h>().sx[sx0 + 16 * (c + 1)];
-        } else {
-          // the next block has arrived, and every wave has read all of this one
-          asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-          xn = pick(stage_x<BT, to>().x, x0, x1, 0);
-          sn = stage_x<BT, to>().sx[sx0];
-        }
-#pragma unroll
-        for (int a = 0; a < TN; ++a) {
-          d[a] = block_product(wf[a], xf);
-          if (c + 1 == TT) wf[a] = Frag<WIDE>(pick(stage_w<BN, to>().w, w0, w1, a));
-          if (c > 0) scale_add(acc[c - 1][a], last[a], sc_last);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-        if (c + 1 == TT) fetch(i, next(step + 2));
-#pragma unroll
-        for (int a = 0; a < TN; ++a) last[a] = d[a];
-        sc_last = sw * sc;
-        sc = sn;
-        xf = Frag<WIDE>(xn);
-      }
-#pragma unroll
-      for (int a = 0; a < TN; ++a) scale_add(acc[TT - 1][a], last[a], sc_last);
-      sw = sw_next;
-      ++step;
     });
   } else {
     static_assert(S % 2 == 0, "two sets of registers in turn");
@@ -562,36 +525,59 @@ __global__ __launch_bounds__(64 * WT * WN) __attribute__((amdgpu_waves_per_eu(2)
     };
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S - 1) * kLoads) : "memory");
 #pragma unroll
-    for (int l = 0; l < kReads; ++l) read_one(0, stage_x<BT, 0>(), stage_w<BN, 0>(), l);
-    run([&](auto i) {
+    for (int l = 0; l < kReads; ++l) read_one(0, stage_x<BT, WK, 0>()[g], stage_w<BN, WK, 0>()[g], l);
+    run([&](auto i, bool has) {
       constexpr int h = i.value, set = h & 1, nx = (h + 1) % S;
       // the next block has arrived, and every wave has read this one
       asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S - 2) * kLoads) : "memory");
       const float sw = sw_next;
       sw_next = swp[next(step + 1)];
       const int b = next(step + S);
+      ++step;
+      if (!has) return;
       multiply(wv[set], [&](int c) { return xv[set][c]; }, [&](int c) { return sxv[set][c]; }, sw, [&](int c) {
 #pragma unroll
         for (int l = 0; l < kReads; ++l)
-          if (l * TT / kReads == c) read_one(set ^ 1, stage_x<BT, nx>(), stage_w<BN, nx>(), l);
+          if (l * TT / kReads == c) read_one(set ^ 1, stage_x<BT, WK, nx>()[g], stage_w<BN, WK, nx>()[g], l);
 #pragma unroll
         for (int l = 0; l < kLoads; ++l)
           if (l * TT / kLoads == c) {
-            if (l <= kXLoads) fetch_x(stage_x<BT, h>(), b, l);
-            else fetch_w(stage_w<BN, h>(), b, l - kXLoads - 1);
+            if (l <= kXLoads) fetch_x(stage_x<BT, WK, h>()[g], b, l);
+            else fetch_w(stage_w<BN, WK, h>()[g], b, l - kXLoads - 1);
           }
       });
-      ++step;
     });
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // unused fetches write LDS: not after this work-group's end
+  if constexpr (WK > 1) {
+    // group 1's sums are added to group 0's through stage 0's rows of X, as many tiles of
+    // each wave at a time as fit
+    constexpr int kFit = (int)sizeof(StageX<BT>::x) / (16 * 64 * kWavesHere);
+    static_assert(WK == 2 && kFit >= 1, "two groups");
+    f32x4* const sums = (f32x4*)stage_x<BT, WK, 0>()[0].x + w * kFit * 64 + lane;
+#pragma unroll
+    for (int e0 = 0; e0 < TT * TN; e0 += kFit) {
+      // every wave's reads are done: of the last block, then of the sums before
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      if (g == 1) {
+#pragma unroll
+        for (int e = e0; e < e0 + kFit && e < TT * TN; ++e) sums[(e - e0) * 64] = acc[e / TN][e % TN];
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      if (g == 0) {
+#pragma unroll
+        for (int e = e0; e < e0 + kFit && e < TT * TN; ++e) acc[e / TN][e % TN] += sums[(e - e0) * 64];
+      }
+    }
+    if (g == 1) return;
+  }
 #pragma unroll
   for (int c = 0; c < TT; ++c) {
     const int64_t i = i0 + wi + 16 * c + lr, j = j0 + wj;
     float* part_y = parts + (int64_t)part * p.m * p.n;
     if constexpr (TN == 4) {
-      if constexpr (SPLIT) store_row64<float>(part_y, p.n, nullptr, i, j, q, p.m, p.n, acc[c]);
-      else store_row64<T>((T*)p.Y, p.ld_y, (const T*)p.bias, i, j, q, p.m, p.n, acc[c]);
+      if constexpr (SPLIT) store_row64<false, float>(part_y, p.n, nullptr, i, j, q, p.m, p.n, acc[c]);
+      else store_row64<(BT == 256), T>((T*)p.Y, p.ld_y, (const T*)p.bias, i, j, q, p.m, p.n, acc[c]);
     } else {
 #pragma unroll
       for (int a = 0; a < TN; ++a) {
@@ -674,14 +660,14 @@ __global__ __launch_bounds__(256) void fp8_tile_kernel(const uint8_t* __restrict
       store4<T>(Y, ld_y, bias, i0 + wi + 16 * c + lr, j0 + wj + 16 * a + 4 * q, m, n, acc[c][a]);
 }
 
-template <typename T, bool WIDE, int BT, int BN, int WT, int WN, int S, Flow FLOW>
+template <typename T, bool WIDE, int BT, int BN, int WT, int WN, int WK, int S, Flow FLOW>
 hipError_t launch_dma(const Fp8Plan& plan, const Fp8Args& p, float* ws, hipStream_t s) {
   const int tt = (int)cdiv(p.m, BT), tn = (int)cdiv(p.n, BN);
   const int per = (int)cdiv(cdiv(p.k, kBlk), plan.splits);
   if (plan.splits == 1) {
-    fp8_dma_kernel<T, WIDE, BT, BN, WT, WN, S, FLOW, false><<<tt * tn, 64 * WT * WN, 0, s>>>(p, tt, tn, per, nullptr);
+    fp8_dma_kernel<T, WIDE, BT, BN, WT, WN, WK, S, FLOW, false><<<tt * tn, 64 * WT * WN * WK, 0, s>>>(p, tt, tn, per, nullptr);
   } else {
-    fp8_dma_kernel<T, WIDE, BT, BN, WT, WN, S, FLOW, true><<<tt * tn * plan.splits, 64 * WT * WN, 0, s>>>(p, tt, tn, per, ws);
+    fp8_dma_kernel<T, WIDE, BT, BN, WT, WN, WK, S, FLOW, true><<<tt * tn * plan.splits, 64 * WT * WN * WK, 0, s>>>(p, tt, tn, per, ws);
     fp8_sum_kernel<T><<<(unsigned)std::min<int64_t>(cdiv(p.m * p.n, 256), 2048), 256, 0, s>>>(p, plan.splits, ws);
   }
   return hipGetLastError();
@@ -712,27 +698,37 @@ hipError_t launch(const Fp8Plan& plan, const Fp8Args& p, float* ws, hipStream_t 
                                             (const T*)p.bias, (T*)p.Y, p.ld_y);
     return hipGetLastError();
   }
-  if (plan.kind == kFp8Large) {
-    if constexpr (WIDE) return launch_dma<T, WIDE, 128, 128, 2, 2, 2, kBlocks>(plan, p, ws, s);
-    else return launch_dma<T, WIDE, 256, 256, 2, 4, 2, kBlocks>(plan, p, ws, s);
+  switch (plan.kind) {
+    case kFp8T64x32: return launch_dma<T, WIDE, 64, 32, 2, 2, 2, 4, kAhead>(plan, p, ws, s);
+    case kFp8T64x64: return launch_dma<T, WIDE, 64, 64, 2, 2, 2, 4, kAhead>(plan, p, ws, s);
+    case kFp8T96x64: return launch_dma<T, WIDE, 96, 64, 2, 2, 2, 3, kBlocks>(plan, p, ws, s);
+    case kFp8T128x64: return launch_dma<T, WIDE, 128, 64, 2, 2, 2, 3, kBlocks>(plan, p, ws, s);
+    case kFp8T256x256:
+      if constexpr (!WIDE) return launch_dma<T, WIDE, 256, 256, 2, 4, 1, 2, kBlocks>(plan, p, ws, s);
+      [[fallthrough]];
+    default: return launch_dma<T, WIDE, 128, 128, 2, 2, 1, 2, kBlocks>(plan, p, ws, s);
   }
-  return launch_dma<T, WIDE, 128, 64, 4, 2, 6, kAhead>(plan, p, ws, s);
 }
 
 }  // namespace
 
 Fp8Plan fp8_plan(int64_t m, int64_t n, int64_t k) {
   Fp8Plan p{kFp8Few, 1, 0};
-  if (m <= 64) return p;
-  if (cdiv(m, 256) * cdiv(n, 256) >= 192) {
-    p.kind = kFp8Large;
+  if (m <= 32 || (m <= 64 && n <= 16 * 256)) return p;
+  // the smallest tiles that one round of 256 CUs covers
+  const struct { int kind, bt, bn; } small[] = {
+      {kFp8T64x32, 64, 32}, {kFp8T64x64, 64, 64}, {kFp8T96x64, 96, 64}, {kFp8T128x64, 128, 64}};
+  for (const auto& c : small) {
+    const int64_t tiles = cdiv(m, c.bt) * cdiv(n, c.bn);
+    if (tiles > 256) continue;
+    p.kind = c.kind;
+    const int64_t nblk = cdiv(k, kBlk), splits = std::max<int64_t>(1, std::min<int64_t>(256 / tiles, nblk / 16));
+    p.splits = (int)cdiv(nblk, cdiv(nblk, splits));     // none empty
+    if (p.splits > 1) p.ws_bytes = (size_t)p.splits * m * n * sizeof(float);
     return p;
   }
-  p.kind = kFp8Medium;
-  const int64_t tiles = cdiv(m, 128) * cdiv(n, 64), nblk = cdiv(k, kBlk);
-  const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(256 / tiles, nblk / 8));
-  p.splits = (int)cdiv(nblk, cdiv(nblk, splits));     // none empty
-  if (p.splits > 1) p.ws_bytes = (size_t)p.splits * m * n * sizeof(float);
+  const int64_t t128 = cdiv(m, 128) * cdiv(n, 128), t256 = cdiv(m, 256) * cdiv(n, 256);
+  p.kind = cdiv(t256, 256) * 854 < t128 ? kFp8T256x256 : kFp8T128x128;
   return p;
 }
 

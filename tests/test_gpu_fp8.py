@@ -112,7 +112,7 @@ def check(y, out, xc, sx, wc, sw, bias=None):
 SHAPES = [(1, 1, 1), (1, 128, 128), (1, 129, 100), (2, 300, 256), (5, 17, 1000), (15, 64, 384), (16, 260, 129),
           (17, 128, 512), (31, 333, 640), (33, 1, 200), (48, 500, 300), (64, 128, 2048), (65, 130, 260), (100, 100, 100),
           (128, 128, 128), (129, 129, 129), (130, 384, 1024), (200, 520, 77), (257, 260, 640), (300, 1030, 1200),
-          (520, 390, 256)]
+          (520, 390, 256), (70, 70, 130), (66, 200, 384), (90, 64, 1153), (100, 140, 1663), (250, 1000, 897)]
 
 
 @pytest.mark.parametrize("m,n,k", SHAPES, ids=[f"{m}x{n}x{k}" for m, n, k in SHAPES])
@@ -128,7 +128,9 @@ def test_matmul_parity(m, n, k, out, biased):
     check(y, out, xc, sx, wc, sw, bias)
 
 
-@pytest.mark.parametrize("m,n,k,out", [(300, 24581, 200, "f16"), (260, 24580, 257, "f32"), (1025, 10001, 128, "bf16"),
+@pytest.mark.parametrize("m,n,k,out", [(300, 24581, 200, "f16"), (1000, 16300, 384, "f16"), (2050, 8190, 263, "bf16"),
+                                       (300, 3300, 1150, "f16"), (500, 4100, 520, "bf16"), (100, 8200, 1000, "f16"),
+                                       (40, 5000, 2050, "f32"), (64, 4000, 1040, "f16"), (380, 4096, 1280, "f32"), (260, 24580, 257, "f32"), (1025, 10001, 128, "bf16"),
                                        (513, 16500, 384, "f32")])
 def test_matmul_parity_large(m, n, k, out):
     """Enough outputs for the largest tiles, with ragged edges on every side."""
