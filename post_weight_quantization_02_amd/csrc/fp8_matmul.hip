@@ -703,6 +703,7 @@ hipError_t launch(const Fp8Plan& plan, const Fp8Args& p, float* ws, hipStream_t 
     case kFp8T64x64: return launch_dma<T, WIDE, 64, 64, 2, 2, 2, 4, kAhead>(plan, p, ws, s);
     case kFp8T96x64: return launch_dma<T, WIDE, 96, 64, 2, 2, 2, 3, kBlocks>(plan, p, ws, s);
     case kFp8T128x64: return launch_dma<T, WIDE, 128, 64, 2, 2, 2, 3, kBlocks>(plan, p, ws, s);
+    case kFp8T128x128Two: return launch_dma<T, WIDE, 128, 128, 2, 2, 2, 2, kBlocks>(plan, p, ws, s);
     case kFp8T256x256:
       if constexpr (!WIDE) return launch_dma<T, WIDE, 256, 256, 2, 4, 1, 2, kBlocks>(plan, p, ws, s);
       [[fallthrough]];
@@ -717,7 +718,8 @@ Fp8Plan fp8_plan(int64_t m, int64_t n, int64_t k) {
   if (m <= 32 || (m <= 64 && n <= 16 * 256)) return p;
   // the smallest tiles that one round of 256 CUs covers
   const struct { int kind, bt, bn; } small[] = {
-      {kFp8T64x32, 64, 32}, {kFp8T64x64, 64, 64}, {kFp8T96x64, 96, 64}, {kFp8T128x64, 128, 64}};
+      {kFp8T64x32, 64, 32}, {kFp8T64x64, 64, 64}, {kFp8T96x64, 96, 64}, {kFp8T128x64, 128, 64},
+      {kFp8T128x128Two, 128, 128}};
   for (const auto& c : small) {
     const int64_t tiles = cdiv(m, c.bt) * cdiv(n, c.bn);
     if (tiles > 256) continue;

@@ -76,7 +76,8 @@ enum { kF32 = 0, kF16 = 1, kBF16 = 2 };
 hipError_t fp8_quantize_launch(const void* X, int x_dtype, int64_t m, int64_t k, int64_t ld_x, int64_t block_rows,
                                uint8_t* codes, int64_t ld_codes, float* scales, int64_t ld_scales, hipStream_t s);
 
-enum { kFp8Few, kFp8T64x32, kFp8T64x64, kFp8T96x64, kFp8T128x64, kFp8T128x128, kFp8T256x256 };   // rows of X x rows of W
+enum { kFp8Few, kFp8T64x32, kFp8T64x64, kFp8T96x64, kFp8T128x64, kFp8T128x128Two, kFp8T128x128,
+       kFp8T256x256 };      // rows of X x rows of W
 struct Fp8Plan {
   int kind;
   int splits;             // parts of k, summed by a second launch when more than one
