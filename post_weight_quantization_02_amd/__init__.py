@@ -229,25 +229,25 @@ def _expect(t, name, shape, dtypes, device):
             raise ValueError(f"{name} has overlapping rows")
 
 
-def _no_grad(where, *tensors):
-    if _torch().is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
-        raise ValueError(f"{where} has no backward pass: detach its inputs or call it under torch.no_grad()")
+def _grad_error(where):
+    return ValueError(f"{where} has no backward pass: detach its inputs or call it under torch.no_grad()")
 
 
-def _launch(device, stream, fn, args, tensors, where):
+def _launch(torch, device, stream, fn, args, tensors, where):
     """fn(*args, stream handle) on ``device``: on its current stream, or on ``stream``,
     which has to belong to it (ordered as in _stream)."""
-    torch = _torch()
     if stream is not None and stream.device != device:
         raise ValueError(f"{where}: the stream belongs to {stream.device}, the tensors to {device}")
     if device.index != torch.cuda.current_device():
         with torch.cuda.device(device):
-            return _launch(device, stream, fn, args, tensors, where)
+            return _launch(torch, device, stream, fn, args, tensors, where)
     if stream is None:
         handle = torch._C._cuda_getCurrentRawStream(device.index)     # current_stream() without the Python object
     else:
         handle = _stream(stream, *tensors)
-    _check(fn(*args, handle), where)
+    status = fn(*args, handle)
+    if status != 0:
+        raise GPTQError(status, where)
 
 
 def _pitch(t) -> int:
@@ -255,14 +255,14 @@ def _pitch(t) -> int:
     return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
 
 
-def _ws_ptr(nbytes: int, device, ws):
+def _ws_ptr(torch, nbytes: int, device, ws):
     """(tensor or None, address, bytes) of a workspace that may be empty."""
-    torch = _torch()
     if ws is None:
         if nbytes == 0:
             return None, None, 0
         ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    elif ws.device != device or not ws.is_contiguous():
+        return ws, ws.data_ptr(), nbytes
+    if ws.device != device or not ws.is_contiguous():
         raise ValueError(f"ws must be a contiguous tensor on {device}")
     return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
@@ -506,7 +506,8 @@ def gptq_fp8_quantize(X, block_rows: int = 1, codes=None, scales=None, stream=No
     made here have rows a multiple of 128 bytes apart."""
     torch = _torch()
     _rowmajor(X, "X")
-    _no_grad("gptq_fp8_quantize", X)
+    if X.requires_grad and torch.is_grad_enabled():
+        raise _grad_error("gptq_fp8_quantize")
     code = _elem_code(X, "X")
     m, k = X.shape
     dev = X.device
@@ -522,7 +523,7 @@ def gptq_fp8_quantize(X, block_rows: int = 1, codes=None, scales=None, stream=No
         scales = torch.empty(shape, dtype=torch.float32, device=dev)
     else:
         _expect(scales, "scales", shape, (torch.float32,), dev)
-    _launch(dev, stream, library().gptq_fp8_quantize,
+    _launch(torch, dev, stream, library().gptq_fp8_quantize,
             (X.data_ptr(), code, m, k, _pitch(X), int(block_rows), codes.data_ptr(), _pitch(codes), scales.data_ptr(),
              _pitch(scales)), (X, codes, scales), "gptq_fp8_quantize")
     return codes, scales
@@ -550,7 +551,9 @@ def gptq_fp8_matmul(x_codes, x_scales, w_codes, w_scales, bias=None, Y=None, out
     _expect(w_codes, "w_codes", (n, k), fp8, dev)
     _expect(x_scales, "x_scales", (kb, m), (torch.float32,), dev)
     _expect(w_scales, "w_scales", (-(-n // 128), kb), (torch.float32,), dev)
-    _no_grad("gptq_fp8_matmul", x_scales, w_scales, bias, Y)
+    if torch.is_grad_enabled() and (x_scales.requires_grad or w_scales.requires_grad or
+                                    (bias is not None and bias.requires_grad) or (Y is not None and Y.requires_grad)):
+        raise _grad_error("gptq_fp8_matmul")
     if Y is None:
         Y = torch.empty((m, n), dtype=out_dtype or torch.float32, device=dev)
     else:
@@ -558,8 +561,8 @@ def gptq_fp8_matmul(x_codes, x_scales, w_codes, w_scales, bias=None, Y=None, out
     y_code = _elem_code(Y, "Y")
     if bias is not None:
         _expect(bias, "bias", (n,), (Y.dtype,), dev)
-    ws, ws_ptr, ws_bytes = _ws_ptr(library().gptq_fp8_matmul_workspace_size(m, n, k), dev, ws)
-    _launch(dev, stream, library().gptq_fp8_matmul,
+    ws, ws_ptr, ws_bytes = _ws_ptr(torch, library().gptq_fp8_matmul_workspace_size(m, n, k), dev, ws)
+    _launch(torch, dev, stream, library().gptq_fp8_matmul,
             (x_codes.data_ptr(), _pitch(x_codes), x_scales.data_ptr(), _pitch(x_scales), w_codes.data_ptr(),
              _pitch(w_codes), w_scales.data_ptr(), _pitch(w_scales), m, n, k, _ptr(bias), Y.data_ptr(), y_code,
              _pitch(Y), ws_ptr, ws_bytes), (x_codes, x_scales, w_codes, w_scales, bias, Y, ws), "gptq_fp8_matmul")
@@ -579,29 +582,30 @@ def gptq_token_logprobs(logits, tokens, top_k: int = 0, logprobs=None, entropy=N
     [n x top_k]), fp32 but for the ids."""
     torch = _torch()
     _rowmajor(logits, "logits")
-    _no_grad("gptq_token_logprobs", logits)
+    if logits.requires_grad and torch.is_grad_enabled():
+        raise _grad_error("gptq_token_logprobs")
     code = _elem_code(logits, "logits")
     n, v = logits.shape
     dev = logits.device
     top_k = int(top_k)
-    _expect(tokens, "tokens", (n,), (torch.int64,), dev)
-    if not tokens.is_contiguous():
-        raise ValueError("tokens must be contiguous")
-
-    def out(t, name, shape, dtype):
-        if t is None:
-            return torch.empty(shape, dtype=dtype, device=dev)
-        _expect(t, name, shape, (dtype,), dev)
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        return t
-
-    logprobs = out(logprobs, "logprobs", (n,), torch.float32)
-    entropy = out(entropy, "entropy", (n,), torch.float32)
-    top_ids = out(top_ids, "top_ids", (n, max(top_k, 0)), torch.int32)
-    top_logprobs = out(top_logprobs, "top_logprobs", (n, max(top_k, 0)), torch.float32)
-    ws, ws_ptr, ws_bytes = _ws_ptr(library().gptq_token_logprobs_workspace_size(n, v, top_k), dev, ws)
-    _launch(dev, stream, library().gptq_token_logprobs,
+    given = (("tokens", tokens, (n,), torch.int64), ("logprobs", logprobs, (n,), torch.float32),
+             ("entropy", entropy, (n,), torch.float32), ("top_ids", top_ids, (n, max(top_k, 0)), torch.int32),
+             ("top_logprobs", top_logprobs, (n, max(top_k, 0)), torch.float32))
+    for name, t, shape, dtype in given:
+        if t is not None:
+            _expect(t, name, shape, (dtype,), dev)
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+    if logprobs is None:
+        logprobs = torch.empty(n, dtype=torch.float32, device=dev)
+    if entropy is None:
+        entropy = torch.empty(n, dtype=torch.float32, device=dev)
+    if top_ids is None:
+        top_ids = torch.empty((n, max(top_k, 0)), dtype=torch.int32, device=dev)
+    if top_logprobs is None:
+        top_logprobs = torch.empty((n, max(top_k, 0)), dtype=torch.float32, device=dev)
+    ws, ws_ptr, ws_bytes = _ws_ptr(torch, library().gptq_token_logprobs_workspace_size(n, v, top_k), dev, ws)
+    _launch(torch, dev, stream, library().gptq_token_logprobs,
             (logits.data_ptr(), code, n, v, _pitch(logits), tokens.data_ptr(), top_k, logprobs.data_ptr(),
              entropy.data_ptr(), top_ids.data_ptr(), top_logprobs.data_ptr(), ws_ptr, ws_bytes),
             (logits, tokens, logprobs, entropy, top_ids, top_logprobs, ws), "gptq_token_logprobs")

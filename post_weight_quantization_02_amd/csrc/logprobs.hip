@@ -6,10 +6,13 @@
 //   log p(t) = (x_t - M) - log S,    H = log S - T / S.
 //
 // Both terms of H are non-negative, so a row that is almost certain keeps its small
-// entropy to fp32's absolute precision.  A wave keeps one running M; a part's sums
-// move to a new M as S' = r S, T' = r (T + d S), d = M - M', r = e^d.  x - M is
-// subtracted before anything is multiplied, so a common offset of the logits costs
-// nothing.  Sums are fp32, exponentials in base 2 (T in units of log 2).
+// entropy to fp32's absolute precision.  Exponents are taken in base 2 with one rounding,
+// y = fma(x, log2 e, -c), c = M log2 e as rounded: S, T (here sum 2^y y) and the given
+// token's y all refer to the same c, so its rounding, and with it a common offset of the
+// logits, cancels.  A wave keeps one running M; sums move to a new reference as S' = r S,
+// T' = r (T + d S), d = c - c', r = 2^d.  Sums are fp32.  Where |M| >= 2^126 (a row masked
+// with its type's lowest value throughout, say) M log2 e would overflow: values that
+// differ then differ by 2^102 or more, and y = 2^-90 (x - M) serves as well.
 //
 // Top tokens: a wave keeps its best 64 (value, index) pairs sorted, one per lane, and
 // a bound g; a vector whose maximum is at most g (all but a few, once the list has
@@ -26,28 +29,34 @@ namespace gptq {
 namespace {
 
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
-constexpr int kUnroll = 4;              // 16-byte vectors per lane and iteration
+constexpr int kUnroll = 2;              // 16-byte vectors per lane and iteration
 constexpr int kMaxTop = 64;
 constexpr int kMaxSplits = 128;
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
-constexpr float kFloor = -1e30f;        // stands for -inf in a product with e^-inf = 0
+constexpr float kFloor = -1e30f;        // stands for -inf in a product with 2^-inf = 0
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 
 struct F32 {
   typedef float elem;
   static constexpr int E = 4;           // elements of a 16-byte vector
+  static constexpr uint32_t kNone = 0xff800000u;      // a word of -inf
   static __device__ float one(elem x) { return x; }
+  static __device__ uint32_t word(elem x) { return __builtin_bit_cast(uint32_t, x); }   // x, then -inf
 };
 struct F16 {
   typedef uint16_t elem;
   static constexpr int E = 8;
+  static constexpr uint32_t kNone = 0xfc00fc00u;
   static __device__ float one(elem x) { return (float)__builtin_bit_cast(_Float16, x); }
+  static __device__ uint32_t word(elem x) { return (kNone & 0xffff0000u) | x; }
 };
 struct BF16 {
   typedef uint16_t elem;
   static constexpr int E = 8;
+  static constexpr uint32_t kNone = 0xff80ff80u;
   static __device__ float one(elem x) { return __builtin_bit_cast(float, (uint32_t)x << 16); }
+  static __device__ uint32_t word(elem x) { return (kNone & 0xffff0000u) | x; }
 };
 
 template <typename T>
@@ -87,91 +96,102 @@ __device__ __forceinline__ uint32_t lane_value(uint32_t v, int l) {
   return (uint32_t)__builtin_amdgcn_readlane((int)v, l);
 }
 
-// moves the sums from maximum m to maximum M
-__device__ __forceinline__ void rescale(float& s, float& t, float m, float M) {
-  if (!(m > -INFINITY)) return;         // nothing summed yet
-  const float d = fmaxf((m - M) * kLog2e, kFloor);   // finite also from a mask of the type's lowest value
+// the reference of a maximum: y = fma(x, scale, -c)
+struct Ref {
+  float m, scale, c;
+};
+__device__ __forceinline__ Ref make_ref(float m) {
+#pragma clang fp contract(off)      // c as rounded, wherever it is used
+  const float scale = fabsf(m) < 0x1p126f ? kLog2e : 0x1p-90f;
+  return Ref{m, scale, m * scale};
+}
+
+// moves sums from one reference to another of no smaller maximum
+__device__ __forceinline__ void rescale(float& s, float& t, const Ref& a, const Ref& b) {
+  if (!(a.m > -INFINITY)) return;         // nothing summed yet
+  const float d = a.scale == b.scale ? fmaxf(a.c - b.c, kFloor) : kFloor;   // no overflow in t below
   const float r = __builtin_amdgcn_exp2f(d);
   t = r * fmaf(d, s, t);
   s *= r;
 }
 
 struct Wave {
-  float m, s, t;        // s, t per lane; m of the wave
+  Ref ref;              // of the wave
+  float s, t;           // per lane
   float g;              // elements at or below g change neither m nor the list
   uint32_t gkey, key;   // key, idx: entry `lane` of the sorted list
   int idx;
 };
 
-template <bool TOP, int E>
-__device__ __forceinline__ void take(Wave& a, const float (&x)[E], int i0, bool valid, int top_k, int lane) {
-  float v = x[0];
-#pragma unroll
-  for (int e = 1; e < E; ++e) v = fmaximum(v, x[e]);
-  if (__any(!(v <= a.g))) {
-    if (__any(!(v <= a.m))) {
-      const float M = fmaximum(a.m, wave_maximum(v));
-      rescale(a.s, a.t, a.m, M);
-      a.m = M;
-    }
-    if constexpr (TOP) {
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        uint64_t todo = __ballot(valid && !(x[e] <= a.g));
-        while (todo) {
-          const int l = __builtin_ctzll(todo);
-          todo &= todo - 1;
-          const uint32_t k = key_of(__builtin_bit_cast(float, lane_value(__builtin_bit_cast(uint32_t, x[e]), l)));
-          const int i = (int)lane_value((uint32_t)i0, l) + e;
-          const int pos = __popcll(__ballot(a.key > k || (a.key == k && a.idx < i)));
-          if (pos >= top_k) continue;
-          const uint32_t pk = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)a.key, 0x138, 0xf, 0xf, false);
-          const int pi = __builtin_amdgcn_update_dpp(0, a.idx, 0x138, 0xf, 0xf, false);
-          a.key = lane < pos ? a.key : lane == pos ? k : pk;
-          a.idx = lane < pos ? a.idx : lane == pos ? i : pi;
-        }
-      }
-      a.gkey = max(a.gkey, lane_value(a.key, top_k - 1));
-      a.g = value_of(a.gkey);
-    } else {
-      a.g = a.m;
-    }
-  }
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const float d = fmaxf((x[e] - a.m) * kLog2e, kFloor);
-    const float p = __builtin_amdgcn_exp2f(d);
-    a.s += p;
-    a.t = fmaf(p, d, a.t);
-  }
-}
-
 struct Part {
   float m, s, t;
 };
 
-// outputs of one row from its joined sums; sorted: the row's top_k entries
+// the largest value below the one of a key (0: none); -0 is no value of its own
+__device__ __forceinline__ float value_below(uint32_t key) {
+  return value_of(key == 0u ? 0u : key == 0x80000000u ? 0x7ffffffeu : key - 1);
+}
+
+// puts the elements above g into the list.  x: a lane's elements, of which the first
+// `count` exist, from index i0 on
+template <int E>
+__device__ __forceinline__ void insert(Wave& a, const float (&x)[E], int count, int i0, int top_k, int lane) {
+  uint32_t mask = 0u;
+#pragma unroll
+  for (int e = 0; e < E; ++e) mask |= (e < count && !(x[e] <= a.g)) ? 1u << e : 0u;
+  while (__any(mask != 0u)) {          // each lane's next element ...
+    uint64_t todo = __ballot(mask != 0u);
+    const int e = mask ? __builtin_ctz(mask) : 0;
+    mask &= mask - 1;
+    float v = x[0];
+#pragma unroll
+    for (int j = 1; j < E; ++j) v = e == j ? x[j] : v;
+    const uint32_t vk = key_of(v);
+    while (todo) {                     // ... lane by lane
+      const int l = __builtin_ctzll(todo);
+      todo &= todo - 1;
+      const uint32_t k = lane_value(vk, l);
+      const int i = (int)lane_value((uint32_t)(i0 + e), l);
+      const int pos = __popcll(__ballot(a.key > k || (a.key == k && a.idx < i)));
+      if (pos >= top_k) continue;
+      const uint32_t pk = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)a.key, 0x138, 0xf, 0xf, false);
+      const int pi = __builtin_amdgcn_update_dpp(0, a.idx, 0x138, 0xf, 0xf, false);
+      a.key = lane < pos ? a.key : lane == pos ? k : pk;
+      a.idx = lane < pos ? a.idx : lane == pos ? i : pi;
+    }
+  }
+}
+
+// a list entry as one number: larger is better (the key, then the lower index)
+__device__ __forceinline__ uint64_t entry(uint32_t key, int idx) { return ((uint64_t)key << 32) | (uint32_t)~idx; }
+
+// outputs of one row from its joined sums; best: the row's entry t
 template <typename T>
-__device__ __forceinline__ void finish(const LogprobArgs& p, int64_t row, Part r, int t, const uint32_t* key,
-                                       const int* idx) {
-  const float log_s = logf(r.s);
+__device__ __forceinline__ void finish(const LogprobArgs& p, int64_t row, Part r, int t, uint64_t best) {
   const bool sound = fabsf(r.m) < INFINITY;      // neither empty nor with +inf or NaN
+  const Ref ref = make_ref(r.m);
+  const float log2_s = log2f(r.s);
+  const auto log_p = [&](float x) {
+    if (!sound) return NAN;
+    const float y = fmaf(x, ref.scale, -ref.c);
+    if (ref.scale != kLog2e || y < kFloor) return (x - r.m) - kLn2 * log2_s;     // beyond y's range, or -inf
+    return kLn2 * (y - log2_s);
+  };
   if (t < p.top_k) {
-    p.top_ids[row * p.top_k + t] = idx[t];
-    p.top_logprobs[row * p.top_k + t] = sound ? (value_of(key[t]) - r.m) - log_s : NAN;
+    p.top_ids[row * p.top_k + t] = ~(int)(uint32_t)best;
+    p.top_logprobs[row * p.top_k + t] = log_p(value_of((uint32_t)(best >> 32)));
   }
   if (t == 0) {
     const int64_t tok = p.tokens[row];
     float lp = 0.f;
     if (tok >= p.v) lp = NAN;
-    else if (tok >= 0)
-      lp = sound ? (T::one(((const typename T::elem*)p.logits)[row * p.ld + tok]) - r.m) - log_s : NAN;
+    else if (tok >= 0) lp = log_p(T::one(((const typename T::elem*)p.logits)[row * p.ld + tok]));
     p.logprobs[row] = lp;
-    p.entropy[row] = sound ? log_s - kLn2 * (r.t / r.s) : NAN;
+    p.entropy[row] = sound ? kLn2 * (log2_s - r.t / r.s) : NAN;
   }
 }
 
-// a part's record in the workspace: m, s, t, unused, then top_k keys and top_k indices
+// a part's record in the workspace: m, s, t, unused, then top_k list entries
 __host__ __device__ inline int64_t record_words(int top_k) { return 4 + 2 * top_k; }
 
 template <typename T, bool TOP>
@@ -179,10 +199,9 @@ __global__ __launch_bounds__(kThreads) void logprob_kernel(LogprobArgs p, int sp
                                                            uint32_t* __restrict__ ws) {
   constexpr int E = T::E;
   __shared__ float ps[kWaves][3];
-  __shared__ uint32_t key[kWaves][kMaxTop];
-  __shared__ int idx[kWaves][kMaxTop];
-  __shared__ uint32_t skey[kMaxTop];
-  __shared__ int sidx[kMaxTop];
+  __shared__ __attribute__((aligned(16))) uint64_t list[kWaves][kMaxTop];     // 0: no entry
+  __shared__ uint64_t sorted[kMaxTop];
+  __shared__ u32x4 found[TOP ? kWaves : 1][kUnroll][64];
   const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
   const int64_t row = blockIdx.x / splits;
   const int part = (int)(blockIdx.x % splits);
@@ -192,65 +211,89 @@ __global__ __launch_bounds__(kThreads) void logprob_kernel(LogprobArgs p, int sp
   const int head = min(v, (int)(((16 - ((uintptr_t)x & 15)) & 15) / sizeof(typename T::elem)));
   const int nvec = (v - head) / E, tail0 = head + nvec * E;
   const u32x4* xv = (const u32x4*)(x + head);
-  Wave a{-INFINITY, 0.f, 0.f, NAN, 0u, 0u, 0x7fffffff};
-  if constexpr (!TOP) a.g = -INFINITY;
-  if (part == 0 && w == 0 && head > 0) {
-    const float one[1] = {lane < head ? T::one(x[lane]) : -INFINITY};
-    take<TOP>(a, one, lane, lane < head, p.top_k, lane);
-  }
+  Wave a{make_ref(-INFINITY), 0.f, 0.f, TOP ? NAN : -INFINITY, 0u, 0u, 0x7fffffff};
   const int first = (int)min<int64_t>((int64_t)part * span, nvec), last = (int)min<int64_t>(first + span, nvec);
-  bool fresh = true;
-  for (int b = first + w * (64 * kUnroll); b < last; b += kWaves * 64 * kUnroll) {
-    u32x4 ld[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) ld[u] = xv[min(b + 64 * u + lane, last - 1)];
-    if (fresh) {
-      // the first loads' maximum, and a bound below which no element belongs to the top:
-      // the K-th largest lane maximum (at most M, so what g lets pass needs no new M)
-      fresh = false;
-      float lm = -INFINITY;
+  const int edges = head + v - tail0;
+  bool fresh = true, more = part == 0 && w == 0 && edges > 0;
+  for (int b = first + w * (64 * kUnroll); b < last || more; b += kWaves * 64 * kUnroll) {
+    u32x4 ld[kUnroll];          // elements that do not exist are -inf: they add nothing
+    const bool edge = b >= last;
+    if (!edge) {
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
-        float f[E];
-        unpack<T>(ld[u], f);
-        if (b + 64 * u + lane < last) {     // a lane past the end holds another lane's vector again
+        const int i = b + 64 * u + lane;
+        ld[u] = xv[min(i, last - 1)];
+        if (i >= last) ld[u] = u32x4{T::kNone, T::kNone, T::kNone, T::kNone};
+      }
+    } else {
+      // what lies outside whole vectors comes last, one element to a lane; some have a
+      // lower index than those before, so they pass at g too
+      more = false;
 #pragma unroll
-          for (int e = 0; e < E; ++e) lm = fmaximum(lm, f[e]);
-        }
-      }
-      const float M = fmaximum(a.m, wave_maximum(lm));
-      rescale(a.s, a.t, a.m, M);
-      a.m = M;
-      if constexpr (TOP) {
-        const uint32_t lk = b + lane < last ? key_of(lm) : 0u;
-        uint32_t bound = 0u;
-#pragma unroll 1
-        for (uint32_t bit = 0x80000000u; bit >= 0x1000u; bit >>= 1)
-          if (__popcll(__ballot(lk >= (bound | bit))) >= p.top_k) bound |= bit;
-        // the largest key below the bound; -0 is no key of its own
-        if (bound) bound = bound == 0x80000000u ? 0x7ffffffeu : bound - 1;
-        a.gkey = max(a.gkey, bound);
-        a.g = value_of(a.gkey);
-      } else {
-        a.g = M;
-      }
+      for (int u = 0; u < kUnroll; ++u) ld[u] = u32x4{T::kNone, T::kNone, T::kNone, T::kNone};
+      if (lane < edges) ld[0][0] = T::word(x[lane < head ? lane : tail0 + lane - head]);
+      if (TOP && !fresh) a.g = value_below(a.gkey);
     }
+    float f[kUnroll][E], lm = -INFINITY;
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int i = b + 64 * u + lane;
-      float f[E];
-      unpack<T>(ld[u], f);
-      if (i >= last) {
+      unpack<T>(ld[u], f[u]);
 #pragma unroll
-        for (int e = 0; e < E; ++e) f[e] = -INFINITY;
-      }
-      take<TOP>(a, f, head + i * E, i < last, p.top_k, lane);
+      for (int e = 0; e < E; ++e) lm = fmaximum(lm, f[u][e]);
     }
-  }
-  if (part == 0 && w == 0 && tail0 < v) {
-    const bool has = tail0 + lane < v;
-    const float one[1] = {has ? T::one(x[tail0 + lane]) : -INFINITY};
-    take<TOP>(a, one, tail0 + lane, has, p.top_k, lane);
+    if (__any(!(lm <= a.g))) {
+      if (__any(!(lm <= a.ref.m))) {
+        const Ref next = make_ref(fmaximum(a.ref.m, wave_maximum(lm)));
+        rescale(a.s, a.t, a.ref, next);
+        a.ref = next;
+      }
+      if constexpr (TOP) {
+        if (fresh) {
+          // a bound below which no element belongs to the top: the K-th largest lane
+          // maximum, to its upper 20 bits
+          const uint32_t lk = (edge ? lane < edges : b + lane < last) ? key_of(lm) : 0u;
+          uint32_t bound = 0u;
+#pragma unroll 1
+          for (uint32_t bit = 0x80000000u; bit >= 0x1000u; bit >>= 1)
+            if (__popcll(__ballot(lk >= (bound | bit))) >= p.top_k) bound |= bit;
+          a.g = value_below(bound);
+        }
+        // through LDS, so that the rare path is one piece of code for all vectors
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) found[w][u][lane] = ld[u];
+#pragma unroll 1
+        for (int u = 0; u < kUnroll; ++u) {
+          const int i = b + 64 * u + lane;
+          float z[E];
+          unpack<T>(found[w][u][lane], z);
+          const int n = edge ? (u == 0 && lane < edges ? 1 : 0) : (i < last ? E : 0);
+          const int i0 = !edge ? head + i * E : lane < head ? lane : tail0 + lane - head;
+          insert<E>(a, z, n, i0, p.top_k, lane);
+        }
+        a.gkey = lane_value(a.key, p.top_k - 1);
+        const float kth = value_of(a.gkey);
+        // the first loads' bound stays until the list has filled
+        a.g = a.gkey != 0u ? kth : a.g;
+      } else {
+        a.g = a.ref.m;
+      }
+      // unpacked anew: kept over this path, the elements would cost registers and so waves
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        asm volatile("" : "+v"(ld[u]));
+        unpack<T>(ld[u], f[u]);
+      }
+    }
+    fresh = false;
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float y = fmaxf(fmaf(f[u][e], a.ref.scale, -a.ref.c), kFloor);
+        const float q = __builtin_amdgcn_exp2f(y);
+        a.s += q;
+        a.t = fmaf(q, y, a.t);
+      }
   }
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) {
@@ -258,17 +301,14 @@ __global__ __launch_bounds__(kThreads) void logprob_kernel(LogprobArgs p, int sp
     a.t += __shfl_xor(a.t, o, 64);
   }
   if (lane == 0) {
-    ps[w][0] = a.m;
+    ps[w][0] = a.ref.m;
     ps[w][1] = a.s;
     ps[w][2] = a.t;
   }
-  if (TOP && lane < p.top_k) {
-    key[w][lane] = a.key;
-    idx[w][lane] = a.idx;
-    if (w == 0) {
-      skey[lane] = 0u;
-      sidx[lane] = 0x7fffffff;
-    }
+  const uint64_t mine = entry(a.key, a.idx);
+  if (TOP) {
+    list[w][lane] = lane < p.top_k ? mine : 0u;
+    if (w == 0) sorted[lane] = 0u;
   }
   __syncthreads();
   Part r{ps[0][0], 0.f, 0.f};
@@ -277,7 +317,7 @@ __global__ __launch_bounds__(kThreads) void logprob_kernel(LogprobArgs p, int sp
 #pragma unroll
   for (int i = 0; i < kWaves; ++i) {
     float s = ps[i][1], q = ps[i][2];
-    rescale(s, q, ps[i][0], r.m);
+    rescale(s, q, make_ref(ps[i][0]), make_ref(r.m));
     r.s += s;
     r.t += q;
   }
@@ -285,20 +325,18 @@ __global__ __launch_bounds__(kThreads) void logprob_kernel(LogprobArgs p, int sp
     // an entry's place among the waves' lists is the number of better ones
     if (lane < p.top_k && a.key != 0u) {
       int rank = 0;
-      for (int i = 0; i < kWaves; ++i)
-        for (int j = 0; j < p.top_k; ++j) {
-          const uint32_t k = key[i][j];
-          rank += k > a.key || (k == a.key && idx[i][j] < a.idx);
-        }
-      if (rank < p.top_k) {
-        skey[rank] = a.key;
-        sidx[rank] = a.idx;
-      }
+#pragma unroll 1
+      for (int j = 0; j < p.top_k; j += 2)
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) rank += list[i][j + e] > mine;
+      if (rank < p.top_k) sorted[rank] = mine;
     }
     __syncthreads();
   }
   if (splits == 1) {
-    finish<T>(p, row, r, t, skey, sidx);
+    finish<T>(p, row, r, t, t < p.top_k ? sorted[t] : 0u);
     return;
   }
   uint32_t* rec = ws + (int64_t)blockIdx.x * record_words(p.top_k);
@@ -308,80 +346,90 @@ __global__ __launch_bounds__(kThreads) void logprob_kernel(LogprobArgs p, int sp
     rec[2] = __builtin_bit_cast(uint32_t, r.t);
   }
   if (t < p.top_k) {
-    rec[4 + t] = skey[t];
-    rec[4 + p.top_k + t] = (uint32_t)sidx[t];
+    ((uint64_t*)rec)[2 + t] = sorted[t];
   }
 }
 
-// one row per work-group: sums joined in the order of the parts; the top tokens by
-// taking the best head of the parts' sorted lists top_k times (wave 0, two lists a lane)
+// one row per work-group: wave 0 joins the sums.  The top: among the first `depth`
+// entries of every part's list, the one with top_k - 1 better ones is a bound; the
+// entries at or above it (at most top_k + top_k^2 / depth: a list with more than depth
+// of them has all its first ones there) are gathered, and an entry's place is the number
+// of better ones among them.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void logprob_join_kernel(LogprobArgs p, int splits,
                                                                 const uint32_t* __restrict__ ws) {
-  extern __shared__ uint32_t lists[];      // [splits][2 top_k]
-  __shared__ uint32_t skey[kMaxTop];
-  __shared__ int sidx[kMaxTop];
+  extern __shared__ uint64_t cand[];       // [splits * top_k]
+  __shared__ uint64_t first[kMaxSplits + 2 * kMaxTop];
+  __shared__ uint64_t sorted[kMaxTop];
+  __shared__ uint64_t bound;
+  __shared__ int count;
   const int t = threadIdx.x, lane = t & 63, K = p.top_k;
   const int64_t row = blockIdx.x, words = record_words(K);
   const uint32_t* rec = ws + row * splits * words;
-  for (int i = t; i < splits * 2 * K; i += kThreads) lists[i] = rec[(i / (2 * K)) * words + 4 + i % (2 * K)];
-  __syncthreads();
-  if (t >= 64) return;
   Part r{-INFINITY, 0.f, 0.f};
-  Part own[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int i = lane + 64 * h;
-    own[h] = Part{-INFINITY, 0.f, 0.f};
-    if (i < splits) {
-      const uint32_t* q = rec + i * words;
-      own[h] = Part{__builtin_bit_cast(float, q[0]), __builtin_bit_cast(float, q[1]), __builtin_bit_cast(float, q[2])};
-    }
-    r.m = fmaximum(r.m, own[h].m);
-  }
-  r.m = wave_maximum(r.m);
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    rescale(own[h].s, own[h].t, own[h].m, r.m);
-    r.s += own[h].s;
-    r.t += own[h].t;
-  }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    r.s += __shfl_xor(r.s, o, 64);
-    r.t += __shfl_xor(r.t, o, 64);
-  }
-  int at[2] = {0, 0};
-  for (int j = 0; j < K; ++j) {
-    uint64_t best = 0;
-    int from = 0;
+  if (t < 64) {
+    Part own[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int i = lane + 64 * h;
-      if (i < splits && at[h] < K) {
-        const uint32_t* l = lists + i * 2 * K + at[h];
-        const uint64_t c = ((uint64_t)l[0] << 32) | (0xffffffffu - l[K]);
-        if (c > best) {
-          best = c;
-          from = h;
-        }
+      own[h] = Part{-INFINITY, 0.f, 0.f};
+      if (i < splits) {
+        const uint32_t* q = rec + i * words;
+        own[h] = Part{__builtin_bit_cast(float, q[0]), __builtin_bit_cast(float, q[1]), __builtin_bit_cast(float, q[2])};
       }
+      r.m = fmaximum(r.m, own[h].m);
     }
-    uint64_t top = best;
+    r.m = wave_maximum(r.m);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      rescale(own[h].s, own[h].t, make_ref(own[h].m), make_ref(r.m));
+      r.s += own[h].s;
+      r.t += own[h].t;
+    }
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) {
-      const uint64_t c = ((uint64_t)(uint32_t)__shfl_xor((int)(top >> 32), o, 64) << 32) |
-                         (uint32_t)__shfl_xor((int)(uint32_t)top, o, 64);
-      top = max(top, c);
-    }
-    if (best == top) ++at[from];       // one lane: indices differ
-    if (lane == j) {
-      skey[j] = (uint32_t)(top >> 32);
-      sidx[j] = (int)(0xffffffffu - (uint32_t)top);
+      r.s += __shfl_xor(r.s, o, 64);
+      r.t += __shfl_xor(r.t, o, 64);
     }
   }
-  __builtin_amdgcn_wave_barrier();
-  finish<T>(p, row, r, t, skey, sidx);
+  uint64_t place = 0u;
+  if (K > 0) {
+    const auto at = [&](int i, int j) { return ((const uint64_t*)(rec + i * words))[2 + j]; };
+    const int depth = max(1, min(K, (2 * K + splits - 1) / splits)), some = splits * depth;
+    for (int i = t; i < some; i += kThreads) first[i] = at(i % splits, i / splits);
+    if (t < kMaxTop) sorted[t] = 0u;
+    if (t == 0) {
+      count = 0;
+      bound = 0u;
+    }
+    __syncthreads();
+    for (int i = t; i < some; i += kThreads) {
+      const uint64_t e = first[i];
+      int rank = 0;
+#pragma unroll 8
+      for (int j = 0; j < some; ++j) rank += first[j] > e;
+      if (rank == K - 1 && e != 0u) bound = e;        // one entry: they differ
+    }
+    __syncthreads();
+    const uint64_t least = bound;
+    for (int i = t >> 6; i < splits; i += kWaves)
+      if (lane < K) {
+        const uint64_t e = at(i, lane);
+        if (e >= least && e != 0u) cand[atomicAdd(&count, 1)] = e;
+      }
+    __syncthreads();
+    const int n = count;
+    for (int i = t; i < n; i += kThreads) {
+      const uint64_t e = cand[i];
+      int rank = 0;
+#pragma unroll 8
+      for (int j = 0; j < n; ++j) rank += cand[j] > e;
+      if (rank < K) sorted[rank] = e;
+    }
+    __syncthreads();
+    if (t < K) place = sorted[t];
+  }
+  if (t < 64) finish<T>(p, row, r, t, place);
 }
 
 template <typename T>
@@ -391,7 +439,7 @@ hipError_t launch(const LogprobPlan& plan, const LogprobArgs& p, uint32_t* ws, h
   if (p.top_k > 0) logprob_kernel<T, true><<<grid, kThreads, 0, s>>>(p, plan.splits, span, ws);
   else logprob_kernel<T, false><<<grid, kThreads, 0, s>>>(p, plan.splits, span, ws);
   if (plan.splits > 1)
-    logprob_join_kernel<T><<<dim3((unsigned)p.n), kThreads, (size_t)plan.splits * 2 * p.top_k * 4, s>>>(p, plan.splits, ws);
+    logprob_join_kernel<T><<<dim3((unsigned)p.n), kThreads, (size_t)plan.splits * p.top_k * 8, s>>>(p, plan.splits, ws);
   return hipGetLastError();
 }
 

@@ -65,6 +65,12 @@ def make(n, v, seed, dtype, kind="normal"):
         x[torch.arange(n), torch.randint(0, v, (n,), generator=g)] = 60.0
     elif kind == "ends":                    # the best ones at the row's two ends
         x[:, 0], x[:, -1], x[:, v // 2] = 30.0, 30.0, 29.0
+    elif kind == "all_lowest":
+        x = torch.full((n, v), torch.finfo(TYPES[dtype]).min)
+        x[0, v // 3] = 1.0
+    elif kind == "all_largest":
+        x = torch.full((n, v), torch.finfo(TYPES[dtype]).max)
+        x[:, ::2] = 5.0
     elif kind == "lowest":                  # masked with the type's lowest value
         x[torch.rand(n, v, generator=g) < 0.5] = torch.finfo(TYPES[dtype]).min
     tok = torch.randint(0, v, (n,), generator=g)
@@ -74,7 +80,8 @@ def make(n, v, seed, dtype, kind="normal"):
 CASES = [(1, 1, 1, "normal"), (3, 2, 2, "normal"), (2, 7, 0, "normal"), (5, 63, 20, "normal"), (4, 64, 64, "coarse"),
          (2, 100, 64, "masked"), (3, 513, 5, "sharp"), (2, 2049, 20, "ends"), (1, 4097, 1, "coarse"), (3, 5000, 20, "equal"),
          (2, 9001, 33, "ascending"), (1, 20011, 20, "masked"), (2, 30000, 64, "shifted"), (1100, 300, 5, "normal"),
-         (1030, 2500, 20, "coarse"), (7, 12345, 0, "lowest"), (2, 6000, 7, "lowest"), (1, 131072, 20, "normal")]
+         (1030, 2500, 20, "coarse"), (7, 12345, 0, "lowest"), (2, 6000, 7, "lowest"), (4, 5001, 3, "all_lowest"), (3, 3000, 2, "all_largest"),
+         (9, 260, 1, "masked"), (1500, 77, 77 - 20, "coarse"), (3, 70000, 64, "ascending"), (4, 8200, 64, "equal"), (1, 131072, 20, "normal")]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
@@ -106,7 +113,9 @@ def test_rows_without_a_softmax(v, dtype):
     got = G.gptq_token_logprobs(x.cuda(), tok.cuda(), 20)
     torch.cuda.synchronize()
     check(x, tok, 20, got)
-    assert got[0][4] == 0.0 and got[1][4] == 0.0 and got[0][5] == 0.0
+    # one token left: S is its own 2^y, |y| <= half a step of M log2 e < 2^-20, off by 2 u;
+    # log2 S then by 3 u, T / S by u |y|: log p and the entropy are within 4 u of 0
+    assert abs(got[0][4]) <= 4 * U32 and abs(got[1][4]) <= 4 * U32 and got[0][5] == 0.0
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
