@@ -165,9 +165,20 @@ __device__ __forceinline__ void insert(Wave& a, const float (&x)[E], int count, 
 // a list entry as one number: larger is better (the key, then the lower index)
 __device__ __forceinline__ uint64_t entry(uint32_t key, int idx) { return ((uint64_t)key << 32) | (uint32_t)~idx; }
 
-// outputs of one row from its joined sums; best: the row's entry t
+// the given token of a row and its logit (0 where there is none)
+struct Given {
+  int64_t token;
+  float x;
+};
 template <typename T>
-__device__ __forceinline__ void finish(const LogprobArgs& p, int64_t row, Part r, int t, uint64_t best) {
+__device__ __forceinline__ Given given_token(const LogprobArgs& p, int64_t row) {
+  Given g{p.tokens[row], 0.f};
+  if (g.token >= 0 && g.token < p.v) g.x = T::one(((const typename T::elem*)p.logits)[row * p.ld + g.token]);
+  return g;
+}
+
+// outputs of one row from its joined sums; best: the row's entry t
+__device__ __forceinline__ void finish(const LogprobArgs& p, int64_t row, Part r, Given given, int t, uint64_t best) {
   const bool sound = fabsf(r.m) < INFINITY;      // neither empty nor with +inf or NaN
   const Ref ref = make_ref(r.m);
   const float log2_s = log2f(r.s);
@@ -182,11 +193,7 @@ __device__ __forceinline__ void finish(const LogprobArgs& p, int64_t row, Part r
     p.top_logprobs[row * p.top_k + t] = log_p(value_of((uint32_t)(best >> 32)));
   }
   if (t == 0) {
-    const int64_t tok = p.tokens[row];
-    float lp = 0.f;
-    if (tok >= p.v) lp = NAN;
-    else if (tok >= 0) lp = log_p(T::one(((const typename T::elem*)p.logits)[row * p.ld + tok]));
-    p.logprobs[row] = lp;
+    p.logprobs[row] = given.token < 0 ? 0.f : given.token >= p.v ? NAN : log_p(given.x);
     p.entropy[row] = sound ? kLn2 * (log2_s - r.t / r.s) : NAN;
   }
 }
@@ -222,7 +229,7 @@ __global__ __launch_bounds__(kThreads) void logprob_kernel(LogprobArgs p, int sp
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         const int i = b + 64 * u + lane;
-        ld[u] = xv[min(i, last - 1)];
+        ld[u] = __builtin_nontemporal_load(&xv[min(i, last - 1)]);      // read once
         if (i >= last) ld[u] = u32x4{T::kNone, T::kNone, T::kNone, T::kNone};
       }
     } else {
@@ -336,7 +343,7 @@ __global__ __launch_bounds__(kThreads) void logprob_kernel(LogprobArgs p, int sp
     __syncthreads();
   }
   if (splits == 1) {
-    finish<T>(p, row, r, t, t < p.top_k ? sorted[t] : 0u);
+    finish(p, row, r, given_token<T>(p, row), t, t < p.top_k ? sorted[t] : 0u);
     return;
   }
   uint32_t* rec = ws + (int64_t)blockIdx.x * record_words(p.top_k);
@@ -358,16 +365,28 @@ __global__ __launch_bounds__(kThreads) void logprob_kernel(LogprobArgs p, int sp
 template <typename T>
 __global__ __launch_bounds__(kThreads) void logprob_join_kernel(LogprobArgs p, int splits,
                                                                 const uint32_t* __restrict__ ws) {
-  extern __shared__ uint64_t cand[];       // [splits * top_k]
-  __shared__ uint64_t first[kMaxSplits + 2 * kMaxTop];
+  extern __shared__ uint64_t lists[];      // [splits][top_k], then the entries gathered from them
   __shared__ uint64_t sorted[kMaxTop];
   __shared__ uint64_t bound;
   __shared__ int count;
   const int t = threadIdx.x, lane = t & 63, K = p.top_k;
   const int64_t row = blockIdx.x, words = record_words(K);
   const uint32_t* rec = ws + row * splits * words;
+  for (int i = t; i < splits * K; i += 8 * kThreads) {      // eight loads at a time
+    uint64_t e[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const uint32_t at = i + u * kThreads, l = at / (uint32_t)K;
+      e[u] = at < (uint32_t)(splits * K) ? ((const uint64_t*)(rec + l * words))[2 + at - l * K] : 0u;
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (i + u * kThreads < splits * K) lists[i + u * kThreads] = e[u];
+  }
   Part r{-INFINITY, 0.f, 0.f};
+  Given given{-1, 0.f};
   if (t < 64) {
+    given = given_token<T>(p, row);
     Part own[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -394,9 +413,8 @@ __global__ __launch_bounds__(kThreads) void logprob_join_kernel(LogprobArgs p, i
   }
   uint64_t place = 0u;
   if (K > 0) {
-    const auto at = [&](int i, int j) { return ((const uint64_t*)(rec + i * words))[2 + j]; };
     const int depth = max(1, min(K, (2 * K + splits - 1) / splits)), some = splits * depth;
-    for (int i = t; i < some; i += kThreads) first[i] = at(i % splits, i / splits);
+    uint64_t* const cand = lists + splits * K;
     if (t < kMaxTop) sorted[t] = 0u;
     if (t == 0) {
       count = 0;
@@ -404,19 +422,19 @@ __global__ __launch_bounds__(kThreads) void logprob_join_kernel(LogprobArgs p, i
     }
     __syncthreads();
     for (int i = t; i < some; i += kThreads) {
-      const uint64_t e = first[i];
+      const uint64_t e = lists[(i % splits) * K + i / splits];
       int rank = 0;
+      for (int d = 0; d < depth; ++d)
 #pragma unroll 8
-      for (int j = 0; j < some; ++j) rank += first[j] > e;
+        for (int j = 0; j < splits; ++j) rank += lists[j * K + d] > e;
       if (rank == K - 1 && e != 0u) bound = e;        // one entry: they differ
     }
     __syncthreads();
     const uint64_t least = bound;
-    for (int i = t >> 6; i < splits; i += kWaves)
-      if (lane < K) {
-        const uint64_t e = at(i, lane);
-        if (e >= least && e != 0u) cand[atomicAdd(&count, 1)] = e;
-      }
+    for (int i = t; i < splits * K; i += kThreads) {
+      const uint64_t e = lists[i];
+      if (e >= least && e != 0u) cand[atomicAdd(&count, 1)] = e;
+    }
     __syncthreads();
     const int n = count;
     for (int i = t; i < n; i += kThreads) {
@@ -429,7 +447,7 @@ __global__ __launch_bounds__(kThreads) void logprob_join_kernel(LogprobArgs p, i
     __syncthreads();
     if (t < K) place = sorted[t];
   }
-  if (t < 64) finish<T>(p, row, r, t, place);
+  if (t < 64) finish(p, row, r, given, t, place);
 }
 
 template <typename T>
@@ -439,7 +457,7 @@ hipError_t launch(const LogprobPlan& plan, const LogprobArgs& p, uint32_t* ws, h
   if (p.top_k > 0) logprob_kernel<T, true><<<grid, kThreads, 0, s>>>(p, plan.splits, span, ws);
   else logprob_kernel<T, false><<<grid, kThreads, 0, s>>>(p, plan.splits, span, ws);
   if (plan.splits > 1)
-    logprob_join_kernel<T><<<dim3((unsigned)p.n), kThreads, (size_t)plan.splits * p.top_k * 8, s>>>(p, plan.splits, ws);
+    logprob_join_kernel<T><<<dim3((unsigned)p.n), kThreads, (size_t)plan.splits * p.top_k * 16, s>>>(p, plan.splits, ws);
   return hipGetLastError();
 }
 
