@@ -18,14 +18,24 @@ act-order forms), and What written back into the layer's weight
 weights whose outputs are the next block's inputs.  Every quantizer step runs in
 the library's kernels on the current stream; the forward passes are the caller's
 model.  Biases are left as they are.
+
+Beside it, without calibration: ``quantize_model_fp8`` puts an ``Fp8Linear`` in the place
+of every nn.Linear (e4m3 weights in 128 x 128 tiles, inputs quantized per row on every
+call).  ``evaluate`` judges a model, quantized or not, on given texts: mean negative log
+probability and perplexity (the pages' loss and perplexity before and after), entropy,
+and how often the given token was the most probable one.
 """
 from __future__ import annotations
 
 import dataclasses
+import math
 from typing import Dict, List, Optional, Sequence
 
-from . import (NotPositiveDefinite, _torch, gptq_act_order_perm, gptq_dequantize, gptq_hessian_accumulate,
-               gptq_prepare_hinv, gptq_prepare_hinv_perm, gptq_quantize_layer, gptq_quantize_layer_perm)
+import torch as _t
+
+from . import (NotPositiveDefinite, _torch, gptq_act_order_perm, gptq_dequantize, gptq_fp8_matmul, gptq_fp8_quantize,
+               gptq_hessian_accumulate, gptq_prepare_hinv, gptq_prepare_hinv_perm, gptq_quantize_layer,
+               gptq_quantize_layer_perm, gptq_token_logprobs)
 
 
 @dataclasses.dataclass
@@ -117,3 +127,102 @@ def quantize_model(blocks: Sequence, x_batches: Sequence, bits: int, group_size:
             results.append(BlockQuant(layers, xs if keep_inputs else None))
             xs = [block(x) for x in xs] if sequential else ys
     return results, xs
+
+
+class Fp8Linear(_t.nn.Module):
+    """A linear layer with e4m3 weights: y = dequantized(x) dequantized(W)^T + bias in
+    x's dtype (fp32, fp16 or bf16), x's rows quantized on every call.  For inference:
+    inputs that ask for a gradient are refused."""
+
+    def __init__(self, weight, bias=None):
+        super().__init__()
+        self.out_features, self.in_features = weight.shape
+        codes, scales = gptq_fp8_quantize(weight.detach(), 128)
+        self.register_buffer("codes", codes.view(_t.uint8))      # bit patterns: a cast of the model leaves them alone
+        self.register_buffer("scales", scales)
+        self.register_buffer("bias", None if bias is None else bias.detach().clone())
+
+    def _apply(self, fn, recurse=True):
+        scales = self.scales
+        super()._apply(fn, recurse)
+        if self.scales.dtype != scales.dtype:       # model.half() and the like: the scales stay fp32
+            self.scales = scales.to(self.scales.device)
+        return self
+
+    def forward(self, x):
+        if x.requires_grad and _t.is_grad_enabled():
+            raise ValueError("Fp8Linear has no backward pass: detach its input or call it under torch.no_grad()")
+        rows = x.reshape(-1, self.in_features)
+        codes, scales = gptq_fp8_quantize(rows if rows.stride(-1) == 1 else rows.contiguous())
+        bias = self.bias if self.bias is None or self.bias.dtype == x.dtype else self.bias.to(x.dtype)
+        y = gptq_fp8_matmul(codes, scales, self.codes, self.scales, bias, out_dtype=x.dtype)
+        return y.reshape(*x.shape[:-1], self.out_features)
+
+    def extra_repr(self) -> str:
+        return f"in_features={self.in_features}, out_features={self.out_features}, bias={self.bias is not None}"
+
+
+def quantize_model_fp8(blocks: Sequence) -> List[List[str]]:
+    """Put an Fp8Linear in the place of every nn.Linear of ``blocks`` (torch modules on
+    the GPU), in place.  A layer used under several names stays one layer.  Returns the
+    names of the replaced layers, block by block."""
+    names, made = [], {}
+    for block in blocks:
+        if isinstance(block, _t.nn.Linear):
+            raise ValueError("a block that is itself a Linear cannot be replaced in place: use Fp8Linear")
+        names.append([])
+        for parent_name, parent in list(block.named_modules()):
+            for name, child in list(parent._modules.items()):     # under every name, a shared layer's too
+                if isinstance(child, _t.nn.Linear):
+                    if id(child) not in made:
+                        made[id(child)] = (child, Fp8Linear(child.weight, child.bias))
+                    setattr(parent, name, made[id(child)][1])
+                    names[-1].append(f"{parent_name}.{name}" if parent_name else name)
+    return names
+
+
+@dataclasses.dataclass
+class Evaluation:
+    tokens: int              # judged positions (those with a token >= 0)
+    nll: float               # mean negative log probability of the given tokens, in nats
+    perplexity: float        # e^nll
+    entropy: float           # mean entropy of the model's distributions there, in nats
+    accuracy: float          # share of positions whose most probable token is the given one
+
+
+def evaluate(blocks: Sequence, head, x_batches: Sequence, token_batches: Sequence,
+             rows_per_call: int = 8192) -> Evaluation:
+    """Judge a model on given texts.  ``blocks`` map each batch of ``x_batches`` [S x T x d]
+    on, ``head`` (an nn.Linear, an Fp8Linear, any module) maps hidden rows [rows x d] to
+    logits [rows x v] (fp32, fp16 or bf16); ``token_batches`` hold the tokens to be
+    predicted there, int64 [S x T], negative where there is none (padding, a text's last
+    position).  The head and the judgement run on at most ``rows_per_call`` rows at a time."""
+    if len(x_batches) != len(token_batches):
+        raise ValueError("x_batches and token_batches differ in number")
+    if rows_per_call < 1:
+        raise ValueError("rows_per_call must be at least 1")
+    sums = None
+    with _t.no_grad():
+        for x, tokens in zip(x_batches, token_batches):
+            if tokens.shape != x.shape[:-1]:
+                raise ValueError(f"tokens of shape {tuple(tokens.shape)} for a batch of shape {tuple(x.shape)}")
+            for block in blocks:
+                x = block(x)
+            hidden, tok = x.reshape(-1, x.shape[-1]), tokens.reshape(-1).contiguous()
+            if sums is None:
+                sums = _t.zeros(4, dtype=_t.float64, device=x.device)
+            for i in range(0, hidden.shape[0], rows_per_call):
+                t = tok[i:i + rows_per_call]
+                logits = head(hidden[i:i + rows_per_call])
+                if bool((t >= logits.shape[1]).any()):
+                    raise ValueError(f"a token is not below the {logits.shape[1]} logits")
+                lp, entropy, ids, _ = gptq_token_logprobs(logits, t, 1)
+                judged = t >= 0
+                sums += _t.stack([judged.sum().double(), lp.double().sum(),
+                                  entropy.double().masked_fill(~judged, 0.0).sum(),
+                                  ((ids[:, 0] == t) & judged).sum().double()])
+    n, lp, entropy, hits = (0.0, 0.0, 0.0, 0.0) if sums is None else sums.tolist()
+    if n == 0:
+        raise ValueError("no position holds a token to be judged")
+    nll = -lp / n
+    return Evaluation(int(n), nll, math.exp(nll) if nll < 700 else math.inf, entropy / n, hits / n)
