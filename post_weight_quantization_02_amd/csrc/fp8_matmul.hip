@@ -501,14 +501,25 @@ __global__ __launch_bounds__(64 * WT * WN * WK) __attribute__((amdgpu_waves_per_
       asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S - 2) * kLoads) : "memory");
       const float sw = sw_next;
       sw_next = swp[next(step + 1)];
-      fetch(std::integral_constant<int, to>{}, next(step + S - 1));
+      const int b = next(step + S - 1);
       ++step;
-      if (!has) return;
+      if (!has) return;           // nothing follows: nothing to fetch
+      // the largest tiles issue their loads beside the first half of the products (prompt
+      // case 181 -> 178 us); for the others that is too late (1024 x 4096 x 4096: 24.2 -> 25.8)
+      constexpr int kSpread = TT == 8 ? TT / 2 : 0;
+      if constexpr (kSpread == 0) fetch(std::integral_constant<int, to>{}, b);
       i32x8 wv[TN];
 #pragma unroll
       for (int a = 0; a < TN; ++a) wv[a] = pick(stage_w<BN, WK, h>()[g].w, w0, w1, a);
       multiply(wv, [&](int c) { return pick(s.x, x0, x1, c); }, [&](int c) { return s.sx[sx0 + 16 * c]; }, sw,
-               [](int) {});
+               [&](int c) {
+#pragma unroll
+                 for (int l = 0; l < kLoads; ++l)
+                   if (kSpread > 0 && l * kSpread / kLoads == c) {
+                     if (l <= kXLoads) fetch_x(stage_x<BT, WK, to>()[g], b, l);
+                     else fetch_w(stage_w<BN, WK, to>()[g], b, l - kXLoads - 1);
+                   }
+               });
     });
   } else {
     static_assert(S % 2 == 0, "two sets of registers in turn");
