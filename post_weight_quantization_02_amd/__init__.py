@@ -216,17 +216,18 @@ def _elem_code(t, name) -> int:
 def _expect(t, name, shape, dtypes, device):
     """A tensor of that shape and one of those dtypes on that device, its last
     dimension contiguous and its rows not overlapping."""
+    if t.shape == shape and t.dtype in dtypes and t.device == device and t.is_contiguous():
+        return
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: unsupported dtype {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
-    if not t.is_contiguous():
-        if shape[-1] > 1 and t.stride(-1) != 1:
-            raise ValueError(f"{name} must have unit stride in its last dimension")
-        if len(shape) == 2 and shape[0] > 1 and t.stride(0) < shape[1]:
-            raise ValueError(f"{name} has overlapping rows")
+    if shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have unit stride in its last dimension")
+    if len(shape) == 2 and shape[0] > 1 and t.stride(0) < shape[1]:
+        raise ValueError(f"{name} has overlapping rows")
 
 
 def _grad_error(where):
@@ -236,13 +237,14 @@ def _grad_error(where):
 def _launch(torch, device, stream, fn, args, tensors, where):
     """fn(*args, stream handle) on ``device``: on its current stream, or on ``stream``,
     which has to belong to it (ordered as in _stream)."""
-    if stream is not None and stream.device != device:
-        raise ValueError(f"{where}: the stream belongs to {stream.device}, the tensors to {device}")
-    if device.index != torch.cuda.current_device():
+    index = device.index
+    if index != torch._C._cuda_getDevice():
         with torch.cuda.device(device):
             return _launch(torch, device, stream, fn, args, tensors, where)
     if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(device.index)     # current_stream() without the Python object
+        handle = torch._C._cuda_getCurrentRawStream(index)     # current_stream() without the Python object
+    elif stream.device != device:
+        raise ValueError(f"{where}: the stream belongs to {stream.device}, the tensors to {device}")
     else:
         handle = _stream(stream, *tensors)
     status = fn(*args, handle)
@@ -511,21 +513,24 @@ def gptq_fp8_quantize(X, block_rows: int = 1, codes=None, scales=None, stream=No
     code = _elem_code(X, "X")
     m, k = X.shape
     dev = X.device
-    kb = -(-k // 128)
-    shape = (kb, m) if block_rows == 1 else (-(-m // 128), kb)
+    kb = (k + 127) // 128
+    rows, cols = (kb, m) if block_rows == 1 else ((m + 127) // 128, kb)
     if codes is None:
-        codes = torch.empty((m, kb * 128), dtype=torch.float8_e4m3fn, device=dev)
-        if k != kb * 128:
+        ldc = kb * 128
+        codes = torch.empty(m, ldc, dtype=torch.float8_e4m3fn, device=dev)
+        if k != ldc:
             codes = codes[:, :k]
     else:
         _expect(codes, "codes", (m, k), (torch.float8_e4m3fn, torch.uint8), dev)
+        ldc = _pitch(codes)
     if scales is None:
-        scales = torch.empty(shape, dtype=torch.float32, device=dev)
+        scales, lds = torch.empty(rows, cols, dtype=torch.float32, device=dev), max(cols, 1)
     else:
-        _expect(scales, "scales", shape, (torch.float32,), dev)
+        _expect(scales, "scales", (rows, cols), (torch.float32,), dev)
+        lds = _pitch(scales)
     _launch(torch, dev, stream, library().gptq_fp8_quantize,
-            (X.data_ptr(), code, m, k, _pitch(X), int(block_rows), codes.data_ptr(), _pitch(codes), scales.data_ptr(),
-             _pitch(scales)), (X, codes, scales), "gptq_fp8_quantize")
+            (X.data_ptr(), code, m, k, X.stride(0) if m > 1 else k, int(block_rows), codes.data_ptr(), max(ldc, k),
+             scales.data_ptr(), lds), (X, codes, scales), "gptq_fp8_quantize")
     return codes, scales
 
 
@@ -545,27 +550,34 @@ def gptq_fp8_matmul(x_codes, x_scales, w_codes, w_scales, bias=None, Y=None, out
     dev = x_codes.device
     if w_codes.dim() != 2:
         raise ValueError("w_codes must be a 2-D tensor")
-    n, kb = w_codes.shape[0], -(-k // 128)
-    fp8 = (torch.float8_e4m3fn, torch.uint8)
+    n, kb = w_codes.shape[0], (k + 127) // 128
+    nb = (n + 127) // 128
+    fp8, f32 = (torch.float8_e4m3fn, torch.uint8), torch.float32
     _expect(x_codes, "x_codes", (m, k), fp8, dev)
     _expect(w_codes, "w_codes", (n, k), fp8, dev)
-    _expect(x_scales, "x_scales", (kb, m), (torch.float32,), dev)
-    _expect(w_scales, "w_scales", (-(-n // 128), kb), (torch.float32,), dev)
+    _expect(x_scales, "x_scales", (kb, m), (f32,), dev)
+    _expect(w_scales, "w_scales", (nb, kb), (f32,), dev)
     if torch.is_grad_enabled() and (x_scales.requires_grad or w_scales.requires_grad or
                                     (bias is not None and bias.requires_grad) or (Y is not None and Y.requires_grad)):
         raise _grad_error("gptq_fp8_matmul")
     if Y is None:
-        Y = torch.empty((m, n), dtype=out_dtype or torch.float32, device=dev)
+        Y, ldy = torch.empty(m, n, dtype=out_dtype or f32, device=dev), n
     else:
         _expect(Y, "Y", (m, n), (out_dtype or Y.dtype,), dev)
+        ldy = _pitch(Y)
     y_code = _elem_code(Y, "Y")
+    b_ptr = None
     if bias is not None:
         _expect(bias, "bias", (n,), (Y.dtype,), dev)
-    ws, ws_ptr, ws_bytes = _ws_ptr(torch, library().gptq_fp8_matmul_workspace_size(m, n, k), dev, ws)
-    _launch(torch, dev, stream, library().gptq_fp8_matmul,
-            (x_codes.data_ptr(), _pitch(x_codes), x_scales.data_ptr(), _pitch(x_scales), w_codes.data_ptr(),
-             _pitch(w_codes), w_scales.data_ptr(), _pitch(w_scales), m, n, k, _ptr(bias), Y.data_ptr(), y_code,
-             _pitch(Y), ws_ptr, ws_bytes), (x_codes, x_scales, w_codes, w_scales, bias, Y, ws), "gptq_fp8_matmul")
+        b_ptr = bias.data_ptr()
+    lib = library()
+    need = lib.gptq_fp8_matmul_workspace_size(m, n, k)
+    ws, ws_ptr, ws_bytes = (None, None, 0) if need == 0 and ws is None else _ws_ptr(torch, need, dev, ws)
+    _launch(torch, dev, stream, lib.gptq_fp8_matmul,
+            (x_codes.data_ptr(), x_codes.stride(0) if m > 1 else k, x_scales.data_ptr(),
+             x_scales.stride(0) if kb > 1 else max(m, 1), w_codes.data_ptr(), w_codes.stride(0) if n > 1 else k,
+             w_scales.data_ptr(), w_scales.stride(0) if nb > 1 else kb, m, n, k, b_ptr, Y.data_ptr(), y_code, ldy,
+             ws_ptr, ws_bytes), (x_codes, x_scales, w_codes, w_scales, bias, Y, ws), "gptq_fp8_matmul")
     return Y
 
 
@@ -588,26 +600,38 @@ def gptq_token_logprobs(logits, tokens, top_k: int = 0, logprobs=None, entropy=N
     n, v = logits.shape
     dev = logits.device
     top_k = int(top_k)
-    given = (("tokens", tokens, (n,), torch.int64), ("logprobs", logprobs, (n,), torch.float32),
-             ("entropy", entropy, (n,), torch.float32), ("top_ids", top_ids, (n, max(top_k, 0)), torch.int32),
-             ("top_logprobs", top_logprobs, (n, max(top_k, 0)), torch.float32))
-    for name, t, shape, dtype in given:
-        if t is not None:
-            _expect(t, name, shape, (dtype,), dev)
-            if not t.is_contiguous():
-                raise ValueError(f"{name} must be contiguous")
+    f32, cols = torch.float32, max(top_k, 0)
+    _expect(tokens, "tokens", (n,), (torch.int64,), dev)
+    contiguous = [("tokens", tokens)]
     if logprobs is None:
-        logprobs = torch.empty(n, dtype=torch.float32, device=dev)
+        logprobs = torch.empty(n, dtype=f32, device=dev)
+    else:
+        _expect(logprobs, "logprobs", (n,), (f32,), dev)
+        contiguous.append(("logprobs", logprobs))
     if entropy is None:
-        entropy = torch.empty(n, dtype=torch.float32, device=dev)
+        entropy = torch.empty(n, dtype=f32, device=dev)
+    else:
+        _expect(entropy, "entropy", (n,), (f32,), dev)
+        contiguous.append(("entropy", entropy))
     if top_ids is None:
-        top_ids = torch.empty((n, max(top_k, 0)), dtype=torch.int32, device=dev)
+        top_ids = torch.empty(n, cols, dtype=torch.int32, device=dev)
+    else:
+        _expect(top_ids, "top_ids", (n, cols), (torch.int32,), dev)
+        contiguous.append(("top_ids", top_ids))
     if top_logprobs is None:
-        top_logprobs = torch.empty((n, max(top_k, 0)), dtype=torch.float32, device=dev)
-    ws, ws_ptr, ws_bytes = _ws_ptr(torch, library().gptq_token_logprobs_workspace_size(n, v, top_k), dev, ws)
-    _launch(torch, dev, stream, library().gptq_token_logprobs,
-            (logits.data_ptr(), code, n, v, _pitch(logits), tokens.data_ptr(), top_k, logprobs.data_ptr(),
-             entropy.data_ptr(), top_ids.data_ptr(), top_logprobs.data_ptr(), ws_ptr, ws_bytes),
+        top_logprobs = torch.empty(n, cols, dtype=f32, device=dev)
+    else:
+        _expect(top_logprobs, "top_logprobs", (n, cols), (f32,), dev)
+        contiguous.append(("top_logprobs", top_logprobs))
+    for name, t in contiguous:
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    lib = library()
+    need = lib.gptq_token_logprobs_workspace_size(n, v, top_k)
+    ws, ws_ptr, ws_bytes = (None, None, 0) if need == 0 and ws is None else _ws_ptr(torch, need, dev, ws)
+    _launch(torch, dev, stream, lib.gptq_token_logprobs,
+            (logits.data_ptr(), code, n, v, logits.stride(0) if n > 1 else v, tokens.data_ptr(), top_k,
+             logprobs.data_ptr(), entropy.data_ptr(), top_ids.data_ptr(), top_logprobs.data_ptr(), ws_ptr, ws_bytes),
             (logits, tokens, logprobs, entropy, top_ids, top_logprobs, ws), "gptq_token_logprobs")
     return logprobs, entropy, top_ids, top_logprobs
 
