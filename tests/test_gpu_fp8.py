@@ -129,6 +129,7 @@ def test_matmul_parity(m, n, k, out, biased):
 
 
 @pytest.mark.parametrize("m,n,k,out", [(300, 24581, 200, "f16"), (1000, 16300, 384, "f16"), (2050, 8190, 263, "bf16"),
+                                       (1500, 18500, 384, "bf16"), (1790, 17003, 128, "f16"), (1500, 18500, 256, "f16"),
                                        (300, 3300, 1150, "f16"), (500, 4100, 520, "bf16"), (100, 8200, 1000, "f16"),
                                        (40, 5000, 2050, "f32"), (64, 4000, 1040, "f16"), (380, 4096, 1280, "f32"), (260, 24580, 257, "f32"), (1025, 10001, 128, "bf16"),
                                        (513, 16500, 384, "f32")])
