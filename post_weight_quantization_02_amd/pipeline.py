@@ -164,20 +164,24 @@ class Fp8Linear(_t.nn.Module):
 
 def quantize_model_fp8(blocks: Sequence) -> List[List[str]]:
     """Put an Fp8Linear in the place of every nn.Linear of ``blocks`` (torch modules on
-    the GPU), in place.  A layer used under several names stays one layer.  Returns the
-    names of the replaced layers, block by block."""
-    names, made = [], {}
+    the GPU), in place.  A layer used under several names stays one layer.  Subclasses of
+    nn.Linear stay as they are (nn.MultiheadAttention reads its output projection's weight
+    itself).  All layers are coded before the first one is replaced.  Returns the names of
+    the replaced layers, block by block."""
+    names, made, places = [], {}, []
     for block in blocks:
         if isinstance(block, _t.nn.Linear):
             raise ValueError("a block that is itself a Linear cannot be replaced in place: use Fp8Linear")
         names.append([])
         for parent_name, parent in list(block.named_modules()):
             for name, child in list(parent._modules.items()):     # under every name, a shared layer's too
-                if isinstance(child, _t.nn.Linear):
+                if type(child) is _t.nn.Linear:
                     if id(child) not in made:
-                        made[id(child)] = (child, Fp8Linear(child.weight, child.bias))
-                    setattr(parent, name, made[id(child)][1])
+                        made[id(child)] = Fp8Linear(child.weight, child.bias)
+                    places.append((parent, name, made[id(child)]))
                     names[-1].append(f"{parent_name}.{name}" if parent_name else name)
+    for parent, name, layer in places:
+        setattr(parent, name, layer)
     return names
 
 
@@ -225,4 +229,4 @@ def evaluate(blocks: Sequence, head, x_batches: Sequence, token_batches: Sequenc
     if n == 0:
         raise ValueError("no position holds a token to be judged")
     nll = -lp / n
-    return Evaluation(int(n), nll, math.exp(nll) if nll < 700 else math.inf, entropy / n, hits / n)
+    return Evaluation(int(n), nll, math.inf if nll >= 700 else math.exp(nll), entropy / n, hits / n)

@@ -186,6 +186,37 @@ def test_shared_layer_stays_one_layer_and_refusals():
         P.evaluate([block], head, [x, x], [t])
 
 
+class _WithAttention(torch.nn.Module):
+    def __init__(self):
+        super().__init__()
+        self.att = torch.nn.MultiheadAttention(32, 4, batch_first=True)
+        self.out = torch.nn.Linear(32, 32)
+
+    def forward(self, x):
+        return self.out(self.att(x, x, x, need_weights=False)[0])
+
+
+def test_subclasses_of_linear_stay_and_nothing_is_half_replaced():
+    block = _WithAttention().cuda()
+    kind = type(block.att.out_proj)
+    assert P.quantize_model_fp8([block]) == [["out"]]
+    assert type(block.att.out_proj) is kind and isinstance(block.out, P.Fp8Linear)
+    with torch.no_grad():
+        assert block(torch.randn(2, 5, 32, device="cuda")).shape == (2, 5, 32)
+    mixed = torch.nn.Sequential(linear(32, 32, 1), torch.nn.Linear(32, 32))       # the second on the host
+    with pytest.raises(ValueError, match="device"):
+        P.quantize_model_fp8([mixed])
+    assert type(mixed[0]) is torch.nn.Linear
+
+
+def test_logits_that_are_no_numbers_are_not_hidden():
+    head = linear(10, 32, 2)
+    x, t = torch.randn(2, 3, 32, device="cuda"), torch.zeros(2, 3, dtype=torch.int64, device="cuda")
+    x[0, 1] = float("nan")
+    ev = P.evaluate([], head, [x], [t])
+    assert ev.tokens == 6 and math.isnan(ev.nll) and math.isnan(ev.perplexity) and math.isnan(ev.entropy)
+
+
 def test_captured_chain_replays():
     """A token's step (layer, vocabulary projection, log probabilities) captured once and
     replayed on new inputs, eager steps of the same layers in between; two graphs with
