@@ -318,6 +318,8 @@ gptq_status gptq2d_quantize(const void* X, int32_t x_dtype, int64_t m, int64_t n
  * bits, largest value 448, no infinities, NaN = 0x7F / 0xFF) with one fp32 scale
  * per block of 128 columns.  Nothing is calibrated: a layer's weights are coded
  * once, its inputs on every call, and the product runs on the 8-bit matrix cores.
+ * Outputs and workspaces share no memory with inputs or with each other, in these
+ * calls and in gptq_token_logprobs.
  *
  * gptq_fp8_quantize: X [device] [m x k] (x_dtype GPTQ_F32, GPTQ_F16 or GPTQ_BF16,
  *   leading dimension ld_x >= k) -> codes [device] uint8 [m x ld_codes] (ld_codes >=

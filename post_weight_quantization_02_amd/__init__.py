@@ -230,6 +230,21 @@ def _expect(t, name, shape, dtypes, device):
         raise ValueError(f"{name} has overlapping rows")
 
 
+def _apart(t, name, *others):
+    """An output given by the caller shares no memory with the other tensors of the call."""
+    def span(a):
+        if a.numel() == 0:
+            return 0, 0
+        p = a.data_ptr()
+        return p, p + (sum((d - 1) * st for d, st in zip(a.shape, a.stride())) + 1) * a.element_size()
+    lo, hi = span(t)
+    for o in others:
+        if o is not None:
+            a, b = span(o)
+            if a < hi and lo < b:
+                raise ValueError(f"{name} overlaps another tensor of the call")
+
+
 def _grad_error(where):
     return ValueError(f"{where} has no backward pass: detach its inputs or call it under torch.no_grad()")
 
@@ -522,11 +537,13 @@ def gptq_fp8_quantize(X, block_rows: int = 1, codes=None, scales=None, stream=No
             codes = codes[:, :k]
     else:
         _expect(codes, "codes", (m, k), (torch.float8_e4m3fn, torch.uint8), dev)
+        _apart(codes, "codes", X, scales)
         ldc = _pitch(codes)
     if scales is None:
         scales, lds = torch.empty(rows, cols, dtype=torch.float32, device=dev), max(cols, 1)
     else:
         _expect(scales, "scales", (rows, cols), (torch.float32,), dev)
+        _apart(scales, "scales", X)
         lds = _pitch(scales)
     _launch(torch, dev, stream, library().gptq_fp8_quantize,
             (X.data_ptr(), code, m, k, X.stride(0) if m > 1 else k, int(block_rows), codes.data_ptr(), max(ldc, k),
@@ -564,6 +581,7 @@ def gptq_fp8_matmul(x_codes, x_scales, w_codes, w_scales, bias=None, Y=None, out
         Y, ldy = torch.empty(m, n, dtype=out_dtype or f32, device=dev), n
     else:
         _expect(Y, "Y", (m, n), (out_dtype or Y.dtype,), dev)
+        _apart(Y, "Y", x_codes, x_scales, w_codes, w_scales, bias, ws)
         ldy = _pitch(Y)
     y_code = _elem_code(Y, "Y")
     b_ptr = None
@@ -623,9 +641,11 @@ def gptq_token_logprobs(logits, tokens, top_k: int = 0, logprobs=None, entropy=N
     else:
         _expect(top_logprobs, "top_logprobs", (n, cols), (f32,), dev)
         contiguous.append(("top_logprobs", top_logprobs))
-    for name, t in contiguous:
+    for i, (name, t) in enumerate(contiguous):
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
+        if i > 0:
+            _apart(t, name, logits, ws, *(o for _, o in contiguous[:i]))
     lib = library()
     need = lib.gptq_token_logprobs_workspace_size(n, v, top_k)
     ws, ws_ptr, ws_bytes = (None, None, 0) if need == 0 and ws is None else _ws_ptr(torch, need, dev, ws)

@@ -585,14 +585,13 @@ __global__ __launch_bounds__(64 * WT * WN * WK) __attribute__((amdgpu_waves_per_
 #pragma unroll
   for (int c = 0; c < TT; ++c) {
     const int64_t i = i0 + wi + 16 * c + lr, j = j0 + wj;
-    float* part_y = parts + (int64_t)part * p.m * p.n;
     if constexpr (TN == 4) {
-      if constexpr (SPLIT) store_row64<false, float>(part_y, p.n, nullptr, i, j, q, p.m, p.n, acc[c]);
-      else store_row64<(BT == 256), T>((T*)p.Y, p.ld_y, (const T*)p.bias, i, j, q, p.m, p.n, acc[c]);
+      static_assert(!SPLIT, "split products take narrower tiles");
+      store_row64<(BT == 256), T>((T*)p.Y, p.ld_y, (const T*)p.bias, i, j, q, p.m, p.n, acc[c]);
     } else {
 #pragma unroll
       for (int a = 0; a < TN; ++a) {
-        if constexpr (SPLIT) store4<float>(part_y, p.n, nullptr, i, j + 16 * a + 4 * q, p.m, p.n, acc[c][a]);
+        if constexpr (SPLIT) store4<float>(parts + (int64_t)part * p.m * p.n, p.n, nullptr, i, j + 16 * a + 4 * q, p.m, p.n, acc[c][a]);
         else store4<T>((T*)p.Y, p.ld_y, (const T*)p.bias, i, j + 16 * a + 4 * q, p.m, p.n, acc[c][a]);
       }
     }
@@ -675,12 +674,14 @@ template <typename T, bool WIDE, int BT, int BN, int WT, int WN, int WK, int S, 
 hipError_t launch_dma(const Fp8Plan& plan, const Fp8Args& p, float* ws, hipStream_t s) {
   const int tt = (int)cdiv(p.m, BT), tn = (int)cdiv(p.n, BN);
   const int per = (int)cdiv(cdiv(p.k, kBlk), plan.splits);
-  if (plan.splits == 1) {
-    fp8_dma_kernel<T, WIDE, BT, BN, WT, WN, WK, S, FLOW, false><<<tt * tn, 64 * WT * WN * WK, 0, s>>>(p, tt, tn, per, nullptr);
-  } else {
-    fp8_dma_kernel<T, WIDE, BT, BN, WT, WN, WK, S, FLOW, true><<<tt * tn * plan.splits, 64 * WT * WN * WK, 0, s>>>(p, tt, tn, per, ws);
-    fp8_sum_kernel<T><<<(unsigned)std::min<int64_t>(cdiv(p.m * p.n, 256), 2048), 256, 0, s>>>(p, plan.splits, ws);
+  if constexpr (BT == 64 && BN == 32) {       // the only tiles of products that are split
+    if (plan.splits > 1) {
+      fp8_dma_kernel<T, WIDE, BT, BN, WT, WN, WK, S, FLOW, true><<<tt * tn * plan.splits, 64 * WT * WN * WK, 0, s>>>(p, tt, tn, per, ws);
+      fp8_sum_kernel<T><<<(unsigned)std::min<int64_t>(cdiv(p.m * p.n, 256), 2048), 256, 0, s>>>(p, plan.splits, ws);
+      return hipGetLastError();
+    }
   }
+  fp8_dma_kernel<T, WIDE, BT, BN, WT, WN, WK, S, FLOW, false><<<tt * tn, 64 * WT * WN * WK, 0, s>>>(p, tt, tn, per, nullptr);
   return hipGetLastError();
 }
 
@@ -735,9 +736,11 @@ Fp8Plan fp8_plan(int64_t m, int64_t n, int64_t k) {
     const int64_t tiles = cdiv(m, c.bt) * cdiv(n, c.bn);
     if (tiles > 256) continue;
     p.kind = c.kind;
-    const int64_t nblk = cdiv(k, kBlk), splits = std::max<int64_t>(1, std::min<int64_t>(256 / tiles, nblk / 16));
-    p.splits = (int)cdiv(nblk, cdiv(nblk, splits));     // none empty
-    if (p.splits > 1) p.ws_bytes = (size_t)p.splits * m * n * sizeof(float);
+    if (c.kind == kFp8T64x32) {         // the larger ones are taken from 129 tiles on: nothing to gain
+      const int64_t nblk = cdiv(k, kBlk), splits = std::max<int64_t>(1, std::min<int64_t>(256 / tiles, nblk / 16));
+      p.splits = (int)cdiv(nblk, cdiv(nblk, splits));     // none empty
+      if (p.splits > 1) p.ws_bytes = (size_t)p.splits * m * n * sizeof(float);
+    }
     return p;
   }
   const int64_t t128 = cdiv(m, 128) * cdiv(n, 128), t256 = cdiv(m, 256) * cdiv(n, 256);

@@ -132,7 +132,8 @@ def test_matmul_parity(m, n, k, out, biased):
                                        (1500, 18500, 384, "bf16"), (1790, 17003, 128, "f16"), (1500, 18500, 256, "f16"),
                                        (300, 3300, 1150, "f16"), (500, 4100, 520, "bf16"), (100, 8200, 1000, "f16"),
                                        (40, 5000, 2050, "f32"), (64, 4000, 1040, "f16"), (380, 4096, 1280, "f32"), (260, 24580, 257, "f32"), (1025, 10001, 128, "bf16"),
-                                       (513, 16500, 384, "f32")])
+                                       (513, 16500, 384, "f32"), (70, 300, 5000, "f32"), (100, 64, 8192, "f16"),
+                                       (200, 161, 6200, "bf16"), (65, 33, 12345, "f32")])
 def test_matmul_parity_large(m, n, k, out):
     """Enough outputs for the largest tiles, with ragged edges on every side."""
     xc, sx, wc, sw = operands(m, n, k, k)
@@ -200,6 +201,57 @@ def test_layer_end_to_end(m):
     assert np.all(np.abs(f64(y) - X @ W.T) <= bound * 1.001)
 
 
+def test_rows_far_apart():
+    """Rows of codes beyond the reach of the direct loads' 32-bit offsets."""
+    pitch = (1 << 22) + 16
+    for m, n in ((3, 20), (70, 66)):
+        xc, sx, wc, sw = operands(m, n, 300, m)
+        far = torch.zeros(n, pitch, dtype=torch.uint8, device="cuda")[:, 64:364]
+        far.copy_(wc)
+        y = G.gptq_fp8_matmul(xc, sx, far, sw)
+        torch.cuda.synchronize()
+        check(y, "f32", xc, sx, wc, sw)
+
+
+def test_more_than_2_to_31_elements():
+    """Element offsets past 32 bits: the last rows and columns of large operands."""
+    m, k = 70001, 32768
+    x = torch.zeros(m, k, dtype=torch.float16, device="cuda")
+    x[-3:] = make_x(3, k, 4, "f16", "loud").cuda()
+    for rows in (1, 128):
+        codes, scales = G.gptq_fp8_quantize(x, rows)
+        lo = m - 3 if rows == 1 else (m - 1) // 128 * 128
+        rc, rs = O.fp8.quantize(f64(x[lo:]), rows)
+        np.testing.assert_array_equal(bits(codes[lo:]), rc)
+        np.testing.assert_array_equal((scales[:, lo:] if rows == 1 else scales[-1:]).cpu().numpy(), rs)
+    del x, codes, scales
+    xc, sx, wc, sw = operands(50000, 45000, 128, 5)              # outputs
+    y = G.gptq_fp8_matmul(xc, sx * 1e-3, wc, sw, out_dtype=torch.float16)
+    check(y[-300:, :], "f16", xc[-300:], sx[:, -300:] * 1e-3, wc, sw)
+    del y
+    xc, sx, wc, sw = operands(2, 256, 4096, 6)                   # weights
+    w = torch.zeros(1 << 20, 4096, dtype=torch.uint8, device="cuda")
+    s = torch.ones(1 << 13, 32, device="cuda")
+    w[-256:], s[-2:] = wc, sw
+    y = G.gptq_fp8_matmul(xc, sx, w, s)
+    check(y[:, -256:], "f32", xc, sx, wc, sw)
+    assert (y[:, :-256] == 0).all()
+
+
+def test_outputs_in_other_tensors_memory_are_refused():
+    x = torch.randn(8, 256, device="cuda")
+    with pytest.raises(ValueError, match="overlaps"):
+        G.gptq_fp8_quantize(x, codes=x.view(torch.uint8)[:, :256])
+    with pytest.raises(ValueError, match="overlaps"):
+        G.gptq_fp8_quantize(x, scales=x.view(-1)[5:21].view(2, 8))
+    xc, sx, wc, sw = operands(4, 4, 128, 1)
+    with pytest.raises(ValueError, match="overlaps"):
+        G.gptq_fp8_matmul(xc, sx, wc, sw, Y=xc.view(torch.float32)[:, :4])
+    both = torch.zeros(8, 512, dtype=torch.uint8, device="cuda")
+    codes, scales = G.gptq_fp8_quantize(x, codes=both[:, :256])  # a part of a wider tensor is fine
+    assert torch.equal(codes, G.gptq_fp8_quantize(x)[0].view(torch.uint8)) and (both[:, 256:] == 0).all()
+
+
 def test_empty_batch_and_side_stream():
     xc, sx, wc, sw = operands(40, 300, 700, 9)
     assert G.gptq_fp8_matmul(xc[:0], sx[:, :0], wc, sw).shape == (0, 300)
@@ -217,7 +269,7 @@ def test_empty_batch_and_side_stream():
     assert torch.equal(y, ref)
 
 
-@pytest.mark.parametrize("m,n,k", [(1, 256, 512), (48, 384, 1024), (200, 256, 2048)])
+@pytest.mark.parametrize("m,n,k", [(1, 256, 512), (48, 384, 1024), (200, 256, 2048), (90, 96, 4224)])
 def test_graph_replays_match_eager(m, n, k):
     """Quantize and product captured together; each replay on new inputs equals the
     eager calls bitwise, with eager work on the same operands in between."""

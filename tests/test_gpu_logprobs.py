@@ -81,7 +81,7 @@ CASES = [(1, 1, 1, "normal"), (3, 2, 2, "normal"), (2, 7, 0, "normal"), (5, 63, 
          (2, 100, 64, "masked"), (3, 513, 5, "sharp"), (2, 2049, 20, "ends"), (1, 4097, 1, "coarse"), (3, 5000, 20, "equal"),
          (2, 9001, 33, "ascending"), (1, 20011, 20, "masked"), (2, 30000, 64, "shifted"), (1100, 300, 5, "normal"),
          (1030, 2500, 20, "coarse"), (7, 12345, 0, "lowest"), (2, 6000, 7, "lowest"), (4, 5001, 3, "all_lowest"), (3, 3000, 2, "all_largest"),
-         (9, 260, 1, "masked"), (1500, 77, 77 - 20, "coarse"), (3, 70000, 64, "ascending"), (4, 8200, 64, "equal"), (1, 131072, 20, "normal")]
+         (9, 260, 1, "masked"), (1500, 77, 77 - 20, "coarse"), (3, 70000, 64, "ascending"), (4, 8200, 64, "equal"), (1, 131072, 20, "normal"), (2, 140001, 64, "coarse"), (1, 270000, 32, "masked")]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
@@ -141,6 +141,21 @@ def test_given_outputs_and_empty_batch():
     check(x, tok, 4, got)
     e = G.gptq_token_logprobs(x.cuda()[:0], tok.cuda()[:0], 4)
     assert [t.shape[0] for t in e] == [0, 0, 0, 0]
+
+
+def test_more_than_2_to_31_logits_and_overlaps():
+    n, v = 33000, 65600
+    x = torch.zeros(n, v, dtype=torch.bfloat16, device="cuda")
+    tail, tok = make(4, v, 11, "bf16")
+    x[-4:] = tail.cuda()
+    t = torch.zeros(n, dtype=torch.int64, device="cuda")
+    t[-4:] = tok.cuda()
+    got = G.gptq_token_logprobs(x, t, 3)
+    torch.cuda.synchronize()
+    check(tail, tok, 3, tuple(a[-4:] for a in got))
+    out = torch.zeros(8, device="cuda")
+    with pytest.raises(ValueError, match="overlaps"):
+        G.gptq_token_logprobs(x[:4], t[:4], 0, logprobs=out[:4], entropy=out[3:7])
 
 
 @pytest.mark.parametrize("n", [1, 1200])
