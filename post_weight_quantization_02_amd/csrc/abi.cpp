@@ -316,7 +316,8 @@ gptq_status gptq_fp8_quantize(const void* X, int32_t x_dtype, int64_t m, int64_t
 
 size_t gptq_fp8_matmul_workspace_size(int64_t m, int64_t n, int64_t k) {
   if (m <= 0 || n <= 0 || k <= 0 || m > kMaxDim || n > kMaxDim || k > kMaxDim) return 0;
-  return gptq::fp8_plan(m, n, k).ws_bytes;
+  // enough for every type of output
+  return std::max(gptq::fp8_plan(m, n, k, true).ws_bytes, gptq::fp8_plan(m, n, k, false).ws_bytes);
 }
 
 gptq_status gptq_fp8_matmul(const uint8_t* x_codes, int64_t ld_x, const float* x_scales, int64_t ld_xs,
@@ -330,7 +331,7 @@ gptq_status gptq_fp8_matmul(const uint8_t* x_codes, int64_t ld_x, const float* x
   if (x_codes == nullptr || x_scales == nullptr || w_codes == nullptr || w_scales == nullptr || Y == nullptr)
     return GPTQ_ERR_NULL_POINTER;
   if (ld_x < k || ld_w < k || ld_xs < m || ld_ws < gptq::cdiv(k, 128) || ld_y < n) return GPTQ_ERR_BAD_LEADING_DIM;
-  const gptq::Fp8Plan plan = gptq::fp8_plan(m, n, k);
+  const gptq::Fp8Plan plan = gptq::fp8_plan(m, n, k, y_dtype == GPTQ_F32);
   if (gptq_status st = ws_check(ws, ws_bytes, plan.ws_bytes)) return st;
   const gptq::Fp8Args p{x_codes, ld_x, x_scales, ld_xs, w_codes, ld_w, w_scales, ld_ws, m, n, k, bias, Y, y_dtype, ld_y};
   return from_hip(gptq::fp8_matmul_launch(plan, p, ws, (hipStream_t)stream));

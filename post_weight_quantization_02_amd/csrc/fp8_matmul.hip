@@ -45,6 +45,17 @@ __device__ __forceinline__ u32x4 load_chunk(const uint8_t* __restrict__ row, int
   return v;
 }
 
+// The same in two steps for k >= 16, so that the loads of several chunks are under way
+// together: 16 bytes that lie in the row, then the codes of column c on to the front.
+__device__ __forceinline__ u32x4 load_inside(const uint8_t* __restrict__ row, int64_t c, int64_t k) {
+  return *(const u32x4_any*)(row + min(c, k - 16));
+}
+__device__ __forceinline__ u32x4 align_chunk(u32x4 v, int64_t c, int64_t k) {
+  const int past = (int)(c + 16 - k);
+  if (past >= 16) return u32x4{0u, 0u, 0u, 0u};
+  return past <= 0 ? v : __builtin_bit_cast(u32x4, __builtin_bit_cast(unsigned __int128, v) >> (8 * past));
+}
+
 __device__ __forceinline__ i32x8 join(u32x4 a, u32x4 b) {
   return i32x8{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
 }
@@ -214,7 +225,8 @@ __device__ __forceinline__ void load4_to_lds(__amdgpu_buffer_rsrc_t r, float* to
 // its blocks of W, and the rows of X and their scales with them, through a ring of R
 // LDS slots of its own, filled by direct loads R - 1 blocks ahead: no barriers, and
 // nothing in flight holds registers.  HBM-bound on W, so the exact (widened) block sums
-// cost nothing.  A last block of fewer than 128 columns goes through registers.
+// cost nothing.  A last block of fewer than 128 columns goes through registers, asked
+// for first and multiplied last.
 constexpr int kFewWaves = 4;
 
 template <int TT>
@@ -230,7 +242,7 @@ __device__ __forceinline__ Slot<TT> (&slots())[kFewWaves] {
 }
 
 template <typename T, int TT, int R, bool DMA>
-__global__ __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_per_eu(2))) void fp8_few_kernel(Fp8Args p) {
+__global__ __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_per_eu(TT == 4 ? 1 : 2))) void fp8_few_kernel(Fp8Args p) {
   __shared__ f32x4 part[kFewWaves][TT][64];
   const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
   const int lr = lane & 15, q = lane >> 4;
@@ -241,7 +253,7 @@ __global__ __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_per_eu(
   f32x4 acc[TT];
 #pragma unroll
   for (int c = 0; c < TT; ++c) acc[c] = f32x4{0.f, 0.f, 0.f, 0.f};
-  // blocks through registers: the last one, or all of them where rows may start anywhere
+  // blocks through registers, where rows may start anywhere
   const auto by_registers = [&](int b) {
     const auto both = [&](const uint8_t* r) {
       return join(load_chunk(r, (int64_t)b * kBlk + 16 * q, p.k), load_chunk(r, (int64_t)b * kBlk + 64 + 16 * q, p.k));
@@ -290,6 +302,22 @@ __global__ __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_per_eu(
         scale_add(acc[c], block_product(wf, xf), s.sx[16 * c + lr] * scale);
       }
     };
+    // a last block of fewer columns: asked for before the others, multiplied after them
+    const bool tail = full < nblk && full % kFewWaves == w;
+    const int64_t c0 = (int64_t)full * kBlk + 16 * q;
+    u32x4 tw[2], tx[TT][2];
+    float ts[TT];
+    if (tail) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) tw[h] = load_inside(p.W + (j0 + min(lr, rows_w - 1)) * p.ld_w, c0 + 64 * h, p.k);
+#pragma unroll
+      for (int c = 0; c < TT; ++c) {
+        const int64_t i = min(16 * c + lr, rows_x - 1);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) tx[c][h] = load_inside(p.X + i * p.ld_x, c0 + 64 * h, p.k);
+        ts[c] = p.sx[(int64_t)full * p.ld_sx + i];
+      }
+    }
     if (mine > 0) {
       float sw_next = sw[w];
       static_for<0, R - 1>([&](auto i) { fetch(slots<TT, i.value>()[w], block_of(i.value)); });
@@ -309,7 +337,15 @@ __global__ __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_per_eu(
         if (i < mine) one(h);
       });
     }
-    if (full < nblk && full % kFewWaves == w) by_registers(full);
+    if (tail) {
+      const auto both = [&](const u32x4 (&v)[2]) {
+        return Frag<true>(join(align_chunk(v[0], c0, p.k), align_chunk(v[1], c0 + 64, p.k)));
+      };
+      const Frag<true> wf = both(tw);
+      const float scale = sw[full];
+#pragma unroll
+      for (int c = 0; c < TT; ++c) scale_add(acc[c], block_product(wf, both(tx[c])), ts[c] * scale);
+    }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // unused fetches write LDS: not after this work-group's end
   }
 #pragma unroll
@@ -460,21 +496,34 @@ __global__ __launch_bounds__(64 * WT * WN * WK) __attribute__((amdgpu_waves_per_
 #pragma unroll
     for (int a = 0; a < TN; ++a) scale_add(acc[TT - 1][a], last[a], sc_last);
   };
-  // a block of fewer than 128 columns, through registers
-  const auto fetch_tail = [&](int b) {
-    StageX<BT>& sx = stage_x<BT, WK, 0>()[0];
-    for (int id = t; id < (BT + BN) * 8; id += 64 * kWavesHere * WK) {
-      const bool is_x = id < BT * 8;
-      const int r = is_x ? id >> 3 : (id >> 3) - BT, c = id & 7;
-      const uint8_t* row = is_x ? p.X + (i0 + min(r, rows_x - 1)) * p.ld_x : p.W + (j0 + min(r, rows_w - 1)) * p.ld_w;
-      const u32x4 v = load_chunk(row, (int64_t)b * kBlk + 16 * c, p.k);
-      const int at = r * kBlk + ((c ^ (r & 7)) * 16);
-      if (is_x) *(u32x4*)(sx.x + at) = v;
-      else *(u32x4*)(stage_w<BN, WK, 0>()[0].w + at) = v;
-    }
-    if (t < BT) sx.sx[t] = p.sx[(int64_t)b * p.ld_sx + i0 + min(t, rows_x - 1)];
-  };
+  // a last block of fewer than 128 columns, through registers: all loads first, and LDS
+  // written once the next blocks' loads are under way
   const bool tail = b1 == nblk && (p.k % kBlk) != 0;
+  constexpr int kAll = 64 * kWavesHere * WK, kTail = ((BT + BN) * 8 + kAll - 1) / kAll;
+  static_assert(BT <= kAll, "a scale per thread");
+  u32x4 tail_v[kTail];
+  float tail_s = 0.f;
+  if (tail) {
+#pragma unroll
+    for (int i = 0; i < kTail; ++i) {
+      const int id = t + i * kAll, r = min(id >> 3, BT + BN - 1);
+      const uint8_t* row = r < BT ? p.X + (i0 + min(r, rows_x - 1)) * p.ld_x : p.W + (j0 + min(r - BT, rows_w - 1)) * p.ld_w;
+      tail_v[i] = load_inside(row, (int64_t)(nblk - 1) * kBlk + 16 * (id & 7), p.k);
+    }
+    tail_s = p.sx[(int64_t)(nblk - 1) * p.ld_sx + i0 + min(t, rows_x - 1)];
+  }
+  const auto put_tail = [&]() {
+    if (!tail) return;
+    StageX<BT>& sx = stage_x<BT, WK, 0>()[0];
+#pragma unroll
+    for (int i = 0; i < kTail; ++i) {
+      const int id = t + i * kAll, r = id >> 3, c = id & 7;
+      const u32x4 v = align_chunk(tail_v[i], (int64_t)(nblk - 1) * kBlk + 16 * c, p.k);
+      if (r < BT) *(u32x4*)(sx.x + r * kBlk + ((c ^ (r & 7)) * 16)) = v;
+      else if (r < BT + BN) *(u32x4*)(stage_w<BN, WK, 0>()[0].w + (r - BT) * kBlk + ((c ^ (r & 7)) * 16)) = v;
+    }
+    if (t < BT) sx.sx[t] = tail_s;
+  };
   // the groups take the blocks in turn
   const int count = b1 - b0, steps = (count + WK - 1) / WK;
   const auto block_of = [&](int at) { return !tail ? b0 + at : at == 0 ? nblk - 1 : b0 + at - 1; };
@@ -482,7 +531,6 @@ __global__ __launch_bounds__(64 * WT * WN * WK) __attribute__((amdgpu_waves_per_
   // counts of outstanding loads are known, and no read waits for a later block
   const auto next = [&](int step) { return step * WK + g < count ? block_of(step * WK + g) : 0; };
   float sw_next = swp[next(0)];
-  if (tail) fetch_tail(nblk - 1);
   if (!tail || g > 0) fetch(std::integral_constant<int, 0>{}, next(0));
   int step = 0;
   // one(stage, whether the group has a block): only in the last step may it have none
@@ -494,6 +542,7 @@ __global__ __launch_bounds__(64 * WT * WN * WK) __attribute__((amdgpu_waves_per_
   };
   if constexpr (FLOW == kBlocks) {
     static_for<1, S - 1>([&](auto i) { fetch(i, next(i.value)); });
+    put_tail();
     run([&](auto i, bool has) {
       constexpr int h = i.value, to = (h + S - 1) % S;
       const StageX<BT>& s = stage_x<BT, WK, h>()[g];
@@ -524,6 +573,7 @@ __global__ __launch_bounds__(64 * WT * WN * WK) __attribute__((amdgpu_waves_per_
   } else {
     static_assert(S % 2 == 0, "two sets of registers in turn");
     static_for<1, S>([&](auto i) { fetch(i, next(i.value)); });
+    put_tail();
     i32x8 wv[2][TN], xv[2][TT];
     float sxv[2][TT];
     constexpr int kReads = TN + TT;
@@ -689,8 +739,9 @@ template <typename T>
 hipError_t launch(const Fp8Plan& plan, const Fp8Args& p, float* ws, hipStream_t s) {
   constexpr bool WIDE = std::is_same<T, float>::value;
   // the direct loads need 16-byte rows, 32-bit offsets inside a tile and a whole block
-  const bool dma = p.k >= kBlk && (((uintptr_t)p.X | (uintptr_t)p.W | (uint64_t)p.ld_x | (uint64_t)p.ld_w) & 15) == 0 &&
-                   std::max(p.ld_x, p.ld_w) <= (int64_t(1) << 22);
+  const uint64_t ld_x = p.m > 1 ? (uint64_t)p.ld_x : 0, ld_w = p.n > 1 ? (uint64_t)p.ld_w : 0;
+  const bool dma = p.k >= kBlk && (((uintptr_t)p.X | (uintptr_t)p.W | ld_x | ld_w) & 15) == 0 &&
+                   std::max(ld_x, ld_w) <= (uint64_t(1) << 22);
   const unsigned few = (unsigned)cdiv(p.n, 16);
   if (plan.kind == kFp8Few) {
     if (!dma) {
@@ -716,7 +767,7 @@ hipError_t launch(const Fp8Plan& plan, const Fp8Args& p, float* ws, hipStream_t 
     case kFp8T96x64: return launch_dma<T, WIDE, 96, 64, 2, 2, 2, 3, kBlocks>(plan, p, ws, s);
     case kFp8T128x64: return launch_dma<T, WIDE, 128, 64, 2, 2, 2, 3, kBlocks>(plan, p, ws, s);
     case kFp8T128x128Two: return launch_dma<T, WIDE, 128, 128, 2, 2, 2, 2, kBlocks>(plan, p, ws, s);
-    case kFp8T256x256:
+    case kFp8T256x256:                // 16-bit outputs only
       if constexpr (!WIDE) return launch_dma<T, WIDE, 256, 256, 2, 4, 1, 2, kBlocks>(plan, p, ws, s);
       [[fallthrough]];
     default: return launch_dma<T, WIDE, 128, 128, 2, 2, 1, 2, kBlocks>(plan, p, ws, s);
@@ -725,10 +776,25 @@ hipError_t launch(const Fp8Plan& plan, const Fp8Args& p, float* ws, hipStream_t 
 
 }  // namespace
 
-Fp8Plan fp8_plan(int64_t m, int64_t n, int64_t k) {
+// Which kernel (times: 16-bit outputs, k = 4096, graph replays).
+//   few rows or tiles: 32 x 4096 6.8 against 8.6 us, 64 x 4096 9.2 against 10; from 17 rows
+//     on X is as much of the work as W: 32 x 11008 12.7 against 11.3 (fp32 outputs, whose
+//     tiles have half the matrix rate: 12.8 against 16.4).  Along k > 8192 few work-groups
+//     are too slow: 1 x 512 x 16384 12.7 us, in split tiles 8.8.
+//   the smallest tiles that one round of 256 CUs covers: 128 x 4096 9.1 us in 64 x 32 tiles
+//     against 11.0 in the next; 256 x 4096 11.5 (64 x 64) against 16.4 and 13.6; 384 x 4096
+//     14.3 (96 x 64) against 20.6 and 16.3; 512 x 4096 17.1 (128 x 64) against 26.0 and 20.9;
+//     1024 x 4096 24.6 (128 x 128, two groups) against 32.3 and 26.4 (one group).
+//   k in parts where one round is less than half full: 96 x 512 x 8192 9.1 us, in one 12.3.
+//   beyond one round, 128 x 128 or 256 x 256, by their times in us: a 128 x 128 tile adds
+//     0.0064 + 0.00216 per block of k, a round of the larger ones takes 9.1 + 1.78, one of r
+//     tiles 0.38 + 0.62 r / 256 of that.  2048 x 4096 38 against 46.5 us (r = 128), 1024 x
+//     12288 60 against 56 (r = 192), 4096 x 12288 230 against 185; 2048 x 12288 x 1024 36
+//     against 41.
+Fp8Plan fp8_plan(int64_t m, int64_t n, int64_t k, bool wide) {
   Fp8Plan p{kFp8Few, 1, 0};
-  if (m <= 32 || (m <= 64 && n <= 16 * 256)) return p;
-  // the smallest tiles that one round of 256 CUs covers
+  const bool few = k > 8192 && n <= 1024 ? false : m <= 16 ? true : m <= 32 ? wide || n <= 8192 : m <= 64 && n <= 4096 && k <= 4096;
+  if (few) return p;
   const struct { int kind, bt, bn; } small[] = {
       {kFp8T64x32, 64, 32}, {kFp8T64x64, 64, 64}, {kFp8T96x64, 96, 64}, {kFp8T128x64, 128, 64},
       {kFp8T128x128Two, 128, 128}};
@@ -736,15 +802,16 @@ Fp8Plan fp8_plan(int64_t m, int64_t n, int64_t k) {
     const int64_t tiles = cdiv(m, c.bt) * cdiv(n, c.bn);
     if (tiles > 256) continue;
     p.kind = c.kind;
-    if (c.kind == kFp8T64x32) {         // the larger ones are taken from 129 tiles on: nothing to gain
+    if (c.kind == kFp8T64x32) {         // the larger ones are taken from 129 tiles on: nothing to split
       const int64_t nblk = cdiv(k, kBlk), splits = std::max<int64_t>(1, std::min<int64_t>(256 / tiles, nblk / 16));
       p.splits = (int)cdiv(nblk, cdiv(nblk, splits));     // none empty
       if (p.splits > 1) p.ws_bytes = (size_t)p.splits * m * n * sizeof(float);
     }
     return p;
   }
-  const int64_t t128 = cdiv(m, 128) * cdiv(n, 128), t256 = cdiv(m, 256) * cdiv(n, 256);
-  p.kind = cdiv(t256, 256) * 854 < t128 ? kFp8T256x256 : kFp8T128x128;
+  const int64_t t128 = cdiv(m, 128) * cdiv(n, 128), t256 = cdiv(m, 256) * cdiv(n, 256), rest = t256 % 256;
+  const double nblk = (double)cdiv(k, kBlk), rounds = (double)(t256 / 256) + (rest > 0 ? 0.38 + 0.62 * rest / 256 : 0.0);
+  p.kind = !wide && rounds * (9.1 + 1.78 * nblk) < t128 * (0.0064 + 0.00216 * nblk) ? kFp8T256x256 : kFp8T128x128;
   return p;
 }
 

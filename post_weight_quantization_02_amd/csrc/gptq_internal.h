@@ -83,7 +83,7 @@ struct Fp8Plan {
   int splits;             // parts of k, summed by a second launch when more than one
   size_t ws_bytes;
 };
-Fp8Plan fp8_plan(int64_t m, int64_t n, int64_t k);
+Fp8Plan fp8_plan(int64_t m, int64_t n, int64_t k, bool wide);      // wide: fp32 outputs
 struct Fp8Args {
   const uint8_t* X;
   int64_t ld_x;

@@ -201,6 +201,17 @@ def test_layer_end_to_end(m):
     assert np.all(np.abs(f64(y) - X @ W.T) <= bound * 1.001)
 
 
+def test_single_rows_of_any_pitch():
+    """One row of X, or of W, has no pitch: the same bits whatever is passed for it."""
+    for m, n in ((1, 40), (5, 1), (70, 1), (1, 1)):
+        xc, sx, wc, sw = operands(m, n, 1000, m)
+        y = G.gptq_fp8_matmul(xc, sx, wc, sw)
+        torch.cuda.synchronize()
+        check(y, "f32", xc, sx, wc, sw)
+        own = [c.contiguous() if c.shape[0] == 1 else c for c in (xc, wc)]
+        assert torch.equal(G.gptq_fp8_matmul(own[0], sx, own[1], sw), y)
+
+
 def test_rows_far_apart():
     """Rows of codes beyond the reach of the direct loads' 32-bit offsets."""
     pitch = (1 << 22) + 16
