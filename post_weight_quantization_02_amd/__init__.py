@@ -532,9 +532,7 @@ def gptq_fp8_quantize(X, block_rows: int = 1, codes=None, scales=None, stream=No
     rows, cols = (kb, m) if block_rows == 1 else ((m + 127) // 128, kb)
     if codes is None:
         ldc = kb * 128
-        codes = torch.empty(m, ldc, dtype=torch.float8_e4m3fn, device=dev)
-        if k != ldc:
-            codes = codes[:, :k]
+        codes = torch.empty_strided((m, k), (ldc, 1), dtype=torch.float8_e4m3fn, device=dev)
     else:
         _expect(codes, "codes", (m, k), (torch.float8_e4m3fn, torch.uint8), dev)
         _apart(codes, "codes", X, scales)

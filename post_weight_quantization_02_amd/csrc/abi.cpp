@@ -339,7 +339,8 @@ gptq_status gptq_fp8_matmul(const uint8_t* x_codes, int64_t ld_x, const float* x
 
 size_t gptq_token_logprobs_workspace_size(int64_t n, int64_t v, int64_t top_k) {
   if (n <= 0 || v <= 0 || n > kMaxDim || v > kMaxDim || top_k < 0 || top_k > GPTQ_MAX_TOP || top_k > v) return 0;
-  return gptq::logprob_plan(n, v, top_k).ws_bytes;
+  // enough for every type: rows of wider elements are split sooner, into the same parts
+  return gptq::logprob_plan(n, v, top_k, 4).ws_bytes;
 }
 
 gptq_status gptq_token_logprobs(const void* logits, int32_t dtype, int64_t n, int64_t v, int64_t ld, const int64_t* tokens,
@@ -353,7 +354,7 @@ gptq_status gptq_token_logprobs(const void* logits, int32_t dtype, int64_t n, in
       (top_k > 0 && (top_ids == nullptr || top_logprobs == nullptr)))
     return GPTQ_ERR_NULL_POINTER;
   if (ld < v) return GPTQ_ERR_BAD_LEADING_DIM;
-  const gptq::LogprobPlan plan = gptq::logprob_plan(n, v, top_k);
+  const gptq::LogprobPlan plan = gptq::logprob_plan(n, v, top_k, dtype == GPTQ_F32 ? 4 : 2);
   if (gptq_status st = ws_check(ws, ws_bytes, plan.ws_bytes)) return st;
   const gptq::LogprobArgs p{logits, dtype, n, v, ld, tokens, (int)top_k, logprobs, entropy, top_ids, top_logprobs};
   return from_hip(gptq::logprob_launch(plan, p, ws, (hipStream_t)stream));

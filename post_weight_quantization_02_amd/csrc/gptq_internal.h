@@ -107,7 +107,7 @@ struct LogprobPlan {
   int64_t span;           // elements of a part
   size_t ws_bytes;
 };
-LogprobPlan logprob_plan(int64_t n, int64_t v, int64_t top_k);
+LogprobPlan logprob_plan(int64_t n, int64_t v, int64_t top_k, int elem_bytes);
 struct LogprobArgs {
   const void* logits;
   int dtype;

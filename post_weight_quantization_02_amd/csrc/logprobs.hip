@@ -21,8 +21,12 @@
 // elements are known to lie at or above it.  Values are ordered as 32-bit keys (NaN
 // above +inf, -0 equal to +0); equal values by lower index.
 //
-// Few rows: a row is split over work-groups, and a second launch joins the parts in
+// Few long rows: a row is split over work-groups, and a second launch joins the parts in
 // a fixed order.
+//
+// HBM-bound on long texts: 4096 x 65536 bf16 with the top token 98 us, 5.5 TB/s (a large
+// read reaches 5.95); 8192 x 32000 fp16 91 us, 5.7 TB/s.  1 x 128000 bf16 with 20 top tokens
+// 15 us: about 9 in 63 parts, whose selection is a chain of dependent steps, 5.5 in the join.
 #include "gptq_internal.h"
 
 namespace gptq {
@@ -463,9 +467,16 @@ hipError_t launch(const LogprobPlan& plan, const LogprobArgs& p, uint32_t* ws, h
 
 }  // namespace
 
-LogprobPlan logprob_plan(int64_t n, int64_t v, int64_t top_k) {
+// Parts of a row: at least 2048 elements, together some 2048 work-groups (1024 from 128 rows
+// on), and as many lists as the join's LDS holds.  The second launch pays from rows of about
+// 28 KB on: 1 x 6000 bf16 8.4 us in parts, 6.7 whole; 1 x 40000 8.8 against 12.6; 64 x 6000 fp32
+// with 20 top tokens 15.6 against 15.4, 64 x 9000 15.9 against 18.1.  With more rows than CUs
+// from longer ones on, 512 rows are enough by themselves: 350 x 16000 bf16 14.3 against 12.3,
+// 350 x 50000 20.8 against 22.4, 350 x 128000 32 against 41, 450 x 24000 16.6 against 15.7.
+LogprobPlan logprob_plan(int64_t n, int64_t v, int64_t top_k, int elem_bytes) {
   LogprobPlan p{1, v, 0};
-  const int64_t want = n >= 1024 ? 1 : cdiv(2048, std::max<int64_t>(n, 1));
+  const int64_t least = (28 << 10) * std::max<int64_t>(1, n / 64 - 2);
+  const int64_t want = n >= 512 || v * elem_bytes < least ? 1 : cdiv(n >= 128 ? 1024 : 2048, std::max<int64_t>(n, 1));
   const int64_t most = std::min<int64_t>(std::min<int64_t>(kMaxSplits, 4096 / std::max<int64_t>(top_k, 1)), cdiv(v, 2048));
   p.splits = (int)std::max<int64_t>(1, std::min(want, most));
   p.span = cdiv(v, p.splits);

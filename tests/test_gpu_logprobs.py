@@ -158,18 +158,18 @@ def test_more_than_2_to_31_logits_and_overlaps():
         G.gptq_token_logprobs(x[:4], t[:4], 0, logprobs=out[:4], entropy=out[3:7])
 
 
-@pytest.mark.parametrize("n", [1, 1200])
-def test_graph_replays_match_eager(n):
-    x = torch.randn(n, 6000, device="cuda").to(torch.bfloat16)
-    tok = torch.randint(0, 6000, (n,), device="cuda")
+@pytest.mark.parametrize("n,v", [(1, 6000), (1, 40000), (1200, 6000)])
+def test_graph_replays_match_eager(n, v):
+    x = torch.randn(n, v, device="cuda").to(torch.bfloat16)
+    tok = torch.randint(0, v, (n,), device="cuda")
     G.gptq_token_logprobs(x, tok, 8)
     torch.cuda.synchronize()
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
         got = G.gptq_token_logprobs(x, tok, 8)
     for r in range(3):
-        x.copy_(torch.randn(n, 6000, device="cuda"))
-        tok.random_(0, 6000)
+        x.copy_(torch.randn(n, v, device="cuda"))
+        tok.random_(0, v)
         ref = G.gptq_token_logprobs(x, tok, 8)
         torch.cuda.synchronize()
         g.replay()
