@@ -131,63 +131,127 @@ __device__ __forceinline__ void store4(T* __restrict__ Y, int64_t ld_y, const T*
   }
 }
 
-// A wave's 16 rows x 64 outputs of four neighbouring tiles: v[a] holds outputs 16 a +
-// 4 q .. + 3 of the lane's row.  For 16-bit types the four lanes of a row swap parts
-// (registers only), so that each holds 16 outputs in a row and stores 32 bytes; STREAM:
-// past the caches' keeping, for outputs larger than they hold.
-template <bool STREAM, typename T>
-__device__ __forceinline__ void store_row64(T* __restrict__ Y, int64_t ld_y, const T* __restrict__ bias, int64_t i, int64_t j0,
-                                            int q, int64_t m, int64_t n, const f32x4 (&v)[4]) {
-  if constexpr (sizeof(T) == 2) {
-    typedef T T4 __attribute__((ext_vector_type(4)));
-    typedef T T4_any __attribute__((ext_vector_type(4), aligned(2)));
-    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-    typedef uint32_t u32x4_at2 __attribute__((ext_vector_type(4), aligned(2)));
-    if (j0 + 64 <= n) {         // the same for the whole wave
-      uint32_t u[4][2];
+// a lane's v from the lane whose number differs in bit 0 or bit 1
+template <int BIT>
+__device__ __forceinline__ uint32_t other_lane(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, BIT == 0 ? 0xB1 : 0x4E, 0xf, 0xf, true);
+}
+
+// an empty statement, to keep the compiler from joining a store past the caches with the
+// plain one of the other branch, which would drop the hint
+__device__ __forceinline__ void keep_apart() { asm volatile(""); }
+
+// A wave's 16 rows from i0 on x 64 outputs from j0 on, four neighbouring tiles: v[a] holds
+// outputs 16 a + 4 q .. + 3 of row lr.  Lanes swap parts (registers only), so that one store
+// instruction writes whole rows of 64: 4 rows of fp32, 8 of 16 bits.  stream: past the
+// caches' keeping.
+template <typename T>
+__device__ __forceinline__ void store_rows64(T* __restrict__ Y, int64_t ld_y, const T* __restrict__ bias, int64_t i0, int64_t j0,
+                                             int lr, int q, int64_t m, int64_t n, bool stream, const f32x4 (&v)[4]) {
+  typedef T T4 __attribute__((ext_vector_type(4)));
+  typedef T T4_any __attribute__((ext_vector_type(4), aligned(2)));
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  typedef uint32_t u32x4_at2 __attribute__((ext_vector_type(4), aligned(2)));
+  if (j0 + 64 > n) {         // the same for the whole wave
 #pragma unroll
-      for (int a = 0; a < 4; ++a) {
-        f32x4 f = v[a];
-        if (bias) {
-          const T4_any b = *(const T4_any*)(bias + j0 + 16 * a + 4 * q);
+    for (int a = 0; a < 4; ++a) store4<T>(Y, ld_y, bias, i0 + lr, j0 + 16 * a + 4 * q, m, n, v[a]);
+    return;
+  }
+  if constexpr (sizeof(T) == 4) {
+    // four lanes of neighbouring rows and their four tiles change places
+    uint32_t u[4][4];
 #pragma unroll
-          for (int r = 0; r < 4; ++r) f[r] += (float)b[r];
-        }
-        const u32x2 w = __builtin_bit_cast(u32x2, T4{(T)f[0], (T)f[1], (T)f[2], (T)f[3]});
-        u[a][0] = w[0];
-        u[a][1] = w[1];
+    for (int a = 0; a < 4; ++a)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float f = v[a][e];
+        u[a][e] = __builtin_bit_cast(uint32_t, f);
       }
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+    for (int e = 0; e < 4; ++e) {
 #pragma unroll
-        for (int a = 0; a < 2; ++a) {
-          const auto r = __builtin_amdgcn_permlane32_swap(u[a][h], u[a + 2][h], false, false);
-          u[a][h] = r[0];
-          u[a + 2][h] = r[1];
-        }
+      for (int a = 0; a < 4; a += 2) {
+        const uint32_t r = other_lane<0>((lr & 1) ? u[a][e] : u[a + 1][e]);
+        u[a][e] = (lr & 1) ? r : u[a][e];
+        u[a + 1][e] = (lr & 1) ? u[a + 1][e] : r;
+      }
 #pragma unroll
-        for (int a = 0; a < 4; a += 2) {
-          const auto r = __builtin_amdgcn_permlane16_swap(u[a][h], u[a + 1][h], false, false);
-          u[a][h] = r[0];
-          u[a + 1][h] = r[1];
-        }
+      for (int a = 0; a < 2; ++a) {
+        const uint32_t r = other_lane<1>((lr & 2) ? u[a][e] : u[a + 2][e]);
+        u[a][e] = (lr & 2) ? r : u[a][e];
+        u[a + 2][e] = (lr & 2) ? u[a + 2][e] : r;
       }
-      if (i < m) {
-        T* y = Y + i * ld_y + j0 + 16 * q;
-        const u32x4_at2 lo = {u[0][0], u[0][1], u[1][0], u[1][1]}, hi = {u[2][0], u[2][1], u[3][0], u[3][1]};
-        if constexpr (STREAM) {
-          __builtin_nontemporal_store(lo, (u32x4_at2*)y);
-          __builtin_nontemporal_store(hi, (u32x4_at2*)(y + 8));
-        } else {
-          *(u32x4_at2*)y = lo;
-          *(u32x4_at2*)(y + 8) = hi;
-        }
+    }
+    const int64_t j = j0 + 16 * (lr & 3) + 4 * q;
+    f32x4 b = {0.f, 0.f, 0.f, 0.f};
+    if (bias) b = *(const T4_any*)(bias + j);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int64_t i = i0 + (lr & ~3) + t;
+      f32x4 f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[e] = __builtin_bit_cast(float, u[t][e]) + b[e];
+      if (i >= m) continue;
+      if (stream) {
+        keep_apart();
+        __builtin_nontemporal_store(T4_any(f), (T4_any*)(Y + i * ld_y + j));
+        keep_apart();
+      } else {
+        *(T4_any*)(Y + i * ld_y + j) = f;
       }
-      return;
+    }
+  } else {
+    uint32_t u[4][2];
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      f32x4 f = v[a];
+      if (bias) {
+        const T4_any b = *(const T4_any*)(bias + j0 + 16 * a + 4 * q);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) f[r] += (float)b[r];
+      }
+      const u32x2 w = __builtin_bit_cast(u32x2, T4{(T)f[0], (T)f[1], (T)f[2], (T)f[3]});
+      u[a][0] = w[0];
+      u[a][1] = w[1];
+    }
+    // the four lanes of a row: 16 outputs in a row for each ...
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+        const auto r = __builtin_amdgcn_permlane32_swap(u[a][h], u[a + 2][h], false, false);
+        u[a][h] = r[0];
+        u[a + 2][h] = r[1];
+      }
+#pragma unroll
+      for (int a = 0; a < 4; a += 2) {
+        const auto r = __builtin_amdgcn_permlane16_swap(u[a][h], u[a + 1][h], false, false);
+        u[a][h] = r[0];
+        u[a + 1][h] = r[1];
+      }
+    }
+    // ... and two neighbouring rows: the even lane takes the first 8 of both, the odd one the others
+    const bool odd = lr & 1;
+    u32x4_at2 even_row, odd_row;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t lo = u[e >> 1][e & 1], hi = u[2 + (e >> 1)][e & 1];
+      const uint32_t r = other_lane<0>(odd ? lo : hi);
+      even_row[e] = odd ? r : lo;
+      odd_row[e] = odd ? hi : r;
+    }
+    const int64_t i = i0 + (lr & ~1);
+    T* y = Y + i * ld_y + j0 + 16 * q + 8 * (lr & 1);
+    if (stream) {
+      keep_apart();
+      if (i < m) __builtin_nontemporal_store(even_row, (u32x4_at2*)y);
+      if (i + 1 < m) __builtin_nontemporal_store(odd_row, (u32x4_at2*)(y + ld_y));
+      keep_apart();
+    } else {
+      if (i < m) *(u32x4_at2*)y = even_row;
+      if (i + 1 < m) *(u32x4_at2*)(y + ld_y) = odd_row;
     }
   }
-#pragma unroll
-  for (int a = 0; a < 4; ++a) store4<T>(Y, ld_y, bias, i, j0 + 16 * a + 4 * q, m, n, v[a]);
 }
 
 // sum v (+ bias) over the parts of a split product or the waves of a work-group is
@@ -371,10 +435,10 @@ __global__ __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_per_eu(
 // block; the tile of W has one scale, fetched a block ahead.  A last block of fewer than
 // 128 columns is taken first, through registers, with zeros behind column k.  Scaling
 // lags one row of tiles behind the matrix instructions, so it runs beside them.
-// 4096 x 12288 x 4096, fp16 outputs: 178 us, 2.32 PF, of which the loop takes 161 and the
-// outputs 17 (without loads and scaling 124 to 137, the card's own limit); what the waves
-// wait for is a block's arrival and its barrier.  1000 x 50001 x 1536, fp32 outputs: 171 us,
-// 0.90 PF.  384 x 4096 x 4096: 14.1 us; its work-groups fetch 655 KB each, 60 to 80 bytes
+// 4096 x 12288 x 4096, fp16 outputs: 174 us, 2.37 PF, of which the loop takes 160 and the
+// outputs 14 (without loads and scaling 124 to 137, the card's own limit); what the waves
+// wait for is a block's arrival and its barrier.  1000 x 50001 x 1536, fp32 outputs: 167 us,
+// 0.92 PF, of which 28 are 200 MB of outputs (widening the codes costs nothing).  384 x 4096 x 4096: 14.1 us; its work-groups fetch 655 KB each, 60 to 80 bytes
 // per ns and CU of the 114 that L2 gives at most.  Not kept, no gain: a second barrier with W
 // two blocks ahead, the next block's fragments carried over the barrier, work-groups that
 // go on from tile to tile; slower: higher wave priority around the products.
@@ -641,12 +705,16 @@ __global__ __launch_bounds__(64 * WT * WN * WK) __attribute__((amdgpu_waves_per_
     }
     if (g == 1) return;
   }
+  // Outputs of more than 80 MiB go past the caches' keeping: 4096 x 12288 x 4096 fp16 173 us
+  // against 184, 1000 x 50001 x 1536 fp32 166 against 179 (with the call that reads them
+  // next, 1 to 2 % slower); 4096 x 8192 x 1024 fp16, 64 MiB, 48 against 42.
+  const bool stream = (uint64_t)p.m * (uint64_t)p.n * sizeof(T) > (uint64_t)80 << 20;
 #pragma unroll
   for (int c = 0; c < TT; ++c) {
     const int64_t i = i0 + wi + 16 * c + lr, j = j0 + wj;
     if constexpr (TN == 4) {
       static_assert(!SPLIT, "split products take narrower tiles");
-      store_row64<(BT == 256), T>((T*)p.Y, p.ld_y, (const T*)p.bias, i, j, q, p.m, p.n, acc[c]);
+      store_rows64<T>((T*)p.Y, p.ld_y, (const T*)p.bias, i - lr, j, lr, q, p.m, p.n, stream, acc[c]);
     } else {
 #pragma unroll
       for (int a = 0; a < TN; ++a) {
