@@ -230,18 +230,21 @@ def _expect(t, name, shape, dtypes, device):
         raise ValueError(f"{name} has overlapping rows")
 
 
+def _end(t, start) -> int:
+    """Address behind the last element of a tensor that starts at ``start``."""
+    if t.is_contiguous():
+        return start + t.numel() * t.element_size()
+    return start + (sum((d - 1) * st for d, st in zip(t.shape, t.stride())) + 1) * t.element_size()
+
+
 def _apart(t, name, *others):
     """An output given by the caller shares no memory with the other tensors of the call."""
-    def span(a):
-        if a.numel() == 0:
-            return 0, 0
-        p = a.data_ptr()
-        return p, p + (sum((d - 1) * st for d, st in zip(a.shape, a.stride())) + 1) * a.element_size()
-    lo, hi = span(t)
+    lo = t.data_ptr()
+    hi = _end(t, lo)
     for o in others:
         if o is not None:
-            a, b = span(o)
-            if a < hi and lo < b:
+            a = o.data_ptr()
+            if a < hi and (a >= lo or _end(o, a) > lo) and o.numel() > 0 and t.numel() > 0:
                 raise ValueError(f"{name} overlaps another tensor of the call")
 
 
