@@ -21,7 +21,7 @@ model.  Biases are left as they are.
 
 Beside it, without calibration: ``quantize_model_fp8`` puts an ``Fp8Linear`` in the place
 of every nn.Linear (e4m3 weights in 128 x 128 tiles, inputs quantized per row on every
-call).  ``evaluate`` judges a model, quantized or not, on given texts: mean negative log
+call).  ``evaluate`` scores a model, quantized or not, on given texts: mean negative log
 probability and perplexity (the pages' loss and perplexity before and after), entropy,
 and how often the given token was the most probable one.
 """
@@ -187,7 +187,7 @@ def quantize_model_fp8(blocks: Sequence) -> List[List[str]]:
 
 @dataclasses.dataclass
 class Evaluation:
-    tokens: int              # judged positions (those with a token >= 0)
+    tokens: int              # scored positions (those with a token >= 0)
     nll: float               # mean negative log probability of the given tokens, in nats
     perplexity: float        # e^nll
     entropy: float           # mean entropy of the model's distributions there, in nats
@@ -196,11 +196,11 @@ class Evaluation:
 
 def evaluate(blocks: Sequence, head, x_batches: Sequence, token_batches: Sequence,
              rows_per_call: int = 8192) -> Evaluation:
-    """Judge a model on given texts.  ``blocks`` map each batch of ``x_batches`` [S x T x d]
+    """Score a model on given texts.  ``blocks`` map each batch of ``x_batches`` [S x T x d]
     on, ``head`` (an nn.Linear, an Fp8Linear, any module) maps hidden rows [rows x d] to
     logits [rows x v] (fp32, fp16 or bf16); ``token_batches`` hold the tokens to be
     predicted there, int64 [S x T], negative where there is none (padding, a text's last
-    position).  The head and the judgement run on at most ``rows_per_call`` rows at a time."""
+    position).  The head and the scores run on at most ``rows_per_call`` rows at a time."""
     if len(x_batches) != len(token_batches):
         raise ValueError("x_batches and token_batches differ in number")
     if rows_per_call < 1:
@@ -221,12 +221,12 @@ def evaluate(blocks: Sequence, head, x_batches: Sequence, token_batches: Sequenc
                 if bool((t >= logits.shape[1]).any()):
                     raise ValueError(f"a token is not below the {logits.shape[1]} logits")
                 lp, entropy, ids, _ = gptq_token_logprobs(logits, t, 1)
-                judged = t >= 0
-                sums += _t.stack([judged.sum().double(), lp.double().sum(),
-                                  entropy.double().masked_fill(~judged, 0.0).sum(),
-                                  ((ids[:, 0] == t) & judged).sum().double()])
+                scored = t >= 0
+                sums += _t.stack([scored.sum().double(), lp.double().sum(),
+                                  entropy.double().masked_fill(~scored, 0.0).sum(),
+                                  ((ids[:, 0] == t) & scored).sum().double()])
     n, lp, entropy, hits = (0.0, 0.0, 0.0, 0.0) if sums is None else sums.tolist()
     if n == 0:
-        raise ValueError("no position holds a token to be judged")
+        raise ValueError("no position holds a token to be scored")
     nll = -lp / n
     return Evaluation(int(n), nll, math.inf if nll >= 700 else math.exp(nll), entropy / n, hits / n)
