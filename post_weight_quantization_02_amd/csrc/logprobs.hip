@@ -169,6 +169,52 @@ __device__ __forceinline__ void insert(Wave& a, const float (&x)[E], int count, 
 // a list entry as one number: larger is better (the key, then the lower index)
 __device__ __forceinline__ uint64_t entry(uint32_t key, int idx) { return ((uint64_t)key << 32) | (uint32_t)~idx; }
 
+// sum over the lanes up to this one
+__device__ __forceinline__ int lanes_up_to(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, true);
+  return v;
+}
+
+// Fills the empty list with the elements above g at once, if they are at most 64: one to a
+// lane, whose place is the number of better ones.  mask: a lane's elements above g, bit
+// u E + e; first(u): index of a lane's element (u, 0); scratch: 64 entries of the wave's own.
+template <typename T, typename First>
+__device__ __forceinline__ bool fill_list(Wave& a, const u32x4 (&found)[kUnroll][64], uint32_t mask, First&& first,
+                                          int top_k, int lane, uint64_t* scratch) {
+  const int c = __popc(mask), upto = lanes_up_to(c), n = (int)lane_value((uint32_t)upto, 63);
+  if (n > 64) return false;
+  int at = upto - c;
+  while (__any(mask != 0u)) {
+    if (mask != 0u) {
+      const int b = __builtin_ctz(mask), u = b / T::E, e = b % T::E;
+      mask &= mask - 1;
+      const float v = T::one(((const typename T::elem*)&found[u][lane])[e]);
+      scratch[at++] = entry(key_of(v), first(u) + e);
+    }
+  }
+  const uint64_t mine = lane < n ? scratch[lane] : 0u;
+  int rank = 0;
+  for (int j = 0; j < n; j += 4) {       // lanes from n on hold 0
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t other = ((uint64_t)lane_value((uint32_t)(mine >> 32), j + i) << 32) | lane_value((uint32_t)mine, j + i);
+      rank += other > mine;
+    }
+  }
+  if (lane < n && rank < top_k) scratch[rank] = mine;
+  if (lane < min(n, top_k)) {
+    const uint64_t e = scratch[lane];
+    a.key = (uint32_t)(e >> 32);
+    a.idx = ~(int)(uint32_t)e;
+  }
+  return true;
+}
+
 // the given token of a row and its logit (0 where there is none)
 struct Given {
   int64_t token;
@@ -270,16 +316,30 @@ __global__ __launch_bounds__(kThreads) void logprob_kernel(LogprobArgs p, int sp
           a.g = value_below(bound);
         }
         // through LDS, so that the rare path is one piece of code for all vectors
+        const auto count = [&](int u) { return edge ? (u == 0 && lane < edges ? 1 : 0) : (b + 64 * u + lane < last ? E : 0); };
+        const auto first_index = [&](int u) {
+          return !edge ? head + (b + 64 * u + lane) * E : lane < head ? lane : tail0 + lane - head;
+        };
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) found[w][u][lane] = ld[u];
+        bool done = false;
+        if (fresh && p.top_k >= 4) {        // of later loads few elements are above g
+          uint32_t mask = 0u;
+#pragma unroll
+          for (int u = 0; u < kUnroll; ++u) {
+            const int n = count(u);
+#pragma unroll
+            for (int e = 0; e < E; ++e) mask |= (e < n && !(f[u][e] <= a.g)) ? 1u << (u * E + e) : 0u;
+          }
+          done = fill_list<T>(a, found[w], mask, first_index, p.top_k, lane, list[w]);
+        }
+        if (!done) {
 #pragma unroll 1
-        for (int u = 0; u < kUnroll; ++u) {
-          const int i = b + 64 * u + lane;
-          float z[E];
-          unpack<T>(found[w][u][lane], z);
-          const int n = edge ? (u == 0 && lane < edges ? 1 : 0) : (i < last ? E : 0);
-          const int i0 = !edge ? head + i * E : lane < head ? lane : tail0 + lane - head;
-          insert<E>(a, z, n, i0, p.top_k, lane);
+          for (int u = 0; u < kUnroll; ++u) {
+            float z[E];
+            unpack<T>(found[w][u][lane], z);
+            insert<E>(a, z, count(u), first_index(u), p.top_k, lane);
+          }
         }
         a.gkey = lane_value(a.key, p.top_k - 1);
         const float kth = value_of(a.gkey);
