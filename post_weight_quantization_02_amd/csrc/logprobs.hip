@@ -14,7 +14,7 @@
 // with its type's lowest value throughout, say) M log2 e would overflow: values that
 // differ then differ by 2^102 or more, and y = 2^-90 (x - M) serves as well.
 //
-// Top tokens: a wave keeps its best 64 (value, index) pairs sorted, one per lane, and
+// Top tokens: a wave keeps its best (value, index) pairs sorted, one per lane, and
 // a bound g; a vector whose maximum is at most g (all but a few, once the list has
 // filled) costs one comparison, which also finds a new M and a NaN.  Before the first
 // vector g comes from the K-th largest of the lanes' maxima over the first loads: K
@@ -35,6 +35,10 @@ namespace {
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr int kUnroll = 2;              // 16-byte vectors per lane and iteration
 constexpr int kMaxTop = 64;
+// lanes with elements for the list from which on it is merged with all of them at once (first
+// loads: 4): 4096 x 65536 bf16 with 20 top tokens 149 us, 160 with 4, 155 never after the
+// first loads, 167 with a lane's elements picked by comparisons in every lane
+constexpr int kMerge = 8;
 constexpr int kMaxSplits = 128;
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 constexpr float kFloor = -1e30f;        // stands for -inf in a product with 2^-inf = 0
@@ -123,8 +127,8 @@ struct Wave {
   Ref ref;              // of the wave
   float s, t;           // per lane
   float g;              // elements at or below g change neither m nor the list
-  uint32_t gkey, key;   // key, idx: entry `lane` of the sorted list
-  int idx;
+  uint32_t gkey;        // key of the list's entry top_k
+  uint64_t best;        // entry `lane` of the sorted list, 0: none
 };
 
 struct Part {
@@ -136,38 +140,28 @@ __device__ __forceinline__ float value_below(uint32_t key) {
   return value_of(key == 0u ? 0u : key == 0x80000000u ? 0x7ffffffeu : key - 1);
 }
 
-// puts the elements above g into the list.  x: a lane's elements, of which the first
-// `count` exist, from index i0 on
-template <int E>
-__device__ __forceinline__ void insert(Wave& a, const float (&x)[E], int count, int i0, int top_k, int lane) {
-  uint32_t mask = 0u;
-#pragma unroll
-  for (int e = 0; e < E; ++e) mask |= (e < count && !(x[e] <= a.g)) ? 1u << e : 0u;
-  while (__any(mask != 0u)) {          // each lane's next element ...
-    uint64_t todo = __ballot(mask != 0u);
-    const int e = mask ? __builtin_ctz(mask) : 0;
-    mask &= mask - 1;
-    float v = x[0];
-#pragma unroll
-    for (int j = 1; j < E; ++j) v = e == j ? x[j] : v;
-    const uint32_t vk = key_of(v);
-    while (todo) {                     // ... lane by lane
-      const int l = __builtin_ctzll(todo);
-      todo &= todo - 1;
-      const uint32_t k = lane_value(vk, l);
-      const int i = (int)lane_value((uint32_t)(i0 + e), l);
-      const int pos = __popcll(__ballot(a.key > k || (a.key == k && a.idx < i)));
-      if (pos >= top_k) continue;
-      const uint32_t pk = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)a.key, 0x138, 0xf, 0xf, false);
-      const int pi = __builtin_amdgcn_update_dpp(0, a.idx, 0x138, 0xf, 0xf, false);
-      a.key = lane < pos ? a.key : lane == pos ? k : pk;
-      a.idx = lane < pos ? a.idx : lane == pos ? i : pi;
-    }
-  }
-}
-
 // a list entry as one number: larger is better (the key, then the lower index)
 __device__ __forceinline__ uint64_t entry(uint32_t key, int idx) { return ((uint64_t)key << 32) | (uint32_t)~idx; }
+
+// Puts the elements above g of one lane's loads into the list: a lane takes one of them.
+// first: index of element 0 of this lane's vector there, negative: none
+template <typename T>
+__device__ __forceinline__ void insert(Wave& a, const u32x4 (&found)[kUnroll][64], int from, int first, int top_k, int lane) {
+  const int u = lane / T::E, e = lane % T::E;
+  const float v = T::one(((const typename T::elem*)&found[u < kUnroll ? u : 0][from])[e]);
+  const uint64_t mine = entry(key_of(v), first + e);
+  uint64_t todo = __ballot(u < kUnroll && first >= 0 && !(v <= a.g));
+  while (todo) {
+    const int l = __builtin_ctzll(todo);
+    todo &= todo - 1;
+    const uint64_t k = ((uint64_t)lane_value((uint32_t)(mine >> 32), l) << 32) | lane_value((uint32_t)mine, l);
+    const int pos = __popcll(__ballot(a.best > k));
+    if (pos >= top_k) continue;
+    const uint64_t before = ((uint64_t)(uint32_t)__builtin_amdgcn_update_dpp(0, (int)(a.best >> 32), 0x138, 0xf, 0xf, false) << 32) |
+                            (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)a.best, 0x138, 0xf, 0xf, false);
+    a.best = lane < pos ? a.best : lane == pos ? k : before;
+  }
+}
 
 // sum over the lanes up to this one
 __device__ __forceinline__ int lanes_up_to(int v) {
@@ -180,15 +174,17 @@ __device__ __forceinline__ int lanes_up_to(int v) {
   return v;
 }
 
-// Fills the empty list with the elements above g at once, if they are at most 64: one to a
-// lane, whose place is the number of better ones.  mask: a lane's elements above g, bit
-// u E + e; first(u): index of a lane's element (u, 0); scratch: 64 entries of the wave's own.
+// Puts all elements above g into the list at once, if they and it are at most 64: one
+// element or entry to a lane, whose place is the number of better ones.  mask: a lane's
+// elements above g, bit u E + e; first(u): index of a lane's element (u, 0); scratch: 64
+// entries of the wave's own.
 template <typename T, typename First>
-__device__ __forceinline__ bool fill_list(Wave& a, const u32x4 (&found)[kUnroll][64], uint32_t mask, First&& first,
-                                          int top_k, int lane, uint64_t* scratch) {
-  const int c = __popc(mask), upto = lanes_up_to(c), n = (int)lane_value((uint32_t)upto, 63);
+__device__ __forceinline__ bool merge(Wave& a, const u32x4 (&found)[kUnroll][64], uint32_t mask, First&& first, int top_k,
+                                      int lane, uint64_t* scratch) {
+  const int c = __popc(mask), upto = lanes_up_to(c);
+  const int held = __popcll(__ballot(lane < top_k && a.best != 0u)), n = held + (int)lane_value((uint32_t)upto, 63);
   if (n > 64) return false;
-  int at = upto - c;
+  int at = held + upto - c;
   while (__any(mask != 0u)) {
     if (mask != 0u) {
       const int b = __builtin_ctz(mask), u = b / T::E, e = b % T::E;
@@ -197,7 +193,7 @@ __device__ __forceinline__ bool fill_list(Wave& a, const u32x4 (&found)[kUnroll]
       scratch[at++] = entry(key_of(v), first(u) + e);
     }
   }
-  const uint64_t mine = lane < n ? scratch[lane] : 0u;
+  const uint64_t mine = lane < held ? a.best : lane < n ? scratch[lane] : 0u;
   int rank = 0;
   for (int j = 0; j < n; j += 4) {       // lanes from n on hold 0
 #pragma unroll
@@ -207,11 +203,7 @@ __device__ __forceinline__ bool fill_list(Wave& a, const u32x4 (&found)[kUnroll]
     }
   }
   if (lane < n && rank < top_k) scratch[rank] = mine;
-  if (lane < min(n, top_k)) {
-    const uint64_t e = scratch[lane];
-    a.key = (uint32_t)(e >> 32);
-    a.idx = ~(int)(uint32_t)e;
-  }
+  a.best = lane < min(n, top_k) ? scratch[lane] : 0u;
   return true;
 }
 
@@ -252,7 +244,7 @@ __device__ __forceinline__ void finish(const LogprobArgs& p, int64_t row, Part r
 __host__ __device__ inline int64_t record_words(int top_k) { return 4 + 2 * top_k; }
 
 template <typename T, bool TOP>
-__global__ __launch_bounds__(kThreads) void logprob_kernel(LogprobArgs p, int splits, int64_t span,
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(8))) void logprob_kernel(LogprobArgs p, int splits, int64_t span,
                                                            uint32_t* __restrict__ ws) {
   constexpr int E = T::E;
   __shared__ float ps[kWaves][3];
@@ -268,7 +260,7 @@ __global__ __launch_bounds__(kThreads) void logprob_kernel(LogprobArgs p, int sp
   const int head = min(v, (int)(((16 - ((uintptr_t)x & 15)) & 15) / sizeof(typename T::elem)));
   const int nvec = (v - head) / E, tail0 = head + nvec * E;
   const u32x4* xv = (const u32x4*)(x + head);
-  Wave a{make_ref(-INFINITY), 0.f, 0.f, TOP ? NAN : -INFINITY, 0u, 0u, 0x7fffffff};
+  Wave a{make_ref(-INFINITY), 0.f, 0.f, TOP ? NAN : -INFINITY, 0u, 0u};
   const int first = (int)min<int64_t>((int64_t)part * span, nvec), last = (int)min<int64_t>(first + span, nvec);
   const int edges = head + v - tail0;
   bool fresh = true, more = part == 0 && w == 0 && edges > 0;
@@ -316,32 +308,34 @@ __global__ __launch_bounds__(kThreads) void logprob_kernel(LogprobArgs p, int sp
           a.g = value_below(bound);
         }
         // through LDS, so that the rare path is one piece of code for all vectors
-        const auto count = [&](int u) { return edge ? (u == 0 && lane < edges ? 1 : 0) : (b + 64 * u + lane < last ? E : 0); };
-        const auto first_index = [&](int u) {
-          return !edge ? head + (b + 64 * u + lane) * E : lane < head ? lane : tail0 + lane - head;
+        // index of element 0 of vector u of a lane, negative: none
+        const auto first_index = [&](int u, int l) {
+          const int i = b + 64 * u + l;
+          return !edge ? (i < last ? head + i * E : -1) : u > 0 || l >= edges ? -1 : l < head ? l : tail0 + l - head;
         };
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) found[w][u][lane] = ld[u];
+        uint64_t lanes = __ballot(!(lm <= a.g));
         bool done = false;
-        if (fresh && p.top_k >= 4) {        // of later loads few elements are above g
+        if (__popcll(lanes) >= (fresh ? 4 : kMerge)) {
           uint32_t mask = 0u;
 #pragma unroll
           for (int u = 0; u < kUnroll; ++u) {
-            const int n = count(u);
+            const int n = first_index(u, lane) < 0 ? 0 : edge ? 1 : E;
 #pragma unroll
             for (int e = 0; e < E; ++e) mask |= (e < n && !(f[u][e] <= a.g)) ? 1u << (u * E + e) : 0u;
           }
-          done = fill_list<T>(a, found[w], mask, first_index, p.top_k, lane, list[w]);
+          done = merge<T>(a, found[w], mask, [&](int u) { return first_index(u, lane); }, p.top_k, lane, list[w]);
         }
         if (!done) {
-#pragma unroll 1
-          for (int u = 0; u < kUnroll; ++u) {
-            float z[E];
-            unpack<T>(found[w][u][lane], z);
-            insert<E>(a, z, count(u), first_index(u), p.top_k, lane);
+          while (lanes) {
+            const int l = __builtin_ctzll(lanes);
+            lanes &= lanes - 1;
+            const int at = first_index(lane / E, l);
+            insert<T>(a, found[w], l, edge && lane % E != 0 ? -1 : at, p.top_k, lane);
           }
         }
-        a.gkey = lane_value(a.key, p.top_k - 1);
+        a.gkey = lane_value((uint32_t)(a.best >> 32), p.top_k - 1);
         const float kth = value_of(a.gkey);
         // the first loads' bound stays until the list has filled
         a.g = a.gkey != 0u ? kth : a.g;
@@ -376,7 +370,7 @@ __global__ __launch_bounds__(kThreads) void logprob_kernel(LogprobArgs p, int sp
     ps[w][1] = a.s;
     ps[w][2] = a.t;
   }
-  const uint64_t mine = entry(a.key, a.idx);
+  const uint64_t mine = a.best;
   if (TOP) {
     list[w][lane] = lane < p.top_k ? mine : 0u;
     if (w == 0) sorted[lane] = 0u;
@@ -394,7 +388,7 @@ __global__ __launch_bounds__(kThreads) void logprob_kernel(LogprobArgs p, int sp
   }
   if (TOP) {
     // an entry's place among the waves' lists is the number of better ones
-    if (lane < p.top_k && a.key != 0u) {
+    if (lane < p.top_k && mine != 0u) {
       int rank = 0;
 #pragma unroll 1
       for (int j = 0; j < p.top_k; j += 2)
