@@ -24,9 +24,10 @@
 // Few long rows: a row is split over work-groups, and a second launch joins the parts in
 // a fixed order.
 //
-// HBM-bound on long texts: 4096 x 65536 bf16 with the top token 98 us, 5.5 TB/s (a large
-// read reaches 5.95); 8192 x 32000 fp16 91 us, 5.7 TB/s.  1 x 128000 bf16 with 20 top tokens
-// 15 us: about 9 in 63 parts, whose selection is a chain of dependent steps, 5.5 in the join.
+// HBM-bound on long texts: 4096 x 65536 bf16 with the top token 94 us, 5.7 TB/s (a large
+// read reaches 5.95); 8192 x 32000 fp16 91 us, 5.7 TB/s.  With 20 top tokens the former takes
+// 149 us: some 70 elements per wave pass its bound.  1 x 128000 bf16 with 20 top tokens 13 us:
+// about 7 in 63 parts, whose selection is a chain of dependent steps, 5.5 in the join.
 #include "gptq_internal.h"
 
 namespace gptq {
@@ -523,10 +524,10 @@ hipError_t launch(const LogprobPlan& plan, const LogprobArgs& p, uint32_t* ws, h
 
 // Parts of a row: at least 2048 elements, together some 2048 work-groups (1024 from 128 rows
 // on), and as many lists as the join's LDS holds.  The second launch pays from rows of about
-// 28 KB on: 1 x 6000 bf16 8.4 us in parts, 6.7 whole; 1 x 40000 8.8 against 12.6; 64 x 6000 fp32
-// with 20 top tokens 15.6 against 15.4, 64 x 9000 15.9 against 18.1.  With more rows than CUs
-// from longer ones on, 512 rows are enough by themselves: 350 x 16000 bf16 14.3 against 12.3,
-// 350 x 50000 20.8 against 22.4, 350 x 128000 32 against 41, 450 x 24000 16.6 against 15.7.
+// 28 KB on: 1 x 6000 bf16 8.1 us in parts, 6.2 whole, 1 x 20000 8.4 against 8.7; 64 x 6000 fp32
+// with 20 top tokens 13.6 against 12.4, 64 x 9000 14.0 against 16.0.  With more rows than CUs
+// from longer ones on, 512 rows are enough by themselves: 350 x 16000 bf16 13.5 against 10.8,
+// 350 x 50000 19.4 against 20.7, 350 x 128000 29 against 39, 500 x 50000 with 20 40.4 against 37.4.
 LogprobPlan logprob_plan(int64_t n, int64_t v, int64_t top_k, int elem_bytes) {
   LogprobPlan p{1, v, 0};
   const int64_t least = (28 << 10) * std::max<int64_t>(1, n / 64 - 2);
