@@ -133,7 +133,10 @@ def test_matmul_parity(m, n, k, out, biased):
                                        (300, 3300, 1150, "f16"), (500, 4100, 520, "bf16"), (100, 8200, 1000, "f16"),
                                        (40, 5000, 2050, "f32"), (64, 4000, 1040, "f16"), (380, 4096, 1280, "f32"), (260, 24580, 257, "f32"), (1025, 10001, 128, "bf16"),
                                        (513, 16500, 384, "f32"), (70, 300, 5000, "f32"), (100, 64, 8192, "f16"),
-                                       (200, 161, 6200, "bf16"), (65, 33, 12345, "f32"), (1030, 20999, 130, "f32")])
+                                       (200, 161, 6200, "bf16"), (65, 33, 12345, "f32"), (1030, 20999, 130, "f32"),
+                                       (24, 9001, 300, "f16"), (31, 8193, 1000, "f32"), (250, 3900, 1000, "bf16"),
+                                       (260, 3000, 400, "f32"), (1, 500, 9000, "f16"), (1, 1000, 8200, "f32"),
+                                       (10, 1000, 12300, "bf16"), (33, 4096, 4100, "f16"), (64, 4096, 4096, "bf16")])
 def test_matmul_parity_large(m, n, k, out):
     """Enough outputs for the largest tiles, with ragged edges on every side."""
     xc, sx, wc, sw = operands(m, n, k, k)

@@ -81,7 +81,10 @@ CASES = [(1, 1, 1, "normal"), (3, 2, 2, "normal"), (2, 7, 0, "normal"), (5, 63, 
          (2, 100, 64, "masked"), (3, 513, 5, "sharp"), (2, 2049, 20, "ends"), (1, 4097, 1, "coarse"), (3, 5000, 20, "equal"),
          (2, 9001, 33, "ascending"), (1, 20011, 20, "masked"), (2, 30000, 64, "shifted"), (1100, 300, 5, "normal"),
          (1030, 2500, 20, "coarse"), (7, 12345, 0, "lowest"), (2, 6000, 7, "lowest"), (4, 5001, 3, "all_lowest"), (3, 3000, 2, "all_largest"),
-         (9, 260, 1, "masked"), (1500, 77, 77 - 20, "coarse"), (3, 70000, 64, "ascending"), (4, 8200, 64, "equal"), (1, 131072, 20, "normal"), (2, 140001, 64, "coarse"), (1, 270000, 32, "masked")]
+         (9, 260, 1, "masked"), (1500, 77, 77 - 20, "coarse"), (3, 70000, 64, "ascending"), (4, 8200, 64, "equal"), (1, 131072, 20, "normal"), (2, 140001, 64, "coarse"), (1, 270000, 32, "masked"),
+         (3, 40001, 20, "ends"), (2, 33000, 7, "lowest"), (3, 50001, 9, "all_lowest"), (2, 30001, 5, "all_largest"),
+         (2, 40000, 20, "equal"), (4, 60001, 3, "sharp"), (130, 16003, 20, "coarse"), (257, 30000, 5, "masked"),
+         (2, 90000, 20, "ascending"), (1, 25000, 64, "normal")]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
@@ -97,7 +100,7 @@ def test_parity(n, v, top, kind, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("v", [40, 3001])
+@pytest.mark.parametrize("v", [40, 3001, 40003])
 def test_rows_without_a_softmax(v, dtype):
     x, tok = make(8, v, 3, dtype)
     inf = float("inf")
@@ -119,14 +122,14 @@ def test_rows_without_a_softmax(v, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
-@pytest.mark.parametrize("off", [0, 1, 3])
-def test_rows_at_any_address(off, dtype):
+@pytest.mark.parametrize("off,v", [(0, 2051), (1, 2051), (3, 2051), (1, 30011), (5, 30011)])
+def test_rows_at_any_address(off, v, dtype):
     """Rows of a wider tensor, starting at every alignment; what lies beside them is
     larger than any logit and must not be seen."""
-    x, tok = make(9, 2051, off, dtype)
-    wide = torch.full((9, 2051 + 7), 1000.0, dtype=x.dtype)
-    wide[:, off:off + 2051] = x
-    got = G.gptq_token_logprobs(wide.cuda()[:, off:off + 2051], tok.cuda(), 6)
+    x, tok = make(9, v, off, dtype)
+    wide = torch.full((9, v + 7), 1000.0, dtype=x.dtype)
+    wide[:, off:off + v] = x
+    got = G.gptq_token_logprobs(wide.cuda()[:, off:off + v], tok.cuda(), 6)
     torch.cuda.synchronize()
     check(x, tok, 6, got)
 
