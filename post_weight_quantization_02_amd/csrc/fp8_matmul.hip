@@ -742,7 +742,9 @@ constexpr int kTile = 128;
 
 // ---------------------------------------------------------------- rows at any address
 // Code rows that do not start at multiples of 16: 128 x 128 outputs per work-group,
-// 4 waves of 64 x 64, the same LDS layout filled through registers by unaligned loads.
+// 4 waves of 64 x 64, the same LDS layout filled through registers by unaligned loads, block
+// after block.  1024 x 4096 x 4096 with rows 4097 bytes apart 115 us, 4096 bytes apart 25: the
+// quantizer's own codes always have aligned rows, and so has whoever wants the speed.
 template <typename T>
 __global__ __launch_bounds__(256) void fp8_tile_kernel(const uint8_t* __restrict__ X, int64_t ld_x,
                                                        const float* __restrict__ sx, int64_t ld_sx,
