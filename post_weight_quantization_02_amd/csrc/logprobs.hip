@@ -8,11 +8,12 @@
 // Both terms of H are non-negative, so a row that is almost certain keeps its small
 // entropy to fp32's absolute precision.  Exponents are taken in base 2 with one rounding,
 // y = fma(x, log2 e, -c), c = M log2 e as rounded: S, T (here sum 2^y y) and the given
-// token's y all refer to the same c, so its rounding, and with it a common offset of the
-// logits, cancels.  A wave keeps one running M; sums move to a new reference as S' = r S,
-// T' = r (T + d S), d = c - c', r = 2^d.  Sums are fp32.  Where |M| >= 2^126 (a row masked
-// with its type's lowest value throughout, say) M log2 e would overflow: values that
-// differ then differ by 2^102 or more, and y = 2^-90 (x - M) serves as well.
+// token's y all refer to the same c, so its rounding cancels.  But that rounding is the
+// y of the maximum itself, up to half a step of c: 1/16 for |M| < 2^20, where it is let be,
+// and 128 or more, past the range of 2^y, from |c| = 2^31 on.  So from |M| = 2^20 on (a row or a
+// part of one masked with -1e9 or -1e30, say) M is taken off first, y = (x - M) log2 e, which
+// costs an instruction per element there and elsewhere a test per step.  A wave keeps one running M; sums move to a new reference as S' = r S,
+// T' = r (T + d S), d the difference of the references, r = 2^d.  Sums are fp32.
 //
 // Top tokens: a wave keeps its best (value, index) pairs sorted, one per lane, and
 // a bound g; a vector whose maximum is at most g (all but a few, once the list has
@@ -43,6 +44,7 @@ constexpr int kMerge = 8;
 constexpr int kMaxSplits = 128;
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 constexpr float kFloor = -1e30f;        // stands for -inf in a product with 2^-inf = 0
+constexpr float kFar = 0x1p20f;         // maxima of at least this magnitude are subtracted first
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 
@@ -105,20 +107,22 @@ __device__ __forceinline__ uint32_t lane_value(uint32_t v, int l) {
   return (uint32_t)__builtin_amdgcn_readlane((int)v, l);
 }
 
-// the reference of a maximum: y = fma(x, scale, -c)
+// the reference of a maximum: y = fma(x - base, log2 e, -c), either base or c being 0
 struct Ref {
-  float m, scale, c;
+  float m, base, c;
 };
 __device__ __forceinline__ Ref make_ref(float m) {
 #pragma clang fp contract(off)      // c as rounded, wherever it is used
-  const float scale = fabsf(m) < 0x1p126f ? kLog2e : 0x1p-90f;
-  return Ref{m, scale, m * scale};
+  return fabsf(m) < kFar ? Ref{m, 0.f, m * kLog2e} : Ref{m, m, 0.f};
 }
+// the maximum's own y
+__device__ __forceinline__ float own_y(const Ref& r) { return r.base == 0.f ? fmaf(r.m, kLog2e, -r.c) : 0.f; }
 
 // moves sums from one reference to another of no smaller maximum
 __device__ __forceinline__ void rescale(float& s, float& t, const Ref& a, const Ref& b) {
   if (!(a.m > -INFINITY)) return;         // nothing summed yet
-  const float d = a.scale == b.scale ? fmaxf(a.c - b.c, kFloor) : kFloor;   // no overflow in t below
+  const float by = a.base == 0.f && b.base == 0.f ? a.c - b.c : fmaf(a.m - b.m, kLog2e, own_y(b) - own_y(a));
+  const float d = fmaxf(by, kFloor);      // no overflow in t below
   const float r = __builtin_amdgcn_exp2f(d);
   t = r * fmaf(d, s, t);
   s *= r;
@@ -227,8 +231,8 @@ __device__ __forceinline__ void finish(const LogprobArgs& p, int64_t row, Part r
   const float log2_s = log2f(r.s);
   const auto log_p = [&](float x) {
     if (!sound) return NAN;
-    const float y = fmaf(x, ref.scale, -ref.c);
-    if (ref.scale != kLog2e || y < kFloor) return (x - r.m) - kLn2 * log2_s;     // beyond y's range, or -inf
+    const float y = fmaf(x - ref.base, kLog2e, -ref.c);
+    if (y < kFloor) return (x - r.m) - kLn2 * log2_s;      // beyond y's range, or -inf
     return kLn2 * (y - log2_s);
   };
   if (t < p.top_k) {
@@ -351,11 +355,17 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(8))) v
       }
     }
     fresh = false;
+    if (__any(a.ref.base != 0.f)) {
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+        for (int e = 0; e < E; ++e) f[u][e] -= a.ref.base;
+    }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const float y = fmaxf(fmaf(f[u][e], a.ref.scale, -a.ref.c), kFloor);
+        const float y = fmaxf(fmaf(f[u][e], kLog2e, -a.ref.c), kFloor);
         const float q = __builtin_amdgcn_exp2f(y);
         a.s += q;
         a.t = fmaf(q, y, a.t);
