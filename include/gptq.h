@@ -338,13 +338,23 @@ gptq_status gptq2d_quantize(const void* X, int32_t x_dtype, int64_t m, int64_t n
  *   leading dimension ld_y >= n) with
  *     Y[i][j] = bias[j] + sum_b x_scales[b * ld_xs + i] * w_scales[(j / 128) * ld_ws + b]
  *                         * sum_{c = 128 b}^{min(128 b + 128, k) - 1} x_codes[i][c] w_codes[j][c]
- *   in fp32, rounded once to y_dtype.  x_codes [device] [m x ld_x], x_scales [device]
- *   float [ceil(k / 128) x ld_xs], ld_xs >= m; w_codes [device] [n x ld_w], w_scales
- *   [device] float [ceil(n / 128) x ld_ws], ld_ws >= ceil(k / 128): the outputs of
- *   gptq_fp8_quantize with block_rows 1 and 128, or any codes and fp32 scales in that
- *   layout.  bias: NULL or [device] n values of y_dtype.  Code rows may start at any
- *   address; with ld_x, ld_w and both base addresses multiples of 16 (and at most 2^22
- *   for ld_x and ld_w, and k >= 128) the product is 3 to 5 times as fast.  m == 0 is a no-op.  Results are bitwise reproducible for a given shape
+ *   rounded once to y_dtype.  Scales, bias and the sum over blocks are taken in fp32; the
+ *   sum inside a block of 128 products goes by y_dtype:
+ *     GPTQ_F32: fp32, off by rounding alone.
+ *     GPTQ_F16, GPTQ_BF16: the 8-bit matrix instruction's own sum.  It adds products in
+ *       groups of 8, each truncated below 2^-13 of its group's largest, so Y is off by up
+ *       to 7 * 2^-13 * sum |scaled products| before it is rounded (1e-5 to 5e-5 of Y's
+ *       norm on random codes, a tenth of fp16's rounding; more than a step of y_dtype
+ *       where products cancel).  Calls of few rows sum in fp32 here too, so a row's last
+ *       places depend on how many rows are in the call.
+ *   A caller who needs fp32 sums takes fp32 outputs, at half the matrix rate.
+ *   x_codes [device] [m x ld_x], x_scales [device] float [ceil(k / 128) x ld_xs], ld_xs >=
+ *   m; w_codes [device] [n x ld_w], w_scales [device] float [ceil(n / 128) x ld_ws], ld_ws
+ *   >= ceil(k / 128): the outputs of gptq_fp8_quantize with block_rows 1 and 128, or any
+ *   codes and fp32 scales in that layout.  bias: NULL or [device] n values of y_dtype.
+ *   Code rows may start at any address; with ld_x, ld_w and both base addresses multiples
+ *   of 16 (and at most 2^22 for ld_x and ld_w, and k >= 128) the product is 3 to 5 times
+ *   as fast.  m == 0 is a no-op.  Results are bitwise reproducible for a given shape, type
  *   and alignment.  ws: >= gptq_fp8_matmul_workspace_size() bytes (may be 0).
  */
 gptq_status gptq_fp8_quantize(const void* X, int32_t x_dtype, int64_t m, int64_t k, int64_t ld_x, int64_t block_rows,

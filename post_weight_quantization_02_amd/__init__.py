@@ -560,8 +560,11 @@ def gptq_fp8_matmul(x_codes, x_scales, w_codes, w_scales, bias=None, Y=None, out
                     stream=None):
     """Y [m x n] = X W^T (+ bias) from e4m3 codes (float8_e4m3fn or uint8 bit patterns)
     x_codes [m x k], w_codes [n x k] and fp32 scales x_scales [ceil(k/128) x m],
-    w_scales [ceil(n/128) x ceil(k/128)]; fp32 sums, rounded once to Y's dtype
-    (``out_dtype``: fp32, fp16 or bf16; fp32 if not given).  bias: n values of that dtype."""
+    w_scales [ceil(n/128) x ceil(k/128)], rounded once to Y's dtype (``out_dtype``: fp32,
+    fp16 or bf16; fp32 if not given).  bias: n values of that dtype.  fp32 outputs are
+    fp32 sums.  fp16 and bf16 outputs of more than a few rows take the 8-bit matrix
+    instruction's sum inside each block of 128 columns, off by up to 7 * 2^-13 sum |x w|
+    before the rounding (1e-5 to 5e-5 of Y's norm on random codes)."""
     torch = _torch()
     _rowmajor(x_codes, "x_codes")
     m, k = x_codes.shape

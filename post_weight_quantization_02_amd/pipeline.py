@@ -131,8 +131,9 @@ def quantize_model(blocks: Sequence, x_batches: Sequence, bits: int, group_size:
 
 class Fp8Linear(_t.nn.Module):
     """A linear layer with e4m3 weights: y = dequantized(x) dequantized(W)^T + bias in
-    x's dtype (fp32, fp16 or bf16), x's rows quantized on every call.  For inference:
-    inputs that ask for a gradient are refused."""
+    x's dtype (fp32, fp16 or bf16; with fp32 the sums are fp32 too, see gptq_fp8_matmul),
+    x's rows quantized on every call.  For inference: inputs that ask for a gradient are
+    refused."""
 
     def __init__(self, weight, bias=None):
         super().__init__()
