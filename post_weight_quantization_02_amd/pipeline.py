@@ -129,6 +129,13 @@ def quantize_model(blocks: Sequence, x_batches: Sequence, bits: int, group_size:
     return results, xs
 
 
+def _own_rows(t):
+    """t [rows x width], copied unless its columns are adjacent and its rows do not overlap."""
+    if t.stride(1) == 1 and (t.shape[0] < 2 or t.stride(0) >= t.shape[1]):
+        return t
+    return t.clone(memory_format=_t.contiguous_format)
+
+
 class Fp8Linear(_t.nn.Module):
     """A linear layer with e4m3 weights: y = dequantized(x) dequantized(W)^T + bias in
     x's dtype (fp32, fp16 or bf16; with fp32 the sums are fp32 too, see gptq_fp8_matmul),
@@ -138,7 +145,7 @@ class Fp8Linear(_t.nn.Module):
     def __init__(self, weight, bias=None):
         super().__init__()
         self.out_features, self.in_features = weight.shape
-        codes, scales = gptq_fp8_quantize(weight.detach(), 128)
+        codes, scales = gptq_fp8_quantize(_own_rows(weight.detach()), 128)
         self.register_buffer("codes", codes.view(_t.uint8))      # bit patterns: a cast of the model leaves them alone
         self.register_buffer("scales", scales)
         self.register_buffer("bias", None if bias is None else bias.detach().clone())
@@ -153,8 +160,7 @@ class Fp8Linear(_t.nn.Module):
     def forward(self, x):
         if x.requires_grad and _t.is_grad_enabled():
             raise ValueError("Fp8Linear has no backward pass: detach its input or call it under torch.no_grad()")
-        rows = x.reshape(-1, self.in_features)
-        codes, scales = gptq_fp8_quantize(rows if rows.stride(-1) == 1 else rows.contiguous())
+        codes, scales = gptq_fp8_quantize(_own_rows(x.reshape(-1, self.in_features)))
         bias = self.bias if self.bias is None or self.bias.dtype == x.dtype else self.bias.to(x.dtype)
         y = gptq_fp8_matmul(codes, scales, self.codes, self.scales, bias, out_dtype=x.dtype)
         return y.reshape(*x.shape[:-1], self.out_features)
