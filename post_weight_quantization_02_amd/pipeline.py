@@ -155,7 +155,20 @@ class Fp8Linear(_t.nn.Module):
         super()._apply(fn, recurse)
         if self.scales.dtype != scales.dtype:       # model.half() and the like: the scales stay fp32
             self.scales = scales.to(self.scales.device)
+        self._align_rows()
         return self
+
+    def _load_from_state_dict(self, *args, **kwargs):
+        super()._load_from_state_dict(*args, **kwargs)
+        self._align_rows()
+
+    def _align_rows(self):
+        """Rows of codes a multiple of 128 bytes apart again, which the product's fast kernels
+        want: a move to another device and some ways of loading close the gaps."""
+        n, k = self.codes.shape
+        if self.codes.stride(0) % 16 or self.codes.stride(1) != 1:
+            codes = self.codes.new_zeros(n, (k + 127) // 128 * 128)[:, :k]
+            self.codes = codes.copy_(self.codes)
 
     def forward(self, x):
         if x.requires_grad and _t.is_grad_enabled():

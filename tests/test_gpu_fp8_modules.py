@@ -47,3 +47,23 @@ def test_weights_of_any_strides(n, k):
     for v in (w, torch.empty(n, 2 * k, device="cuda")[:, ::2].copy_(w), w[:1].expand(n, k), w[:, :1].expand(n, k)):
         own = torch.empty(n, k, device="cuda").copy_(v)
         assert torch.equal(P.Fp8Linear(v)(x), P.Fp8Linear(own)(x))
+
+
+@pytest.mark.parametrize("k", [128, 200, 300])
+def test_rows_of_codes_stay_aligned(k):
+    """The product's fast kernels want rows of codes a multiple of 16 bytes apart."""
+    q = P.Fp8Linear(linear(40, k).weight)
+    x = torch.randn(3, k, device="cuda")
+    ref, at = q(x), q.codes.stride(0)
+    assert at % 16 == 0 and q.codes.shape == (40, k)
+    for step in (lambda m: m.cpu().cuda(), lambda m: m.half(), lambda m: m.to("cpu", torch.float64).to("cuda", torch.float32)):
+        q = step(q)
+        assert q.codes.stride(0) == at and q.scales.dtype == torch.float32 and q.codes.dtype == torch.uint8
+        assert torch.equal(q(x), ref)
+    state = {name: v.contiguous() for name, v in q.state_dict().items()}
+    other = P.Fp8Linear(linear(40, k, 1).weight)
+    other.load_state_dict(state, assign=True)
+    assert other.codes.stride(0) == at and torch.equal(other(x), ref)
+    holder = torch.nn.Sequential(P.Fp8Linear(linear(40, k, 1).weight))
+    holder.load_state_dict({"0." + name: v for name, v in state.items()}, assign=True)
+    assert holder[0].codes.stride(0) == at and torch.equal(holder(x), ref)
