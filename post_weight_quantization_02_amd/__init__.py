@@ -248,8 +248,24 @@ def _apart(t, name, *others):
                 raise ValueError(f"{name} overlaps another tensor of the call")
 
 
-def _grad_error(where):
-    return ValueError(f"{where} has no backward pass: detach its inputs or call it under torch.no_grad()")
+_AUTOGRAD = None
+
+
+def _forward_only(torch, where, *tensors):
+    """Refuses what autograd or a trace would lose without a word: the calls run outside torch."""
+    global _AUTOGRAD
+    if _AUTOGRAD is None:
+        _AUTOGRAD = torch._C._get_tracing_state, torch.autograd.forward_ad
+    tracing, forward = _AUTOGRAD
+    for t in tensors:
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
+            raise ValueError(f"{where} has no backward pass: detach its inputs or call it under torch.no_grad()")
+    if tracing() is not None:
+        raise RuntimeError(f"{where} cannot be traced: its kernels run outside torch's operators")
+    if forward._current_level >= 0:
+        for t in tensors:
+            if t is not None and forward.unpack_dual(t).tangent is not None:
+                raise ValueError(f"{where} has no forward-mode derivative: call it on the primals")
 
 
 def _launch(torch, device, stream, fn, args, tensors, where):
@@ -526,8 +542,7 @@ def gptq_fp8_quantize(X, block_rows: int = 1, codes=None, scales=None, stream=No
     made here have rows a multiple of 128 bytes apart."""
     torch = _torch()
     _rowmajor(X, "X")
-    if X.requires_grad and torch.is_grad_enabled():
-        raise _grad_error("gptq_fp8_quantize")
+    _forward_only(torch, "gptq_fp8_quantize", X)
     code = _elem_code(X, "X")
     m, k = X.shape
     dev = X.device
@@ -578,9 +593,7 @@ def gptq_fp8_matmul(x_codes, x_scales, w_codes, w_scales, bias=None, Y=None, out
     _expect(w_codes, "w_codes", (n, k), fp8, dev)
     _expect(x_scales, "x_scales", (kb, m), (f32,), dev)
     _expect(w_scales, "w_scales", (nb, kb), (f32,), dev)
-    if torch.is_grad_enabled() and (x_scales.requires_grad or w_scales.requires_grad or
-                                    (bias is not None and bias.requires_grad) or (Y is not None and Y.requires_grad)):
-        raise _grad_error("gptq_fp8_matmul")
+    _forward_only(torch, "gptq_fp8_matmul", x_scales, w_scales, bias, Y)
     if Y is None:
         Y, ldy = torch.empty(m, n, dtype=out_dtype or f32, device=dev), n
     else:
@@ -616,8 +629,7 @@ def gptq_token_logprobs(logits, tokens, top_k: int = 0, logprobs=None, entropy=N
     [n x top_k]), fp32 but for the ids."""
     torch = _torch()
     _rowmajor(logits, "logits")
-    if logits.requires_grad and torch.is_grad_enabled():
-        raise _grad_error("gptq_token_logprobs")
+    _forward_only(torch, "gptq_token_logprobs", logits)
     code = _elem_code(logits, "logits")
     n, v = logits.shape
     dev = logits.device

@@ -67,3 +67,29 @@ def test_rows_of_codes_stay_aligned(k):
     holder = torch.nn.Sequential(P.Fp8Linear(linear(40, k, 1).weight))
     holder.load_state_dict({"0." + name: v for name, v in state.items()}, assign=True)
     assert holder[0].codes.stride(0) == at and torch.equal(holder(x), ref)
+
+
+def test_tangents_and_traces_are_refused():
+    """Neither is carried by the calls: refused, not lost without a word."""
+    import torch.autograd.forward_ad as fwd
+    x, w = torch.randn(3, 256, device="cuda"), torch.randn(40, 256, device="cuda")
+    t = torch.zeros(3, dtype=torch.int64, device="cuda")
+    q = P.Fp8Linear(w)
+    xc, xs = G.gptq_fp8_quantize(x)
+    ref, logits = q(x), torch.randn(3, 50, device="cuda")
+    with fwd.dual_level():
+        def dual(v):
+            return fwd.make_dual(v, torch.ones_like(v))
+        for call in (lambda: q(dual(x)), lambda: G.gptq_fp8_quantize(dual(x)),
+                     lambda: G.gptq_fp8_matmul(xc, dual(xs), q.codes, q.scales),
+                     lambda: G.gptq_fp8_matmul(xc, xs, q.codes, dual(q.scales)),
+                     lambda: G.gptq_fp8_matmul(xc, xs, q.codes, q.scales, dual(torch.zeros(40, device="cuda"))),
+                     lambda: G.gptq_token_logprobs(dual(logits), t)):
+            with pytest.raises(ValueError, match="derivative"):
+                call()
+        assert torch.equal(q(x), ref)                       # no tangent: nothing to lose
+    for f, args in ((q, (x,)), (lambda v: G.gptq_fp8_quantize(v)[1], (x,)), (lambda v: G.gptq_token_logprobs(v, t)[0], (logits,)),
+                    (lambda v: G.gptq_fp8_matmul(xc, v, q.codes, q.scales), (xs,))):
+        with pytest.raises(Exception, match="cannot be traced"):
+            torch.jit.trace(f, args)
+    assert torch.equal(q(x), ref)
