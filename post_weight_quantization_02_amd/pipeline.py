@@ -186,8 +186,9 @@ def quantize_model_fp8(blocks: Sequence) -> List[List[str]]:
     """Put an Fp8Linear in the place of every nn.Linear of ``blocks`` (torch modules on
     the GPU), in place.  A layer used under several names stays one layer.  Subclasses of
     nn.Linear stay as they are (nn.MultiheadAttention reads its output projection's weight
-    itself).  All layers are coded before the first one is replaced.  Returns the names of
-    the replaced layers, block by block."""
+    itself), and so do layers whose weight is no parameter of their own but computed on every
+    call (weight_norm, prune).  All layers are coded before the first one is replaced.
+    Returns the names of the replaced layers, block by block."""
     names, made, places = [], {}, []
     for block in blocks:
         if isinstance(block, _t.nn.Linear):
@@ -195,7 +196,7 @@ def quantize_model_fp8(blocks: Sequence) -> List[List[str]]:
         names.append([])
         for parent_name, parent in list(block.named_modules()):
             for name, child in list(parent._modules.items()):     # under every name, a shared layer's too
-                if type(child) is _t.nn.Linear:
+                if type(child) is _t.nn.Linear and "weight" in child._parameters:
                     if id(child) not in made:
                         made[id(child)] = Fp8Linear(child.weight, child.bias)
                     places.append((parent, name, made[id(child)]))

@@ -93,3 +93,15 @@ def test_tangents_and_traces_are_refused():
         with pytest.raises(Exception, match="cannot be traced"):
             torch.jit.trace(f, args)
     assert torch.equal(q(x), ref)
+
+
+def test_layers_whose_weight_is_computed_stay():
+    """A weight that a hook computes from other parameters is not a parameter to be coded once."""
+    normed = torch.nn.utils.weight_norm(linear(32, 32).requires_grad_(True))
+    block = torch.nn.Sequential(normed, linear(32, 32, 1))
+    assert P.quantize_model_fp8([block]) == [["1"]]
+    with torch.no_grad():
+        x = torch.randn(3, 32, device="cuda")
+        y = block[0](x)
+        block[0].weight_g.mul_(2)
+        assert block[0] is normed and torch.allclose(block[0](x) - normed.bias, 2 * (y - normed.bias), rtol=1e-4, atol=1e-5)
