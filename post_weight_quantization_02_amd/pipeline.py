@@ -182,13 +182,25 @@ class Fp8Linear(_t.nn.Module):
         return f"in_features={self.in_features}, out_features={self.out_features}, bias={self.bias is not None}"
 
 
+def _in_place_of(child):
+    """The Fp8Linear of a Linear, with its mode and its forward hooks: the same tables, so a
+    hook's handle still removes it.  Backward hooks have nothing to wait for."""
+    layer = Fp8Linear(child.weight, child.bias)
+    layer.training = child.training
+    for table in ("_forward_pre_hooks", "_forward_pre_hooks_with_kwargs", "_forward_hooks",
+                  "_forward_hooks_with_kwargs", "_forward_hooks_always_called"):
+        setattr(layer, table, getattr(child, table))
+    return layer
+
+
 def quantize_model_fp8(blocks: Sequence) -> List[List[str]]:
     """Put an Fp8Linear in the place of every nn.Linear of ``blocks`` (torch modules on
     the GPU), in place.  A layer used under several names stays one layer.  Subclasses of
     nn.Linear stay as they are (nn.MultiheadAttention reads its output projection's weight
-    itself), and so do layers whose weight is no parameter of their own but computed on every
-    call (weight_norm, prune).  All layers are coded before the first one is replaced.
-    Returns the names of the replaced layers, block by block."""
+    itself), and so do layers whose weight or bias is no parameter of their own but computed on
+    every call (weight_norm, prune).  A layer's mode and forward hooks move to its Fp8Linear.  All
+    layers are coded before the first one is replaced.  Returns the names of the replaced
+    layers, block by block."""
     names, made, places = [], {}, []
     for block in blocks:
         if isinstance(block, _t.nn.Linear):
@@ -196,9 +208,9 @@ def quantize_model_fp8(blocks: Sequence) -> List[List[str]]:
         names.append([])
         for parent_name, parent in list(block.named_modules()):
             for name, child in list(parent._modules.items()):     # under every name, a shared layer's too
-                if type(child) is _t.nn.Linear and "weight" in child._parameters:
+                if type(child) is _t.nn.Linear and {"weight", "bias"} <= child._parameters.keys():
                     if id(child) not in made:
-                        made[id(child)] = Fp8Linear(child.weight, child.bias)
+                        made[id(child)] = _in_place_of(child)
                     places.append((parent, name, made[id(child)]))
                     names[-1].append(f"{parent_name}.{name}" if parent_name else name)
     for parent, name, layer in places:

@@ -95,13 +95,33 @@ def test_tangents_and_traces_are_refused():
     assert torch.equal(q(x), ref)
 
 
+def test_forward_hooks_move_to_the_new_layer():
+    block = torch.nn.Sequential(linear(32, 32), torch.nn.GELU(), linear(32, 32, 1))
+    seen = []
+    pre = block[0].register_forward_pre_hook(lambda m, a: (a[0] * 2,))
+    post = block[0].register_forward_hook(lambda m, a, kw, y: seen.append((type(m), kw)) or y + 1, with_kwargs=True)
+    x = torch.randn(3, 32, device="cuda")
+    block.eval()
+    plain = P.Fp8Linear(block[0].weight, block[0].bias)
+    assert P.quantize_model_fp8([block]) == [["0", "2"]]
+    assert not block[0].training
+    assert torch.equal(block[0](x), plain(x * 2) + 1) and seen == [(P.Fp8Linear, {})]
+    pre.remove()
+    assert torch.equal(block[0](x), plain(x) + 1)
+    post.remove()
+    assert torch.equal(block[0](x), plain(x)) and len(seen) == 2
+
+
 def test_layers_whose_weight_is_computed_stay():
-    """A weight that a hook computes from other parameters is not a parameter to be coded once."""
+    """A weight or bias that a hook computes from other parameters is not one to be coded once."""
+    from torch.nn.utils import prune
     normed = torch.nn.utils.weight_norm(linear(32, 32).requires_grad_(True))
-    block = torch.nn.Sequential(normed, linear(32, 32, 1))
-    assert P.quantize_model_fp8([block]) == [["1"]]
+    pruned = prune.random_unstructured(linear(32, 32, 2).requires_grad_(True), "bias", 0.5)
+    block = torch.nn.Sequential(normed, linear(32, 32, 1), pruned, torch.nn.Linear(32, 32, bias=False, device="cuda"))
+    assert P.quantize_model_fp8([block]) == [["1", "3"]]
     with torch.no_grad():
         x = torch.randn(3, 32, device="cuda")
         y = block[0](x)
         block[0].weight_g.mul_(2)
         assert block[0] is normed and torch.allclose(block[0](x) - normed.bias, 2 * (y - normed.bias), rtol=1e-4, atol=1e-5)
+        assert block(x).shape == (3, 32)
