@@ -237,6 +237,26 @@ def _end(t, start) -> int:
     return start + (sum((d - 1) * st for d, st in zip(t.shape, t.stride())) + 1) * t.element_size()
 
 
+def _share_rows(t, o) -> bool:
+    """Whether two tensors whose address ranges meet share an element.  Rows of one pitch are
+    told apart by their columns; of other layouts the ranges alone are looked at."""
+    def rows(v):             # number of rows, bytes of a row, bytes from row to row
+        z = v.element_size()
+        if v.dim() == 2 and v.shape[0] > 1 and v.stride(1) == 1:
+            return v.shape[0], v.shape[1] * z, v.stride(0) * z
+        return (1, v.numel() * z, 0) if v.is_contiguous() else None
+
+    a, b = rows(t), rows(o)
+    if a is None or b is None or (a[2] and b[2] and a[2] != b[2]):
+        return True
+    pitch = max(a[2], b[2])
+    if pitch == 0 or a[1] > pitch or b[1] > pitch:
+        return True
+    down, right = divmod(o.data_ptr() - t.data_ptr(), pitch)      # o's row 0 against t's
+    return (right < a[1] and down < a[0] and down + b[0] > 0 or
+            right + b[1] > pitch and down + 1 < a[0] and down + 1 + b[0] > 0)
+
+
 def _apart(t, name, *others):
     """An output given by the caller shares no memory with the other tensors of the call."""
     lo = t.data_ptr()
@@ -244,7 +264,7 @@ def _apart(t, name, *others):
     for o in others:
         if o is not None:
             a = o.data_ptr()
-            if a < hi and (a >= lo or _end(o, a) > lo) and o.numel() > 0 and t.numel() > 0:
+            if a < hi and (a >= lo or _end(o, a) > lo) and o.numel() > 0 and t.numel() > 0 and _share_rows(t, o):
                 raise ValueError(f"{name} overlaps another tensor of the call")
 
 

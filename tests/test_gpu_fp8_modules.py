@@ -125,3 +125,17 @@ def test_layers_whose_weight_is_computed_stay():
         block[0].weight_g.mul_(2)
         assert block[0] is normed and torch.allclose(block[0](x) - normed.bias, 2 * (y - normed.bias), rtol=1e-4, atol=1e-5)
         assert block(x).shape == (3, 32)
+
+
+def test_outputs_beside_inputs_in_one_tensor():
+    """Column ranges of one tensor share no memory: taken, with the bits of tensors apart."""
+    x, w = torch.randn(6, 256, device="cuda"), torch.randn(40, 256, device="cuda")
+    ref = G.gptq_fp8_matmul(*G.gptq_fp8_quantize(x), *G.gptq_fp8_quantize(w, 128))
+    both = torch.zeros(6, 1024 + 256 + 160, dtype=torch.uint8, device="cuda")
+    held, codes, y = both[:, :1024].view(torch.float32), both[:, 1024:1280], both[:, 1280:].view(torch.float32)
+    held.copy_(x)
+    _, scales = G.gptq_fp8_quantize(held, codes=codes)
+    G.gptq_fp8_matmul(codes, scales, *G.gptq_fp8_quantize(w, 128), Y=y)
+    assert torch.equal(y, ref) and torch.equal(held, x)
+    with pytest.raises(ValueError, match="overlaps"):
+        G.gptq_fp8_quantize(held, codes=both[:, 1020:1276])
