@@ -311,15 +311,14 @@ def _pitch(t) -> int:
     return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
 
 
-def _ws_ptr(torch, nbytes: int, device, ws):
-    """(tensor or None, address, bytes) of a workspace that may be empty."""
+def _ws_ptr(torch, nbytes: int, device, ws, *inputs):
+    """(tensor, address, bytes) of a workspace; a given one shares no memory with the inputs."""
     if ws is None:
-        if nbytes == 0:
-            return None, None, 0
         ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
         return ws, ws.data_ptr(), nbytes
     if ws.device != device or not ws.is_contiguous():
         raise ValueError(f"ws must be a contiguous tensor on {device}")
+    _apart(ws, "ws", *inputs)
     return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
 
@@ -627,7 +626,9 @@ def gptq_fp8_matmul(x_codes, x_scales, w_codes, w_scales, bias=None, Y=None, out
         b_ptr = bias.data_ptr()
     lib = library()
     need = lib.gptq_fp8_matmul_workspace_size(m, n, k)
-    ws, ws_ptr, ws_bytes = (None, None, 0) if need == 0 and ws is None else _ws_ptr(torch, need, dev, ws)
+    ws_ptr, ws_bytes = None, 0
+    if need > 0 or ws is not None:
+        ws, ws_ptr, ws_bytes = _ws_ptr(torch, need, dev, ws, x_codes, x_scales, w_codes, w_scales, bias)
     _launch(torch, dev, stream, lib.gptq_fp8_matmul,
             (x_codes.data_ptr(), x_codes.stride(0) if m > 1 else k, x_scales.data_ptr(),
              x_scales.stride(0) if kb > 1 else max(m, 1), w_codes.data_ptr(), w_codes.stride(0) if n > 1 else k,
@@ -684,7 +685,9 @@ def gptq_token_logprobs(logits, tokens, top_k: int = 0, logprobs=None, entropy=N
             _apart(t, name, logits, ws, *(o for _, o in contiguous[:i]))
     lib = library()
     need = lib.gptq_token_logprobs_workspace_size(n, v, top_k)
-    ws, ws_ptr, ws_bytes = (None, None, 0) if need == 0 and ws is None else _ws_ptr(torch, need, dev, ws)
+    ws_ptr, ws_bytes = None, 0
+    if need > 0 or ws is not None:
+        ws, ws_ptr, ws_bytes = _ws_ptr(torch, need, dev, ws, logits, tokens)
     _launch(torch, dev, stream, lib.gptq_token_logprobs,
             (logits.data_ptr(), code, n, v, logits.stride(0) if n > 1 else v, tokens.data_ptr(), top_k,
              logprobs.data_ptr(), entropy.data_ptr(), top_ids.data_ptr(), top_logprobs.data_ptr(), ws_ptr, ws_bytes),

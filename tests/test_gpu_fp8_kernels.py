@@ -92,10 +92,12 @@ def test_workspaces_of_the_callers_own():
         assert need > 0
         ref = call(None)
         ws = torch.full((need + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
-        for _ in range(2):
-            got = call(ws[:need])
+        for at in (0, 0, 1000, 77):                          # twice the same, and at an odd address
+            got = call(ws[at:at + need])
             torch.cuda.synchronize()
-            assert all(torch.equal(a, b) for a, b in zip(got, ref)) and (ws[need:] == 0x5A).all()
+            assert all(torch.equal(a, b) for a, b in zip(got, ref)) and (ws[at + need:] == 0x5A).all()
+            assert at == 0 or (ws[:at] == 0x5A).all()
+            ws.fill_(0x5A)
         with pytest.raises(G.GPTQError):
             call(ws[:need - 1])
 

@@ -139,3 +139,17 @@ def test_outputs_beside_inputs_in_one_tensor():
     assert torch.equal(y, ref) and torch.equal(held, x)
     with pytest.raises(ValueError, match="overlaps"):
         G.gptq_fp8_quantize(held, codes=both[:, 1020:1276])
+
+
+def test_workspaces_that_overlap_are_refused():
+    x = torch.randn(3, 50000, device="cuda")
+    t = torch.tensor([1, 2, 3], device="cuda")
+    assert 0 < G.gptq_token_logprobs_workspace_size(3, 50000, 7) < x.numel() * 4
+    with pytest.raises(ValueError, match="overlaps"):
+        G.gptq_token_logprobs(x, t, 7, ws=x)
+    xc, xs = G.gptq_fp8_quantize(torch.randn(100, 5000, device="cuda"))
+    wc, ws = G.gptq_fp8_quantize(torch.randn(160, 5000, device="cuda"), 128)
+    for taken in (xc, xs, wc, ws):
+        whole = torch.empty(0, dtype=torch.uint8, device="cuda").set_(taken.untyped_storage())
+        with pytest.raises(ValueError, match="overlaps"):
+            G.gptq_fp8_matmul(xc, xs, wc, ws, ws=whole)
