@@ -233,12 +233,14 @@ def evaluate(blocks: Sequence, head, x_batches: Sequence, token_batches: Sequenc
     on, ``head`` (an nn.Linear, an Fp8Linear, any module) maps hidden rows [rows x d] to
     logits [rows x v] (fp32, fp16 or bf16); ``token_batches`` hold the tokens to be
     predicted there, int64 [S x T], negative where there is none (padding, a text's last
-    position).  The head and the scores run on at most ``rows_per_call`` rows at a time."""
+    position).  The head and the scores run on at most ``rows_per_call`` rows at a time.  The
+    modules run in the mode they are in: call eval() on those with dropout first.  The device
+    is waited for once, at the end."""
     if len(x_batches) != len(token_batches):
         raise ValueError("x_batches and token_batches differ in number")
     if rows_per_call < 1:
         raise ValueError("rows_per_call must be at least 1")
-    sums = None
+    sums, width = None, 0
     with _t.no_grad():
         for x, tokens in zip(x_batches, token_batches):
             if tokens.shape != x.shape[:-1]:
@@ -247,18 +249,20 @@ def evaluate(blocks: Sequence, head, x_batches: Sequence, token_batches: Sequenc
                 x = block(x)
             hidden, tok = x.reshape(-1, x.shape[-1]), tokens.reshape(-1).contiguous()
             if sums is None:
-                sums = _t.zeros(4, dtype=_t.float64, device=x.device)
+                sums = _t.zeros(5, dtype=_t.float64, device=x.device)
             for i in range(0, hidden.shape[0], rows_per_call):
                 t = tok[i:i + rows_per_call]
                 logits = head(hidden[i:i + rows_per_call])
-                if bool((t >= logits.shape[1]).any()):
-                    raise ValueError(f"a token is not below the {logits.shape[1]} logits")
+                width = logits.shape[1]
                 lp, entropy, ids, _ = gptq_token_logprobs(logits, t, 1)
                 scored = t >= 0
                 sums += _t.stack([scored.sum().double(), lp.double().sum(),
                                   entropy.double().masked_fill(~scored, 0.0).sum(),
-                                  ((ids[:, 0] == t) & scored).sum().double()])
-    n, lp, entropy, hits = (0.0, 0.0, 0.0, 0.0) if sums is None else sums.tolist()
+                                  ((ids[:, 0] == t) & scored).sum().double(),
+                                  (t >= width).sum().double()])       # scored as NaN, refused below
+    n, lp, entropy, hits, above = [0.0] * 5 if sums is None else sums.tolist()
+    if above > 0:
+        raise ValueError(f"a token is not below the {width} logits")
     if n == 0:
         raise ValueError("no position holds a token to be scored")
     nll = -lp / n

@@ -153,3 +153,27 @@ def test_workspaces_that_overlap_are_refused():
         whole = torch.empty(0, dtype=torch.uint8, device="cuda").set_(taken.untyped_storage())
         with pytest.raises(ValueError, match="overlaps"):
             G.gptq_fp8_matmul(xc, xs, wc, ws, ws=whole)
+
+
+def test_evaluate_waits_once():
+    """Several chunks and batches without a wait for the device; tokens out of range are
+    still refused, wherever they stand."""
+    x = [torch.randn(2, 6, 32, device="cuda") for _ in range(2)]
+    t = [torch.zeros(2, 6, dtype=torch.int64, device="cuda") for _ in range(2)]
+    lin, calls = linear(10, 32), []
+
+    def head(rows):
+        calls.append(rows.shape[0])
+        torch.cuda.set_sync_debug_mode("error" if len(calls) < 6 else "default")
+        return lin(rows)
+
+    try:
+        ev = P.evaluate([], head, x, t, rows_per_call=5)
+    finally:
+        torch.cuda.set_sync_debug_mode("default")
+    assert calls == [5, 5, 2] * 2 and ev.tokens == 24
+    for batch, at in ((0, 0), (0, 5), (1, 3)):
+        bad = [v.clone() for v in t]
+        bad[batch][1, at] = 10
+        with pytest.raises(ValueError, match="not below"):
+            P.evaluate([], lin, x, bad, rows_per_call=5)
