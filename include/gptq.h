@@ -338,8 +338,9 @@ gptq_status gptq2d_quantize(const void* X, int32_t x_dtype, int64_t m, int64_t n
  *   leading dimension ld_y >= n) with
  *     Y[i][j] = bias[j] + sum_b x_scales[b * ld_xs + i] * w_scales[(j / 128) * ld_ws + b]
  *                         * sum_{c = 128 b}^{min(128 b + 128, k) - 1} x_codes[i][c] w_codes[j][c]
- *   rounded once to y_dtype.  Scales, bias and the sum over blocks are taken in fp32; the
- *   sum inside a block of 128 products goes by y_dtype:
+ *   rounded once to y_dtype.  The two scales (multiplied with each other first), the bias
+ *   and the sum over blocks are taken in fp32; the sum inside a block of 128 products goes
+ *   by y_dtype:
  *     GPTQ_F32: fp32, off by rounding alone.
  *     GPTQ_F16, GPTQ_BF16: the 8-bit matrix instruction's own sum.  It adds products in
  *       groups of 8, each truncated below 2^-13 of its group's largest, so Y is off by up

@@ -256,9 +256,6 @@ __device__ __forceinline__ void store_rows64(T* __restrict__ Y, int64_t ld_y, co
   }
 }
 
-// sum v (+ bias) over the parts of a split product or the waves of a work-group is
-// always taken in the same order, so results do not depend on timing.
-
 typedef __attribute__((address_space(3))) void lds_void;
 
 // `bytes` bytes from a wave-uniform address
@@ -310,7 +307,8 @@ __device__ __forceinline__ Slot<TT> (&slots())[kFewWaves] {
 }
 
 template <typename T, int TT, int R, bool DMA>
-__global__ __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_per_eu(TT == 4 ? 1 : 2))) void fp8_few_kernel(Fp8Args p) {
+__global__ __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_per_eu(TT == 4 ? 1 : 2))) void
+fp8_few_kernel(Fp8Args p) {
   __shared__ f32x4 part[kFewWaves][TT][64];
   const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
   const int lr = lane & 15, q = lane >> 4;
@@ -440,8 +438,10 @@ __global__ __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_per_eu(
 // 4096 x 12288 x 4096, fp16 outputs: 174 us, 2.37 PF, of which the loop takes 160 and the
 // outputs 14 (without loads and scaling 124 to 137, the card's own limit); what the waves
 // wait for is a block's arrival and its barrier.  1000 x 50001 x 1536, fp32 outputs: 167 us,
-// 0.92 PF, of which 28 are 200 MB of outputs (widening the codes costs nothing).  384 x 4096 x 4096: 14.1 us; its work-groups fetch 655 KB each, 60 to 80 bytes
-// per ns and CU of the 114 that L2 gives at most.  Not kept, no gain: a second barrier with W
+// 0.92 PF, of which 28 are 200 MB of outputs (widening the codes costs nothing).
+// 384 x 4096 x 4096: 14.1 to 16.3 us; its work-groups fetch 655 KB each, 60 to 80 bytes per ns
+// and CU of the 114 that L2 gives at most; 17 % of its L2 reads are misses, the first ones of
+// each XCD, and its waves wait 45 % of their time.  Not kept, no gain: a second barrier with W
 // two blocks ahead, the next block's fragments carried over the barrier, work-groups that
 // go on from tile to tile; slower: higher wave priority around the products.
 // stage I of a kernel's buffers, variables of their own: one for each group of waves
@@ -472,8 +472,8 @@ enum Flow {
 };
 
 template <typename T, bool WIDE, int BT, int BN, int WT, int WN, int WK, int S, Flow FLOW, bool SPLIT>
-__global__ __launch_bounds__(64 * WT * WN * WK) __attribute__((amdgpu_waves_per_eu(2))) void fp8_dma_kernel(Fp8Args p, int tiles_t, int tiles_n, int blocks_per_split,
-                                                               float* __restrict__ parts) {
+__global__ __launch_bounds__(64 * WT * WN * WK) __attribute__((amdgpu_waves_per_eu(2))) void
+fp8_dma_kernel(Fp8Args p, int tiles_t, int tiles_n, int blocks_per_split, float* __restrict__ parts) {
   constexpr int kWavesHere = WT * WN, TT = BT / WT / 16, TN = BN / WN / 16;
   constexpr int kXLoads = BT / 8 / kWavesHere, kWLoads = BN / 8 / kWavesHere;
   static_assert(kXLoads * 8 * kWavesHere == BT && kWLoads * 8 * kWavesHere == BN, "loads divide over the waves");
@@ -507,7 +507,8 @@ __global__ __launch_bounds__(64 * WT * WN * WK) __attribute__((amdgpu_waves_per_
   for (int j = 0; j < kWLoads; ++j)
     wo[j] = (uint32_t)(min((w * kWLoads + j) * 8 + (lane >> 3), rows_w - 1) * p.ld_w) + ch;
   const uint32_t so = 4u * (uint32_t)min(w * kScaleRows + lane, rows_x - 1);
-  uniform_float* swp = (uniform_float*)(uintptr_t)p.sw + ((j0 + wj) / kBlk < (p.n + kBlk - 1) / kBlk ? (j0 + wj) / kBlk : 0) * p.ld_sw;
+  const int64_t tile_w = (j0 + wj) / kBlk;
+  uniform_float* swp = (uniform_float*)(uintptr_t)p.sw + (tile_w < (p.n + kBlk - 1) / kBlk ? tile_w : 0) * p.ld_sw;
   // the rows' scales are X's last load
   const auto fetch_x = [&](StageX<BT>& s, int b, int l) {
     if (l < kXLoads) load16_to_lds(xb, s.x + (w * kXLoads + l) * 8 * kBlk, xo[l], b * kBlk);
@@ -720,14 +721,16 @@ __global__ __launch_bounds__(64 * WT * WN * WK) __attribute__((amdgpu_waves_per_
     } else {
 #pragma unroll
       for (int a = 0; a < TN; ++a) {
-        if constexpr (SPLIT) store4<float>(parts + (int64_t)part * p.m * p.n, p.n, nullptr, i, j + 16 * a + 4 * q, p.m, p.n, acc[c][a]);
+        if constexpr (SPLIT)
+          store4<float>(parts + (int64_t)part * p.m * p.n, p.n, nullptr, i, j + 16 * a + 4 * q, p.m, p.n, acc[c][a]);
         else store4<T>((T*)p.Y, p.ld_y, (const T*)p.bias, i, j + 16 * a + 4 * q, p.m, p.n, acc[c][a]);
       }
     }
   }
 }
 
-// Y from the parts of a product split over k
+// Y from the parts of a product split over k, added in one order whatever the timing, as the
+// sums of a work-group's waves are: results repeat bitwise
 template <typename T>
 __global__ __launch_bounds__(256) void fp8_sum_kernel(Fp8Args p, int splits, const float* __restrict__ parts) {
   const int64_t size = p.m * p.n;
@@ -807,7 +810,8 @@ hipError_t launch_dma(const Fp8Plan& plan, const Fp8Args& p, float* ws, hipStrea
   const int per = (int)cdiv(cdiv(p.k, kBlk), plan.splits);
   if constexpr (BT == 64 && BN == 32) {       // the only tiles of products that are split
     if (plan.splits > 1) {
-      fp8_dma_kernel<T, WIDE, BT, BN, WT, WN, WK, S, FLOW, true><<<tt * tn * plan.splits, 64 * WT * WN * WK, 0, s>>>(p, tt, tn, per, ws);
+      fp8_dma_kernel<T, WIDE, BT, BN, WT, WN, WK, S, FLOW, true>
+          <<<tt * tn * plan.splits, 64 * WT * WN * WK, 0, s>>>(p, tt, tn, per, ws);
       fp8_sum_kernel<T><<<(unsigned)std::min<int64_t>(cdiv(p.m * p.n, 256), 2048), 256, 0, s>>>(p, plan.splits, ws);
       return hipGetLastError();
     }
@@ -874,7 +878,10 @@ hipError_t launch(const Fp8Plan& plan, const Fp8Args& p, float* ws, hipStream_t 
 //     against 41.
 Fp8Plan fp8_plan(int64_t m, int64_t n, int64_t k, bool wide) {
   Fp8Plan p{kFp8Few, 1, 0};
-  const bool few = k > 8192 && n <= 1024 ? false : m <= 16 ? true : m <= 32 ? wide || n <= 8192 : m <= 64 && n <= 4096 && k <= 4096;
+  const bool few = k > 8192 && n <= 1024 ? false
+                   : m <= 16             ? true
+                   : m <= 32             ? wide || n <= 8192
+                                         : m <= 64 && n <= 4096 && k <= 4096;
   if (few) return p;
   const struct { int kind, bt, bn; } small[] = {
       {kFp8T64x32, 64, 32}, {kFp8T64x64, 64, 64}, {kFp8T96x64, 96, 64}, {kFp8T128x64, 128, 64},

@@ -10,10 +10,11 @@
 // y = fma(x, log2 e, -c), c = M log2 e as rounded: S, T (here sum 2^y y) and the given
 // token's y all refer to the same c, so its rounding cancels.  But that rounding is the
 // y of the maximum itself, up to half a step of c: 1/16 for |M| < 2^20, where it is let be,
-// and 128 or more, past the range of 2^y, from |c| = 2^31 on.  So from |M| = 2^20 on (a row or a
-// part of one masked with -1e9 or -1e30, say) M is taken off first, y = (x - M) log2 e, which
-// costs an instruction per element there and elsewhere a test per step.  A wave keeps one running M; sums move to a new reference as S' = r S,
-// T' = r (T + d S), d the difference of the references, r = 2^d.  Sums are fp32.
+// and 128 or more, past the range of 2^y, from |c| = 2^31 on.  So from |M| = 2^20 on (a row
+// or a part of one masked with -1e9 or -1e30, say) M is taken off first, y = (x - M) log2 e,
+// which costs an instruction per element there and elsewhere a test per step.  A wave keeps
+// one running M; sums move to a new reference as S' = r S, T' = r (T + d S), d the
+// difference of the references, r = 2^d.  Sums are fp32.
 //
 // Top tokens: a wave keeps its best (value, index) pairs sorted, one per lane, and
 // a bound g; a vector whose maximum is at most g (all but a few, once the list has
@@ -25,8 +26,8 @@
 // Few long rows: a row is split over work-groups, and a second launch joins the parts in
 // a fixed order.
 //
-// HBM-bound on long texts: 4096 x 65536 bf16 with the top token 94 us, 5.7 TB/s (a large
-// read reaches 5.95); 8192 x 32000 fp16 91 us, 5.7 TB/s.  With 20 top tokens the former takes
+// HBM-bound on long texts: 4096 x 65536 bf16 with the top token 94 to 97 us, 5.6 TB/s (a large
+// read reaches 5.95); 8192 x 32000 fp16 92 to 94 us, 5.6 TB/s.  With 20 top tokens the former takes
 // 149 us: some 70 elements per wave pass its bound.  1 x 128000 bf16 with 20 top tokens 13 us:
 // about 7 in 63 parts, whose selection is a chain of dependent steps, 5.5 in the join.
 #include "gptq_internal.h"
@@ -162,8 +163,8 @@ __device__ __forceinline__ void insert(Wave& a, const u32x4 (&found)[kUnroll][64
     const uint64_t k = ((uint64_t)lane_value((uint32_t)(mine >> 32), l) << 32) | lane_value((uint32_t)mine, l);
     const int pos = __popcll(__ballot(a.best > k));
     if (pos >= top_k) continue;
-    const uint64_t before = ((uint64_t)(uint32_t)__builtin_amdgcn_update_dpp(0, (int)(a.best >> 32), 0x138, 0xf, 0xf, false) << 32) |
-                            (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)a.best, 0x138, 0xf, 0xf, false);
+    const auto left = [](uint32_t v) { return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x138, 0xf, 0xf, false); };
+    const uint64_t before = ((uint64_t)left((uint32_t)(a.best >> 32)) << 32) | left((uint32_t)a.best);
     a.best = lane < pos ? a.best : lane == pos ? k : before;
   }
 }
@@ -249,8 +250,8 @@ __device__ __forceinline__ void finish(const LogprobArgs& p, int64_t row, Part r
 __host__ __device__ inline int64_t record_words(int top_k) { return 4 + 2 * top_k; }
 
 template <typename T, bool TOP>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(8))) void logprob_kernel(LogprobArgs p, int splits, int64_t span,
-                                                           uint32_t* __restrict__ ws) {
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(8))) void
+logprob_kernel(LogprobArgs p, int splits, int64_t span, uint32_t* __restrict__ ws) {
   constexpr int E = T::E;
   __shared__ float ps[kWaves][3];
   __shared__ __attribute__((aligned(16))) uint64_t list[kWaves][kMaxTop];     // 0: no entry
