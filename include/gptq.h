@@ -56,14 +56,16 @@ typedef enum {
   GPTQ_ERR_BAD_DAMP = 9,        /* percdamp negative or not finite        */
   GPTQ_ERR_LAUNCH = 10,         /* a HIP launch or runtime call failed    */
   GPTQ_ERR_TOO_LARGE = 11,      /* a size exceeds the library's limits    */
-  GPTQ_ERR_SCRATCH = 12         /* shape too large for the no-allocation  */
+  GPTQ_ERR_SCRATCH = 12,        /* shape too large for the no-allocation  */
                                 /* entry point's fixed workspace          */
+  GPTQ_ERR_BAD_TEMPERATURE = 13 /* temperature outside [1e-4, 1e4]        */
 } gptq_status;
 
 typedef enum {
   GPTQ_F32 = 0, /* IEEE binary32 */
   GPTQ_F16 = 1, /* IEEE binary16 */
-  GPTQ_BF16 = 2 /* bfloat16: the gptq_fp8_* and gptq_token_logprobs calls only */
+  GPTQ_BF16 = 2 /* bfloat16: the gptq_fp8_*, gptq_int8_*, gptq_token_logprobs and
+                   gptq_distill_loss calls only */
 } gptq_dtype;
 
 /*
@@ -389,6 +391,97 @@ size_t gptq_token_logprobs_workspace_size(int64_t n, int64_t v, int64_t top_k);
 gptq_status gptq_token_logprobs(const void* logits, int32_t dtype, int64_t n, int64_t v, int64_t ld, const int64_t* tokens,
                                 int64_t top_k, float* logprobs, float* entropy, int32_t* top_ids, float* top_logprobs,
                                 void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * 8-bit integer layers: int8 codes with one fp32 scale per row -- of activations (a token)
+ * or of weights (a channel).  Nothing is calibrated; the product's sums are whole numbers
+ * and exact.  Outputs and workspaces share no memory with inputs or with each other, in
+ * these calls and in gptq_distill_loss.
+ *
+ * gptq_int8_quantize: X [device] [m x k] (x_dtype GPTQ_F32, GPTQ_F16 or GPTQ_BF16, leading
+ *   dimension ld_x >= k) -> codes [device] int8 [m x ld_codes] (ld_codes >= k; bytes past
+ *   column k are left as they are) and scales [device] float [m], with X ~ scale * code.
+ *   Per row: a = max(max |x|, 2^-100), scale = a / 127, code = x * (127 * (1 / a)) to the
+ *   nearest whole number, halves to even, each quotient and product rounded to fp32 first;
+ *   |code| <= 127.  A row that holds a NaN or an infinity has scale NaN and codes 0.
+ *   m == 0 is a no-op.
+ *
+ * gptq_int8_matmul: Y [device] [m x n] (y_dtype GPTQ_F32, GPTQ_F16 or GPTQ_BF16, leading
+ *   dimension ld_y >= n) with
+ *     Y[i][j] = bias[j] + x_scales[i] * w_scales[j] * sum_c x_codes[i][c] w_codes[j][c]
+ *   rounded once to y_dtype.  The sum is exact (k < 2^17); its conversion to fp32 and its
+ *   product with x_scales[i] are rounded to fp32, and so is the fused step
+ *   (times w_scales[j], plus bias[j]).  Results depend on nothing else: not on the other
+ *   rows of the call, the layout or the alignment.  x_codes [device] int8 [m x ld_x], x_scales
+ *   [device] float [m], w_codes [device] int8 [n x ld_w], w_scales [device] float [n]: the
+ *   outputs of gptq_int8_quantize, or any codes (-128 too) and scales.  bias: NULL or
+ *   [device] n values of y_dtype.  Code rows may start at any address; with ld_x, ld_w and
+ *   both base addresses multiples of 16 (and at most 2^22 for ld_x and ld_w, and k >= 128)
+ *   the product is several times as fast.  m == 0 is a no-op.  ws: >=
+ *   gptq_int8_matmul_workspace_size() bytes (may be 0).
+ *
+ * gptq_int8_matmul_grouped: the same with a stack of `experts` weights (at most 2^16), for m
+ *   positions sorted by expert: positions offsets[e] <= i < offsets[e + 1] belong to expert e
+ *   and take row r = rows[i] of X (rows NULL: r = i):
+ *     Y[i][j] = bias[e][j] + x_scales[r] * w_scales[e][j] * sum_c x_codes[r][c] w_codes[e][j][c]
+ *   with the roundings of gptq_int8_matmul.  Y [device] [m x n]; x_codes [device] int8
+ *   [rows_x x ld_x], x_scales [device] float [rows_x] (rows NULL: rows_x >= m); rows [device]
+ *   int32 [m]; offsets [device] int32 [experts + 1], not decreasing; w_codes [device] int8,
+ *   expert e from w_codes + e * stride_w on, rows ld_w apart (stride_w >= n * ld_w, or
+ *   experts == 1); w_scales [device] float [experts x n]; bias NULL or [device] [experts x n]
+ *   values of y_dtype.  Rows of Y before offsets[0] and from offsets[experts] on are left as
+ *   they are.  A rows[i] outside [0, rows_x) gives a row of NaN; offsets outside [0, m] are
+ *   taken as the nearer end, and where they decrease the rows concerned are unspecified.
+ *   The sizes of the experts' parts are not needed on the host.  No workspace.
+ */
+gptq_status gptq_int8_quantize(const void* X, int32_t x_dtype, int64_t m, int64_t k, int64_t ld_x, int8_t* codes,
+                               int64_t ld_codes, float* scales, void* stream);
+size_t gptq_int8_matmul_workspace_size(int64_t m, int64_t n, int64_t k);
+gptq_status gptq_int8_matmul(const int8_t* x_codes, int64_t ld_x, const float* x_scales, const int8_t* w_codes,
+                             int64_t ld_w, const float* w_scales, int64_t m, int64_t n, int64_t k, const void* bias,
+                             void* Y, int32_t y_dtype, int64_t ld_y, void* ws, size_t ws_bytes, void* stream);
+gptq_status gptq_int8_matmul_grouped(const int8_t* x_codes, int64_t ld_x, const float* x_scales, int64_t rows_x,
+                                     const int32_t* rows, int64_t m, const int32_t* offsets, int64_t experts,
+                                     const int8_t* w_codes, int64_t ld_w, int64_t stride_w, const float* w_scales,
+                                     int64_t n, int64_t k, const void* bias, void* Y, int32_t y_dtype, int64_t ld_y,
+                                     void* stream);
+
+/*
+ * How far a (quantized) model's distributions are from those of the model that it was made
+ * from, of which the top tokens are known, and the gradient by which what is left in
+ * floating point can be tuned towards it.
+ *
+ * gptq_distill_loss: logits [device] [n x v] (dtype GPTQ_F32, GPTQ_F16 or GPTQ_BF16, leading
+ *   dimension ld >= v); ids [device] int32 [n x top_k] and logprobs [device] float [n x
+ *   top_k], 1 <= top_k <= min(v, GPTQ_MAX_TOP): the teacher's tokens and log probabilities,
+ *   as top_ids and top_logprobs of gptq_token_logprobs; an entry with a negative id is none.
+ *   With p = softmax(logits[i] / temperature), temperature in [1e-4, 1e4], per row
+ *     loss[i] = sum_j q_j (log q_j - log p(ids[i][j])) + q_r (log q_r - log p_r)
+ *   in nats, terms of q = 0 left out.
+ *     tail == 0: q = softmax over the listed tokens of logprobs[i][j] / temperature (logits
+ *                do as well: a constant cancels); q_r = 0.
+ *     tail != 0: q_j = exp(logprobs[i][j]), log probabilities at that temperature already;
+ *                q_r = max(0, 1 - sum_j q_j) and p_r stand for all tokens that are not listed
+ *                together (top_k < v).  The loss is then never negative, 0 where the models
+ *                agree, and at most the divergence over all tokens.
+ *   A token that is listed twice counts with both its entries in q and once in p.
+ *   grad: NULL, or [device] [n x ld_grad] (ld_grad >= v) of the logits' type: weights[i] (1
+ *   where weights is NULL; [device] float [n]) times the gradient of loss[i]:
+ *     Q = sum_j q_j + q_r;  listed tokens (Q p - q) / temperature, others p (Q - q_r / p_r) /
+ *     temperature.
+ *   A row without entries has loss and gradient 0, a row of weight 0 gradient 0, whatever the
+ *   logits hold.  A logit of -inf is a token of probability 0; where the teacher gives one
+ *   some probability the loss is infinite, and the others' gradient NaN where it is all of
+ *   the rest.  A row whose logits hold a NaN or +inf, or nothing but -inf, whose log
+ *   probabilities hold a NaN or +inf (tail == 0: or nothing but -inf), or with an id >= v, has
+ *   loss and gradient NaN.  n == 0 is a no-op.  fp32 sums; bitwise reproducible for a given
+ *   shape and type.  ws: >= gptq_distill_loss_workspace_size() bytes (may be 0).
+ */
+size_t gptq_distill_loss_workspace_size(int64_t n, int64_t v);
+gptq_status gptq_distill_loss(const void* logits, int32_t dtype, int64_t n, int64_t v, int64_t ld, const int32_t* ids,
+                              const float* logprobs, int64_t top_k, float temperature, int32_t tail,
+                              const float* weights, float* loss, void* grad, int64_t ld_grad, void* ws, size_t ws_bytes,
+                              void* stream);
 
 /*
  * Per-launch timing of the quantization loop -- a measurement aid, off by

@@ -10,3 +10,4 @@ from .gptq_oracle import (GPTQResult, LayerSolution, NotPositiveDefinite,  # noq
 from . import model_pipeline  # noqa: F401,E402
 from . import gptq2d  # noqa: F401,E402
 from . import fp8  # noqa: F401
+from . import int8, distill  # noqa: F401

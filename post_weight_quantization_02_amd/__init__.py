@@ -29,13 +29,15 @@ __all__ = [
     "gptq2d_quantize", "gptq2d_quantize_workspace_size",
     "GPTQ_BF16", "GPTQ_MAX_TOP", "gptq_fp8_quantize", "gptq_fp8_matmul", "gptq_fp8_matmul_workspace_size",
     "gptq_token_logprobs", "gptq_token_logprobs_workspace_size",
+    "gptq_int8_quantize", "gptq_int8_matmul", "gptq_int8_matmul_workspace_size", "gptq_int8_matmul_grouped",
+    "gptq_distill_loss", "gptq_distill_loss_workspace_size",
     "gptq_launch_timing", "gptq_launch_timing_read", "TIMING_PANEL", "TIMING_PRODUCT",
     "gptq_status_string", "gptq_version", "quantize_layer",
 ]
 
 GPTQ_F32 = 0
 GPTQ_F16 = 1
-GPTQ_BF16 = 2                           # the fp8 and log-probability calls only
+GPTQ_BF16 = 2                           # the fp8, int8, log-probability and distillation calls only
 GPTQ_MAX_TOP = 64                       # include/gptq.h
 GPTQ_NOALLOC_SCRATCH_BYTES = 96 << 20   # include/gptq.h
 TIMING_PANEL, TIMING_PRODUCT = 0, 1     # kinds of gptq_launch_timing_read
@@ -120,6 +122,19 @@ def library() -> ctypes.CDLL:
     lib.gptq_token_logprobs_workspace_size.restype = sz
     lib.gptq_token_logprobs.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, vp, vp, vp, vp, sz, vp]
     lib.gptq_token_logprobs.restype = i32
+    lib.gptq_int8_quantize.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, vp]
+    lib.gptq_int8_quantize.restype = i32
+    lib.gptq_int8_matmul_workspace_size.argtypes = [i64, i64, i64]
+    lib.gptq_int8_matmul_workspace_size.restype = sz
+    lib.gptq_int8_matmul.argtypes = [vp, i64, vp, vp, i64, vp, i64, i64, i64, vp, vp, i32, i64, vp, sz, vp]
+    lib.gptq_int8_matmul.restype = i32
+    lib.gptq_int8_matmul_grouped.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i64, vp, i64, i64, vp, vp, i32,
+                                             i64, vp]
+    lib.gptq_int8_matmul_grouped.restype = i32
+    lib.gptq_distill_loss_workspace_size.argtypes = [i64, i64]
+    lib.gptq_distill_loss_workspace_size.restype = sz
+    lib.gptq_distill_loss.argtypes = [vp, i32, i64, i64, i64, vp, vp, i64, ctypes.c_float, i32, vp, vp, vp, i64, vp, sz, vp]
+    lib.gptq_distill_loss.restype = i32
     lib.gptq_launch_timing.argtypes = [i32]
     lib.gptq_launch_timing.restype = i32
     lib.gptq_launch_timing_read.argtypes = [i32, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(i64),
@@ -203,7 +218,7 @@ _ELEM = {}
 
 
 def _elem_code(t, name) -> int:
-    """Element type of the fp8 and log-probability calls."""
+    """Element type of the calls that take fp32, fp16 and bf16."""
     if not _ELEM:
         torch = _torch()
         _ELEM.update({torch.float32: GPTQ_F32, torch.float16: GPTQ_F16, torch.bfloat16: GPTQ_BF16})
@@ -693,6 +708,193 @@ def gptq_token_logprobs(logits, tokens, top_k: int = 0, logprobs=None, entropy=N
              logprobs.data_ptr(), entropy.data_ptr(), top_ids.data_ptr(), top_logprobs.data_ptr(), ws_ptr, ws_bytes),
             (logits, tokens, logprobs, entropy, top_ids, top_logprobs, ws), "gptq_token_logprobs")
     return logprobs, entropy, top_ids, top_logprobs
+
+
+def gptq_int8_quantize(X, codes=None, scales=None, stream=None):
+    """int8 codes of X [m x k] (fp32, fp16 or bf16) with one fp32 scale per row: a row is a
+    token's activations or a channel's weights.  Returns (codes int8 [m x k], scales [m]),
+    X ~ scales[:, None] * codes.  A row with a NaN or an infinity has scale NaN.  The codes
+    made here have rows a multiple of 128 bytes apart."""
+    torch = _torch()
+    _rowmajor(X, "X")
+    _forward_only(torch, "gptq_int8_quantize", X)
+    code = _elem_code(X, "X")
+    m, k = X.shape
+    dev = X.device
+    if codes is None:
+        ldc = (k + 127) // 128 * 128
+        codes = torch.empty_strided((m, k), (ldc, 1), dtype=torch.int8, device=dev)
+    else:
+        _expect(codes, "codes", (m, k), (torch.int8,), dev)
+        _apart(codes, "codes", X, scales)
+        ldc = _pitch(codes)
+    if scales is None:
+        scales = torch.empty(m, dtype=torch.float32, device=dev)
+    else:
+        _expect(scales, "scales", (m,), (torch.float32,), dev)
+        _apart(scales, "scales", X)
+    _launch(torch, dev, stream, library().gptq_int8_quantize,
+            (X.data_ptr(), code, m, k, X.stride(0) if m > 1 else k, codes.data_ptr(), max(ldc, k), scales.data_ptr()),
+            (X, codes, scales), "gptq_int8_quantize")
+    return codes, scales
+
+
+def gptq_int8_matmul_workspace_size(m: int, n: int, k: int) -> int:
+    return int(library().gptq_int8_matmul_workspace_size(m, n, k))
+
+
+def gptq_int8_matmul(x_codes, x_scales, w_codes, w_scales, bias=None, Y=None, out_dtype=None, ws=None, stream=None):
+    """Y [m x n] = X W^T (+ bias) from int8 codes x_codes [m x k], w_codes [n x k] (k < 2^17)
+    and fp32 scales x_scales [m], w_scales [n], rounded once to Y's dtype (``out_dtype``: fp32,
+    fp16 or bf16; fp32 if not given).  bias: n values of that dtype.  The sums are exact, so
+    a row's result depends neither on the other rows nor on the layout."""
+    torch = _torch()
+    _rowmajor(x_codes, "x_codes")
+    m, k = x_codes.shape
+    dev = x_codes.device
+    if w_codes.dim() != 2:
+        raise ValueError("w_codes must be a 2-D tensor")
+    n = w_codes.shape[0]
+    i8, f32 = (torch.int8,), torch.float32
+    _expect(x_codes, "x_codes", (m, k), i8, dev)
+    _expect(w_codes, "w_codes", (n, k), i8, dev)
+    _expect(x_scales, "x_scales", (m,), (f32,), dev)
+    _expect(w_scales, "w_scales", (n,), (f32,), dev)
+    _forward_only(torch, "gptq_int8_matmul", x_scales, w_scales, bias, Y)
+    if Y is None:
+        Y, ldy = torch.empty(m, n, dtype=out_dtype or f32, device=dev), n
+    else:
+        _expect(Y, "Y", (m, n), (out_dtype or Y.dtype,), dev)
+        _apart(Y, "Y", x_codes, x_scales, w_codes, w_scales, bias, ws)
+        ldy = _pitch(Y)
+    y_code = _elem_code(Y, "Y")
+    b_ptr = None
+    if bias is not None:
+        _expect(bias, "bias", (n,), (Y.dtype,), dev)
+        b_ptr = bias.data_ptr()
+    lib = library()
+    need = lib.gptq_int8_matmul_workspace_size(m, n, k)
+    ws_ptr, ws_bytes = None, 0
+    if need > 0 or ws is not None:
+        ws, ws_ptr, ws_bytes = _ws_ptr(torch, need, dev, ws, x_codes, x_scales, w_codes, w_scales, bias)
+    _launch(torch, dev, stream, lib.gptq_int8_matmul,
+            (x_codes.data_ptr(), x_codes.stride(0) if m > 1 else k, x_scales.data_ptr(), w_codes.data_ptr(),
+             w_codes.stride(0) if n > 1 else k, w_scales.data_ptr(), m, n, k, b_ptr, Y.data_ptr(), y_code, ldy, ws_ptr,
+             ws_bytes), (x_codes, x_scales, w_codes, w_scales, bias, Y, ws), "gptq_int8_matmul")
+    return Y
+
+
+def gptq_int8_matmul_grouped(x_codes, x_scales, w_codes, w_scales, offsets, rows=None, bias=None, Y=None, out_dtype=None,
+                             stream=None):
+    """The product by expert: for positions i with offsets[e] <= i < offsets[e + 1] (offsets
+    int32 [experts + 1] on the device, not decreasing) row i of Y is row rows[i] of X (int32,
+    or row i without ``rows``) times the weights of expert e, w_codes [experts x n x k] and
+    w_scales [experts x n], plus bias[e] (bias [experts x n] of Y's dtype).  Y has a row per
+    position: as many as ``rows``, or x_codes, has.  Rows of Y that belong to no expert are left
+    as they are (in a tensor made here: undefined); a row of X out of range gives NaN."""
+    torch = _torch()
+    _rowmajor(x_codes, "x_codes")
+    rows_x, k = x_codes.shape
+    dev = x_codes.device
+    if w_codes.dim() != 3:
+        raise ValueError("w_codes must be a 3-D tensor")
+    experts, n = w_codes.shape[:2]
+    i8, f32, i32 = (torch.int8,), torch.float32, (torch.int32,)
+    _expect(x_codes, "x_codes", (rows_x, k), i8, dev)
+    _expect(w_codes, "w_codes", (experts, n, k), i8, dev)
+    ld_w = w_codes.stride(1) if n > 1 else k
+    stride_w = w_codes.stride(0) if experts > 1 else n * ld_w
+    if ld_w < k or stride_w < n * ld_w:
+        raise ValueError("w_codes has overlapping rows")
+    _expect(x_scales, "x_scales", (rows_x,), (f32,), dev)
+    _expect(w_scales, "w_scales", (experts, n), (f32,), dev)
+    _expect(offsets, "offsets", (experts + 1,), i32, dev)
+    m, r_ptr = rows_x, None
+    if rows is not None:
+        if rows.dim() != 1:
+            raise ValueError("rows must be a 1-D tensor")
+        m = rows.shape[0]
+        _expect(rows, "rows", (m,), i32, dev)
+        r_ptr = rows.data_ptr()
+    _forward_only(torch, "gptq_int8_matmul_grouped", x_scales, w_scales, bias, Y)
+    if Y is None:
+        Y, ldy = torch.empty(m, n, dtype=out_dtype or f32, device=dev), n
+    else:
+        _expect(Y, "Y", (m, n), (out_dtype or Y.dtype,), dev)
+        _apart(Y, "Y", x_codes, x_scales, w_codes, w_scales, offsets, rows, bias)
+        ldy = _pitch(Y)
+    y_code = _elem_code(Y, "Y")
+    b_ptr = None
+    if bias is not None:
+        _expect(bias, "bias", (experts, n), (Y.dtype,), dev)
+        b_ptr = bias.data_ptr()
+    for t, name in ((w_scales, "w_scales"), (bias, "bias")):
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    _launch(torch, dev, stream, library().gptq_int8_matmul_grouped,
+            (x_codes.data_ptr(), x_codes.stride(0) if rows_x > 1 else k, x_scales.data_ptr(), rows_x, r_ptr, m,
+             offsets.data_ptr(), experts, w_codes.data_ptr(), ld_w, stride_w, w_scales.data_ptr(), n, k, b_ptr,
+             Y.data_ptr(), y_code, ldy), (x_codes, x_scales, w_codes, w_scales, offsets, rows, bias, Y),
+            "gptq_int8_matmul_grouped")
+    return Y
+
+
+def gptq_distill_loss_workspace_size(n: int, v: int) -> int:
+    return int(library().gptq_distill_loss_workspace_size(n, v))
+
+
+def gptq_distill_loss(logits, ids, logprobs, temperature: float = 1.0, tail: bool = False, weights=None,
+                      want_grad: bool = False, loss=None, grad=None, ws=None, stream=None):
+    """Per row of logits [n x v] (fp32, fp16 or bf16) the divergence from a teacher's top
+    tokens, ids int32 [n x top] (negative: no entry) and logprobs fp32 [n x top] as
+    gptq_token_logprobs gives them: sum_j q_j (log q_j - log p(ids_j)), p = softmax(logits /
+    temperature).  q is softmax(logprobs / temperature); with ``tail`` exp(logprobs) and, for
+    all other tokens together, what is missing to 1.  Returns (loss fp32 [n], grad): grad, of
+    logits' shape and dtype, is the loss's gradient times weights (fp32 [n]; 1 if not given)
+    where ``want_grad`` or a tensor for it is given, else None.  Rows without entries have loss
+    and gradient 0, rows of weight 0 gradient 0.  pipeline.distill_loss is the same for
+    autograd."""
+    torch = _torch()
+    _rowmajor(logits, "logits")
+    _forward_only(torch, "gptq_distill_loss", logits, logprobs, weights)
+    code = _elem_code(logits, "logits")
+    n, v = logits.shape
+    dev = logits.device
+    f32 = (torch.float32,)
+    if ids.dim() != 2:
+        raise ValueError("ids must be a 2-D tensor")
+    top = ids.shape[1]
+    _expect(ids, "ids", (n, top), (torch.int32,), dev)
+    _expect(logprobs, "logprobs", (n, top), f32, dev)
+    if not (ids.is_contiguous() and logprobs.is_contiguous()):
+        raise ValueError("ids and logprobs must be contiguous")
+    w_ptr = None
+    if weights is not None:
+        _expect(weights, "weights", (n,), f32, dev)
+        w_ptr = weights.data_ptr()
+    if loss is None:
+        loss = torch.empty(n, dtype=torch.float32, device=dev)
+    else:
+        _expect(loss, "loss", (n,), f32, dev)
+        _apart(loss, "loss", logits, ids, logprobs, weights, grad, ws)
+    g_ptr, ldg = None, v
+    if grad is not None:
+        _expect(grad, "grad", (n, v), (logits.dtype,), dev)
+        _apart(grad, "grad", logits, ids, logprobs, weights, ws)
+        g_ptr, ldg = grad.data_ptr(), _pitch(grad)
+    elif want_grad:
+        grad = torch.empty(n, v, dtype=logits.dtype, device=dev)
+        g_ptr = grad.data_ptr()
+    lib = library()
+    need = lib.gptq_distill_loss_workspace_size(n, v)
+    ws_ptr, ws_bytes = None, 0
+    if need > 0 or ws is not None:
+        ws, ws_ptr, ws_bytes = _ws_ptr(torch, need, dev, ws, logits, ids, logprobs, weights)
+    _launch(torch, dev, stream, lib.gptq_distill_loss,
+            (logits.data_ptr(), code, n, v, logits.stride(0) if n > 1 else v, ids.data_ptr(), logprobs.data_ptr(), top,
+             float(temperature), 1 if tail else 0, w_ptr, loss.data_ptr(), g_ptr, ldg, ws_ptr, ws_bytes),
+            (logits, ids, logprobs, weights, loss, grad, ws), "gptq_distill_loss")
+    return loss, grad
 
 
 def gptq_launch_timing(enable: bool) -> None:

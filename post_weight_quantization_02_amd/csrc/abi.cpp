@@ -14,6 +14,9 @@ namespace {
 
 constexpr int64_t kMaxDim = int64_t(1) << 20;        // d_col and d_row limits
 constexpr int64_t kMaxElems = int64_t(1) << 40;
+constexpr int64_t kMaxRows = int64_t(1) << 30;       // rows of int8 codes
+constexpr int64_t kMaxInt8Sum = (int64_t(1) << 17) - 1;      // 2^14 times this stays below 2^31
+constexpr int64_t kMaxExperts = int64_t(1) << 16;
 
 bool block_ok(int64_t b) { return b == 16 || b == 32 || b == 64 || b == 128; }
 
@@ -360,6 +363,87 @@ gptq_status gptq_token_logprobs(const void* logits, int32_t dtype, int64_t n, in
   return from_hip(gptq::logprob_launch(plan, p, ws, (hipStream_t)stream));
 }
 
+gptq_status gptq_int8_quantize(const void* X, int32_t x_dtype, int64_t m, int64_t k, int64_t ld_x, int8_t* codes,
+                               int64_t ld_codes, float* scales, void* stream) {
+  if (m < 0 || k <= 0) return GPTQ_ERR_BAD_SIZE;
+  // rows: also those of a stack of weights taken as one matrix
+  if (m > kMaxRows || k > kMaxDim) return GPTQ_ERR_TOO_LARGE;
+  if (!elem_ok(x_dtype)) return GPTQ_ERR_BAD_DTYPE;
+  if (m == 0) return GPTQ_OK;
+  if (X == nullptr || codes == nullptr || scales == nullptr) return GPTQ_ERR_NULL_POINTER;
+  if (ld_x < k || ld_codes < k) return GPTQ_ERR_BAD_LEADING_DIM;
+  return from_hip(gptq::int8_quantize_launch(X, x_dtype, m, k, ld_x, codes, ld_codes, scales, (hipStream_t)stream));
+}
+
+size_t gptq_int8_matmul_workspace_size(int64_t m, int64_t n, int64_t k) {
+  if (m <= 0 || n <= 0 || k <= 0 || m > kMaxDim || n > kMaxDim || k > kMaxInt8Sum) return 0;
+  return gptq::int8_plan(m, n, k).ws_bytes;
+}
+
+gptq_status gptq_int8_matmul(const int8_t* x_codes, int64_t ld_x, const float* x_scales, const int8_t* w_codes,
+                             int64_t ld_w, const float* w_scales, int64_t m, int64_t n, int64_t k, const void* bias,
+                             void* Y, int32_t y_dtype, int64_t ld_y, void* ws, size_t ws_bytes, void* stream) {
+  if (m < 0 || n <= 0 || k <= 0) return GPTQ_ERR_BAD_SIZE;
+  if (m > kMaxDim || n > kMaxDim || k > kMaxInt8Sum) return GPTQ_ERR_TOO_LARGE;
+  if (!elem_ok(y_dtype)) return GPTQ_ERR_BAD_DTYPE;
+  if (m == 0) return GPTQ_OK;
+  if (x_codes == nullptr || x_scales == nullptr || w_codes == nullptr || w_scales == nullptr || Y == nullptr)
+    return GPTQ_ERR_NULL_POINTER;
+  if (ld_x < k || ld_w < k || ld_y < n) return GPTQ_ERR_BAD_LEADING_DIM;
+  const gptq::Int8Plan plan = gptq::int8_plan(m, n, k);
+  if (gptq_status st = ws_check(ws, ws_bytes, plan.ws_bytes)) return st;
+  const gptq::Int8Args p{(const uint8_t*)x_codes, ld_x, x_scales, (const uint8_t*)w_codes, ld_w, 0, w_scales, m, n, k,
+                         bias, Y, y_dtype, ld_y, nullptr, 1, nullptr, m};
+  return from_hip(gptq::int8_matmul_launch(plan, p, ws, (hipStream_t)stream));
+}
+
+gptq_status gptq_int8_matmul_grouped(const int8_t* x_codes, int64_t ld_x, const float* x_scales, int64_t rows_x,
+                                     const int32_t* rows, int64_t m, const int32_t* offsets, int64_t experts,
+                                     const int8_t* w_codes, int64_t ld_w, int64_t stride_w, const float* w_scales,
+                                     int64_t n, int64_t k, const void* bias, void* Y, int32_t y_dtype, int64_t ld_y,
+                                     void* stream) {
+  if (m < 0 || rows_x < 0 || experts <= 0 || n <= 0 || k <= 0) return GPTQ_ERR_BAD_SIZE;
+  if (m > kMaxDim || rows_x > kMaxDim || experts > kMaxExperts || n > kMaxDim || k > kMaxInt8Sum)
+    return GPTQ_ERR_TOO_LARGE;
+  if (!elem_ok(y_dtype)) return GPTQ_ERR_BAD_DTYPE;
+  if (m == 0) return GPTQ_OK;
+  if (rows_x < (rows == nullptr ? m : 1)) return GPTQ_ERR_BAD_SIZE;
+  if (x_codes == nullptr || x_scales == nullptr || offsets == nullptr || w_codes == nullptr || w_scales == nullptr ||
+      Y == nullptr)
+    return GPTQ_ERR_NULL_POINTER;
+  if (ld_x < k || ld_w < k || ld_y < n) return GPTQ_ERR_BAD_LEADING_DIM;
+  if (experts > 1 && stride_w / n < ld_w) return GPTQ_ERR_BAD_LEADING_DIM;
+  const gptq::Int8Args p{(const uint8_t*)x_codes, ld_x, x_scales, (const uint8_t*)w_codes, ld_w, stride_w, w_scales, m,
+                         n, k, bias, Y, y_dtype, ld_y, offsets, (int)experts, rows, rows_x};
+  return from_hip(gptq::int8_grouped_launch(p, (hipStream_t)stream));
+}
+
+size_t gptq_distill_loss_workspace_size(int64_t n, int64_t v) {
+  if (n <= 0 || v <= 0 || n > kMaxDim || v > kMaxDim) return 0;
+  size_t need = 0;          // enough for every type, with and without a gradient
+  for (int bytes = 2; bytes <= 4; bytes += 2)
+    for (int grad = 0; grad < 2; ++grad) need = std::max(need, gptq::distill_plan(n, v, bytes, grad != 0).ws_bytes);
+  return need;
+}
+
+gptq_status gptq_distill_loss(const void* logits, int32_t dtype, int64_t n, int64_t v, int64_t ld, const int32_t* ids,
+                              const float* logprobs, int64_t top_k, float temperature, int32_t tail,
+                              const float* weights, float* loss, void* grad, int64_t ld_grad, void* ws, size_t ws_bytes,
+                              void* stream) {
+  if (n < 0 || v <= 0 || top_k <= 0 || top_k > GPTQ_MAX_TOP || top_k > (tail ? v - 1 : v)) return GPTQ_ERR_BAD_SIZE;
+  if (n > kMaxDim || v > kMaxDim) return GPTQ_ERR_TOO_LARGE;
+  if (!elem_ok(dtype)) return GPTQ_ERR_BAD_DTYPE;
+  if (!(temperature >= 1e-4f && temperature <= 1e4f)) return GPTQ_ERR_BAD_TEMPERATURE;
+  if (n == 0) return GPTQ_OK;
+  if (logits == nullptr || ids == nullptr || logprobs == nullptr || loss == nullptr) return GPTQ_ERR_NULL_POINTER;
+  if (ld < v || (grad != nullptr && ld_grad < v)) return GPTQ_ERR_BAD_LEADING_DIM;
+  const gptq::DistillPlan plan = gptq::distill_plan(n, v, dtype == GPTQ_F32 ? 4 : 2, grad != nullptr);
+  if (gptq_status st = ws_check(ws, ws_bytes, plan.ws_bytes)) return st;
+  const gptq::DistillArgs p{logits, dtype, n, v, ld, ids, logprobs, (int)top_k, temperature, tail != 0, weights, loss, grad,
+                            ld_grad};
+  return from_hip(gptq::distill_launch(plan, p, ws, (hipStream_t)stream));
+}
+
 gptq_status gptq_launch_timing(int32_t enable) {
   gptq::thread_timer().on = enable != 0;
   return GPTQ_OK;
@@ -408,6 +492,7 @@ const char* gptq_status_string(int32_t status) {
     case GPTQ_ERR_SCRATCH:
       return "the shape needs more workspace than the no-allocation entry point holds "
              "(gptq_quantize_layer_workspace_size > GPTQ_NOALLOC_SCRATCH_BYTES)";
+    case GPTQ_ERR_BAD_TEMPERATURE: return "temperature must be between 1e-4 and 1e4";
     default: return "unknown status";
   }
 }

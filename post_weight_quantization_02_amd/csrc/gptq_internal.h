@@ -101,6 +101,36 @@ struct Fp8Args {
 };
 hipError_t fp8_matmul_launch(const Fp8Plan& plan, const Fp8Args& p, void* ws, hipStream_t s);
 
+// ---------------------------------------------------------------- int8 codes with scales per row
+hipError_t int8_quantize_launch(const void* X, int x_dtype, int64_t m, int64_t k, int64_t ld_x, int8_t* codes,
+                                int64_t ld_codes, float* scales, hipStream_t s);
+
+struct Int8Plan {
+  int kind;
+  int splits;             // parts of k, summed by a second launch when more than one
+  size_t ws_bytes;
+};
+Int8Plan int8_plan(int64_t m, int64_t n, int64_t k);
+struct Int8Args {
+  const uint8_t* X;
+  int64_t ld_x;
+  const float* sx;        // [rows_x]
+  const uint8_t* W;       // [experts][n][k]
+  int64_t ld_w, stride_w;
+  const float* sw;        // [experts][n]
+  int64_t m, n, k;        // m: positions, rows of Y
+  const void* bias;       // nullptr or [experts][n] values of Y's type
+  void* Y;
+  int y_dtype;
+  int64_t ld_y;
+  const int32_t* offsets; // nullptr (one expert has all positions), or [experts + 1]
+  int experts;
+  const int32_t* rows;    // nullptr (position i takes row i), or [m]
+  int64_t rows_x;
+};
+hipError_t int8_matmul_launch(const Int8Plan& plan, const Int8Args& p, void* ws, hipStream_t s);
+hipError_t int8_grouped_launch(const Int8Args& p, hipStream_t s);      // by offsets
+
 // ---------------------------------------------------------------- log probabilities
 struct LogprobPlan {
   int splits;             // parts of a row, joined by a second launch when more than one
@@ -120,6 +150,29 @@ struct LogprobArgs {
   float* top_logprobs;
 };
 hipError_t logprob_launch(const LogprobPlan& plan, const LogprobArgs& p, void* ws, hipStream_t s);
+
+// ---------------------------------------------------------------- distillation loss
+struct DistillPlan {
+  int splits;             // parts of a row, joined by a second launch when more than one
+  int64_t span;           // elements of a part, a multiple of 8
+  size_t ws_bytes;
+};
+DistillPlan distill_plan(int64_t n, int64_t v, int elem_bytes, bool grad);
+struct DistillArgs {
+  const void* logits;
+  int dtype;
+  int64_t n, v, ld;
+  const int32_t* ids;     // [n][top]
+  const float* logprobs;  // [n][top]
+  int top;
+  float temperature;
+  int tail;
+  const float* weights;   // nullptr or [n]
+  float* loss;            // [n]
+  void* grad;             // nullptr or [n][v] of the logits' type
+  int64_t ld_grad;
+};
+hipError_t distill_launch(const DistillPlan& plan, const DistillArgs& p, void* ws, hipStream_t s);
 
 // ---------------------------------------------------------------- two-sided rounding
 struct Plan2D {
