@@ -420,7 +420,7 @@ gptq_status gptq_token_logprobs(const void* logits, int32_t dtype, int64_t n, in
  *   the product is several times as fast.  m == 0 is a no-op.  ws: >=
  *   gptq_int8_matmul_workspace_size() bytes (may be 0).
  *
- * gptq_int8_matmul_grouped: the same with a stack of `experts` weights (at most 2^16), for m
+ * gptq_int8_matmul_grouped: the same with a stack of `experts` weights (at most 2^12), for m
  *   positions sorted by expert: positions offsets[e] <= i < offsets[e + 1] belong to expert e
  *   and take row r = rows[i] of X (rows NULL: r = i):
  *     Y[i][j] = bias[e][j] + x_scales[r] * w_scales[e][j] * sum_c x_codes[r][c] w_codes[e][j][c]

@@ -16,7 +16,7 @@ constexpr int64_t kMaxDim = int64_t(1) << 20;        // d_col and d_row limits
 constexpr int64_t kMaxElems = int64_t(1) << 40;
 constexpr int64_t kMaxRows = int64_t(1) << 30;       // rows of int8 codes
 constexpr int64_t kMaxInt8Sum = (int64_t(1) << 17) - 1;      // 2^14 times this stays below 2^31
-constexpr int64_t kMaxExperts = int64_t(1) << 16;
+constexpr int64_t kMaxExperts = int64_t(1) << 12;
 
 bool block_ok(int64_t b) { return b == 16 || b == 32 || b == 64 || b == 128; }
 

@@ -17,20 +17,53 @@ namespace gptq {
 namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
 
-__device__ __forceinline__ i32x4 product(u32x4 w, u32x4 x, i32x4 acc) {
-  return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, w), __builtin_bit_cast(i32x4, x), acc, 0, 0, 0);
+// Edge of a matrix instruction's tile: 32 (v_mfma_i32_32x32x32_i8: four chunks of 32 columns a
+// block) or 16 (v_mfma_i32_16x16x64_i8: two of 64).  A lane has 16 codes of row lane % M, and
+// of the sums row lane % M of X and outputs 4 (lane / M) + e, for 32 in steps of 8.
+template <int M>
+struct Tile;
+template <>
+struct Tile<16> {
+  typedef i32x4 Sums;
+  static constexpr int kSteps = 2, kGroups = 1;
+  static __device__ __forceinline__ Sums product(u32x4 w, u32x4 x, Sums acc) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, w), __builtin_bit_cast(i32x4, x), acc, 0, 0, 0);
+  }
+};
+template <>
+struct Tile<32> {
+  typedef i32x16 Sums;
+  static constexpr int kSteps = 4, kGroups = 4;
+  static __device__ __forceinline__ Sums product(u32x4 w, u32x4 x, Sums acc) {
+    return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, w), __builtin_bit_cast(i32x4, x), acc, 0, 0, 0);
+  }
+};
+// outputs 8 g + 4 (lane / M) + e
+template <int M>
+__device__ __forceinline__ i32x4 group(const typename Tile<M>::Sums& s, int g) {
+  return i32x4{s[4 * g], s[4 * g + 1], s[4 * g + 2], s[4 * g + 3]};
 }
 
-// four outputs of a row from their sums; none: -0, whose addition changes nothing
+// an output from its sum; no bias: -0, whose addition changes nothing
+__device__ __forceinline__ float output(int acc, float sx, float sw, float bias) {
+  const float t = (float)acc * sx;
+  float y = __builtin_fmaf(t, sw, bias);
+  asm("" : "+v"(y));          // rounded to fp32 here, not only where it becomes fp16: one kernel's bits are another's
+  return y;
+}
 __device__ __forceinline__ f32x4 outputs(i32x4 acc, float sx, f32x4 sw, f32x4 bias) {
-  f32x4 v;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    float t = (float)acc[e] * sx;
-    v[e] = __builtin_fmaf(t, sw[e], bias[e]);
-  }
-  return v;
+  return f32x4{output(acc[0], sx, sw[0], bias[0]), output(acc[1], sx, sw[1], bias[1]), output(acc[2], sx, sw[2], bias[2]),
+               output(acc[3], sx, sw[3], bias[3])};
+}
+
+// f(a value of Y's type)
+template <typename F>
+__device__ __forceinline__ void with_type(int dtype, F&& f) {
+  if (dtype == kF32) f(0.f);
+  else if (dtype == kF16) f((_Float16)0.f);
+  else f((bf16)0.f);
 }
 
 // the scales and biases of outputs j .. j + 3
@@ -42,6 +75,20 @@ __device__ __forceinline__ void load_channels(const float* __restrict__ sw, cons
     const int64_t at = min(j + e, n - 1);
     s[e] = sw[at];
     b[e] = bias ? (float)bias[at] : -0.f;
+  }
+}
+// the same where all four are there
+template <typename T>
+__device__ __forceinline__ void load_channels_inside(const float* __restrict__ sw, const T* __restrict__ bias, int64_t j,
+                                                     f32x4& s, f32x4& b) {
+  typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+  typedef T T4_any __attribute__((ext_vector_type(4), aligned(2)));
+  s = *(const f32x4_any*)(sw + j);
+  b = f32x4{-0.f, -0.f, -0.f, -0.f};
+  if (bias) {
+    const T4_any v = *(const T4_any*)(bias + j);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) b[e] = (float)v[e];
   }
 }
 
@@ -105,7 +152,7 @@ constexpr int kTile = 128;
 // ---------------------------------------------------------------- rows at any address
 // 128 x 128 outputs per work-group, 4 waves of 64 x 64, LDS filled through registers by
 // unaligned loads, block after block.
-template <typename T, bool GROUPED>
+template <bool GROUPED>
 __global__ __launch_bounds__(256) void int8_tile_kernel(Int8Args p) {
   __shared__ u32x4 xt[kTile * 8], wt[kTile * 8];
   const int t = threadIdx.x, lane = t & 63, w = t >> 6;
@@ -118,7 +165,6 @@ __global__ __launch_bounds__(256) void int8_tile_kernel(Int8Args p) {
   const int64_t j0 = (int64_t)blockIdx.x * kTile, last = g.end - 1;
   const uint8_t* W = p.W + g.expert * p.stride_w;
   const float* sw = p.sw + (int64_t)g.expert * p.n;
-  const T* bias = p.bias ? (const T*)p.bias + (int64_t)g.expert * p.n : nullptr;
   const int wi = (w & 1) * 64, wj = (w >> 1) * 64;
   const int lr = lane & 15, q = lane >> 4;
   i32x4 acc[4][4];
@@ -154,22 +200,549 @@ __global__ __launch_bounds__(256) void int8_tile_kernel(Int8Args p) {
       for (int c = 0; c < 4; ++c) {
         const u32x4 xv = chunk(xt, wi + 16 * c + lr);
 #pragma unroll
-        for (int a = 0; a < 4; ++a) acc[c][a] = product(wv[a], xv, acc[c][a]);
+        for (int a = 0; a < 4; ++a) acc[c][a] = Tile<16>::product(wv[a], xv, acc[c][a]);
       }
     }
   }
+  with_type(p.y_dtype, [&](auto zero) {
+    typedef decltype(zero) T;
+    const T* bias = p.bias ? (const T*)p.bias + (int64_t)g.expert * p.n : nullptr;
 #pragma unroll
-  for (int a = 0; a < 4; ++a) {
-    const int64_t j = j0 + wj + 16 * a + 4 * q;
-    f32x4 s, b;
-    load_channels<T>(sw, bias, j, p.n, s, b);
+    for (int a = 0; a < 4; ++a) {
+      const int64_t j = j0 + wj + 16 * a + 4 * q;
+      f32x4 s, b;
+      load_channels<T>(sw, bias, j, p.n, s, b);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int64_t i = g.i0 + wi + 16 * c + lr;
-      const float sx = scale_of(p, min(i, last));
-      store4<T>((T*)p.Y, p.ld_y, nullptr, i, j, g.end, p.n, outputs(acc[c][a], sx, s, b));
+      for (int c = 0; c < 4; ++c) {
+        const int64_t i = g.i0 + wi + 16 * c + lr;
+        const float sx = scale_of(p, min(i, last));
+        store4<T>((T*)p.Y, p.ld_y, nullptr, i, j, g.end, p.n, outputs(acc[c][a], sx, s, b));
+      }
+    }
+  });
+}
+
+
+// ---------------------------------------------------------------- few rows
+// At most 16 TT positions.  A work-group takes 16 rows of W, its waves every fourth block of
+// 128 columns, and the waves' sums meet in LDS at the end.  Each wave streams its blocks of
+// W, and the rows of X with them, through a ring of R LDS slots of its own, filled by direct
+// loads R - 1 blocks ahead: no barriers, and nothing in flight holds registers.  HBM-bound on
+// W.  A last block of fewer than 128 columns goes through registers, asked for first and
+// multiplied last.
+constexpr int kFewWaves = 4;
+
+template <int TT>
+struct __attribute__((aligned(16))) Slot {
+  uint8_t w[16 * kBlk];
+  uint8_t x[16 * TT * kBlk];
+};
+template <int TT, int I>
+__device__ __forceinline__ Slot<TT> (&slots())[kFewWaves] {
+  __shared__ Slot<TT> s[kFewWaves];
+  return s;
+}
+
+template <int TT, int R, bool DMA, bool GROUPED>
+__global__ __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_per_eu(TT == 4 ? 1 : 2))) void
+int8_few_kernel(Int8Args p) {
+  __shared__ i32x4 part[kFewWaves][TT][64];
+  const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int lr = lane & 15, q = lane >> 4;
+  Rows g{0, p.m, 0};
+  if constexpr (GROUPED) {
+    int total;
+    g = find_rows<16 * TT>(p, blockIdx.y, total);
+    if (g.expert < 0) return;
+  }
+  const uint8_t* W = p.W + g.expert * p.stride_w;
+  const int64_t j0 = (int64_t)blockIdx.x * 16;
+  const int rows_w = (int)min<int64_t>(16, p.n - j0), rows_x = (int)(g.end - g.i0);
+  const int full = (int)(p.k / kBlk), nblk = (int)((p.k + kBlk - 1) / kBlk);
+  i32x4 acc[TT];
+#pragma unroll
+  for (int c = 0; c < TT; ++c) acc[c] = i32x4{0, 0, 0, 0};
+  const uint8_t* const wrow = W + (j0 + min(lr, rows_w - 1)) * p.ld_w;
+  const auto xrow = [&](int c) { return p.X + row_of(p, g.i0 + min(16 * c + lr, rows_x - 1)) * p.ld_x; };
+  if constexpr (!DMA) {
+    // blocks through registers, where rows may start anywhere
+    for (int b = w; b < nblk; b += kFewWaves)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int64_t at = (int64_t)b * kBlk + 64 * h + 16 * q;
+        const u32x4 wv = load_chunk(wrow, at, p.k);
+#pragma unroll
+        for (int c = 0; c < TT; ++c) acc[c] = Tile<16>::product(wv, load_chunk(xrow(c), at, p.k), acc[c]);
+      }
+  } else {
+    const int mine = full > w ? (full - w + kFewWaves - 1) / kFewWaves : 0;      // whole blocks w, w + 4, ...
+    const __amdgpu_buffer_rsrc_t wb = rsrc(W + j0 * p.ld_w, (rows_w - 1) * p.ld_w + p.k);
+    // gathered rows lie anywhere in X, others are neighbours
+    const __amdgpu_buffer_rsrc_t xb = p.rows ? rsrc(p.X, (p.rows_x - 1) * p.ld_x + p.k)
+                                             : rsrc(p.X + g.i0 * p.ld_x, (rows_x - 1) * p.ld_x + p.k);
+    const int ch = ((lane & 7) ^ (lane >> 3)) * 16;
+    uint32_t wo[2], xo[2 * TT];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) wo[j] = (uint32_t)(min(8 * j + (lane >> 3), rows_w - 1) * p.ld_w) + ch;
+#pragma unroll
+    for (int j = 0; j < 2 * TT; ++j) {
+      const int r = min(8 * j + (lane >> 3), rows_x - 1);
+      xo[j] = (uint32_t)((p.rows ? row_of(p, g.i0 + r) : r) * p.ld_x) + ch;
+    }
+    const auto block_of = [&](int i) { return i < mine ? w + kFewWaves * i : 0; };
+    const auto fetch = [&](Slot<TT>& s, int b) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) load16_to_lds(wb, s.w + 8 * j * kBlk, wo[j], b * kBlk);
+#pragma unroll
+      for (int j = 0; j < 2 * TT; ++j) load16_to_lds(xb, s.x + 8 * j * kBlk, xo[j], b * kBlk);
+    };
+    constexpr int kLoads = 2 + 2 * TT;
+    static_assert((R - 1) * kLoads < 64, "counted by vmcnt");
+    const uint32_t a0 = (uint32_t)(lr * kBlk + ((q ^ (lr & 7)) * 16));
+    const auto use = [&](const Slot<TT>& s) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const u32x4 wv = *(const u32x4*)(s.w + (a0 ^ (64 * h)));
+#pragma unroll
+        for (int c = 0; c < TT; ++c)
+          acc[c] = Tile<16>::product(wv, *(const u32x4*)(s.x + 16 * c * kBlk + (a0 ^ (64 * h))), acc[c]);
+      }
+    };
+    // a last block of fewer columns: asked for before the others, multiplied after them
+    const bool tail = full < nblk && full % kFewWaves == w;
+    const int64_t c0 = (int64_t)full * kBlk + 16 * q;
+    u32x4 tw[2], tx[TT][2];
+    if (tail) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) tw[h] = load_inside(wrow, c0 + 64 * h, p.k);
+#pragma unroll
+      for (int c = 0; c < TT; ++c)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) tx[c][h] = load_inside(xrow(c), c0 + 64 * h, p.k);
+    }
+    if (mine > 0) {
+      static_for<0, R - 1>([&](auto i) { fetch(slots<TT, i.value>()[w], block_of(i.value)); });
+      int i = 0;
+      const auto one = [&](auto h) {
+        // the reads of the slot that is refilled next are done; so is this slot's block once it alone is left out
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        fetch(slots<TT, (h.value + R - 1) % R>()[w], block_of(i + R - 1));
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((R - 1) * kLoads) : "memory");
+        use(slots<TT, h.value>()[w]);
+        ++i;
+      };
+      while (i + R <= mine) static_for<0, R>(one);
+      static_for<0, R - 1>([&](auto h) {
+        if (i < mine) one(h);
+      });
+    }
+    if (tail) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const u32x4 wv = align_chunk(tw[h], c0 + 64 * h, p.k);
+#pragma unroll
+        for (int c = 0; c < TT; ++c) acc[c] = Tile<16>::product(wv, align_chunk(tx[c][h], c0 + 64 * h, p.k), acc[c]);
+      }
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // unused fetches write LDS: not after this work-group's end
+  }
+#pragma unroll
+  for (int c = 0; c < TT; ++c) part[w][c][lane] = acc[c];
+  __syncthreads();
+  if (w < TT) {         // TT <= 4 waves
+    i32x4 v = part[0][w][lane];
+#pragma unroll
+    for (int i = 1; i < kFewWaves; ++i) v += part[i][w][lane];
+    const int64_t i = g.i0 + 16 * w + lr, j = j0 + 4 * q;
+    const float sx = scale_of(p, min(i, g.end - 1));
+    with_type(p.y_dtype, [&](auto zero) {
+      typedef decltype(zero) T;
+      f32x4 s, b;
+      load_channels<T>(p.sw + (int64_t)g.expert * p.n, p.bias ? (const T*)p.bias + (int64_t)g.expert * p.n : nullptr, j, p.n, s, b);
+      store4<T>((T*)p.Y, p.ld_y, nullptr, i, j, g.end, p.n, outputs(v, sx, s, b));
+    });
+  }
+}
+
+// ---------------------------------------------------------------- tiles by LDS
+// BT positions by BN rows of W per work-group, WT x WN waves (WK groups of them, which take the
+// blocks in turn).  Each block of 128 columns goes to LDS without passing through registers
+// (16-byte direct loads, a wave's load filling 8 rows of 128 bytes), S - 1 blocks ahead of the
+// products, in S buffers that are variables of their own so that reading one does not wait for
+// the others' loads.  Row r keeps its 16-byte chunk c at place c ^ (r & 7): the rows that a
+// fragment load takes at one chunk then spread over all banks.  A last block of fewer than
+// 128 columns is taken first, through registers, with zeros behind column k.
+template <int ROWS>
+struct __attribute__((aligned(16))) Stage {
+  uint8_t rows[ROWS * kBlk];
+};
+template <int BT, int WK, int I>
+__device__ __forceinline__ Stage<BT> (&stage_x())[WK] {
+  __shared__ Stage<BT> s[WK];
+  return s;
+}
+template <int BN, int WK, int I>
+__device__ __forceinline__ Stage<BN> (&stage_w())[WK] {
+  __shared__ Stage<BN> s[WK];
+  return s;
+}
+
+// A wave's 32 rows from i0 on by 128 bytes of outputs from j0 on (two tiles of 16-bit outputs,
+// one of fp32): lanes of four neighbouring rows change parts (registers only), so that a store
+// instruction writes 8 whole rows of 128 bytes.
+template <typename T>
+__device__ __forceinline__ void store_lines(T* __restrict__ Y, int64_t ld_y, int64_t i0, int64_t j0, int lane, int64_t m,
+                                            bool stream, const f32x4 (&v)[sizeof(T) == 4 ? 4 : 8]) {
+  typedef T T4 __attribute__((ext_vector_type(4)));
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  typedef uint32_t u32x4_at2 __attribute__((ext_vector_type(4), aligned(2)));
+  const int lr = lane & 31, h = lane >> 5;
+  uint32_t u[4][4];         // part s: 16 bytes from byte 16 (2 s + h) on
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float f = v[s][e];
+        u[s][e] = __builtin_bit_cast(uint32_t, f);
+      }
+  } else {
+    // the two lanes of a row: 8 outputs in a row for each
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const f32x4 a = v[2 * s], b = v[2 * s + 1];
+      const u32x2 x = __builtin_bit_cast(u32x2, T4{(T)a[0], (T)a[1], (T)a[2], (T)a[3]});
+      const u32x2 y = __builtin_bit_cast(u32x2, T4{(T)b[0], (T)b[1], (T)b[2], (T)b[3]});
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const auto r = __builtin_amdgcn_permlane32_swap(x[e], y[e], false, false);
+        u[s][e] = r[0];
+        u[s][2 + e] = r[1];
+      }
     }
   }
+  // four lanes of neighbouring rows and their four parts change places
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+#pragma unroll
+    for (int a = 0; a < 4; a += 2) {
+      const uint32_t r = other_lane<0>((lr & 1) ? u[a][e] : u[a + 1][e]);
+      u[a][e] = (lr & 1) ? r : u[a][e];
+      u[a + 1][e] = (lr & 1) ? u[a + 1][e] : r;
+    }
+#pragma unroll
+    for (int a = 0; a < 2; ++a) {
+      const uint32_t r = other_lane<1>((lr & 2) ? u[a][e] : u[a + 2][e]);
+      u[a][e] = (lr & 2) ? r : u[a][e];
+      u[a + 2][e] = (lr & 2) ? u[a + 2][e] : r;
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    const int64_t i = i0 + (lr & ~3) + t;
+    if (i >= m) continue;
+    u32x4_at2* y = (u32x4_at2*)((uint8_t*)(Y + i * ld_y + j0) + 16 * (2 * (lr & 3) + h));
+    const u32x4_at2 o = {u[t][0], u[t][1], u[t][2], u[t][3]};
+    if (stream) {
+      keep_apart();
+      __builtin_nontemporal_store(o, y);
+      keep_apart();
+    } else {
+      *y = o;
+    }
+  }
+}
+
+// how a work-group keeps its buffers full
+enum Flow {
+  kBlocks,      // S buffers; one barrier per block
+  kAhead        // S buffers; a block's codes are read into registers while the one before is multiplied
+};
+
+template <int BT, int BN, int WT, int WN, int WK, int S, Flow FLOW, bool SPLIT, bool GROUPED>
+__global__ __launch_bounds__(64 * WT * WN * WK) __attribute__((amdgpu_waves_per_eu(2))) void
+int8_dma_kernel(Int8Args p, int tiles_t, int tiles_n, int blocks_per_split, int* __restrict__ parts) {
+  constexpr int kWavesHere = WT * WN, M = (BT / WT) % 32 == 0 && (BN / WN) % 32 == 0 ? 32 : 16;
+  constexpr int TT = BT / WT / M, TN = BN / WN / M, KS = Tile<M>::kSteps;
+  constexpr int kXLoads = BT / 8 / kWavesHere, kWLoads = BN / 8 / kWavesHere;
+  static_assert(kXLoads * 8 * kWavesHere == BT && kWLoads * 8 * kWavesHere == BN, "loads divide over the waves");
+  constexpr int kLoads = kXLoads + kWLoads;        // of a wave, per block
+  static_assert((S - 1) * kLoads < 64, "counted by vmcnt");
+  typedef typename Tile<M>::Sums Sums;
+  const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane((t >> 6) % kWavesHere);
+  const int grp = __builtin_amdgcn_readfirstlane((t >> 6) / kWavesHere);      // the wave's group
+  const int lr = lane & (M - 1), q = lane / M;
+  Rows g{0, p.m, 0};
+  int part = 0;
+  int64_t j0;
+  if constexpr (GROUPED) {
+    // experts' tiles by columns: neighbouring work-groups of one XCD share rows of W
+    int total;
+    find_rows<BT>(p, 0, total);
+    if ((int)blockIdx.x >= total * tiles_n) return;
+    const int id = (int)xcd_remap(blockIdx.x, (int64_t)total * tiles_n);
+    const int band = id / (8 * tiles_n), in = id - band * 8 * tiles_n, high = min(8, total - 8 * band);
+    int ignored;
+    g = find_rows<BT>(p, 8 * band + in % high, ignored);
+    if (g.expert < 0) return;
+    j0 = (int64_t)(in / high) * BN;
+  } else {
+    // work-groups of one XCD take neighbouring tiles: bands of 8 tiles along X, W outermost
+    const int tiles = tiles_t * tiles_n;
+    part = blockIdx.x / tiles;
+    const int id = (int)xcd_remap(blockIdx.x % tiles, tiles);
+    const int band = id / (8 * tiles_n), in = id - band * 8 * tiles_n, high = min(8, tiles_t - 8 * band);
+    g.i0 = (int64_t)(8 * band + in % high) * BT;
+    j0 = (int64_t)(in / high) * BN;
+  }
+  const uint8_t* const W = p.W + g.expert * p.stride_w;
+  const int wi = (w % WT) * (BT / WT), wj = (w / WT) * (BN / WN);
+  const int nblk = (int)((p.k + kBlk - 1) / kBlk);
+  const int b0 = part * blocks_per_split, b1 = min(b0 + blocks_per_split, nblk);
+
+  const int rows_x = (int)min<int64_t>(BT, g.end - g.i0), rows_w = (int)min<int64_t>(BN, p.n - j0);
+  const bool gathered = GROUPED && p.rows != nullptr;       // rows anywhere in X, others are neighbours
+  const __amdgpu_buffer_rsrc_t xb = gathered ? rsrc(p.X, (p.rows_x - 1) * p.ld_x + p.k)
+                                             : rsrc(p.X + g.i0 * p.ld_x, (rows_x - 1) * p.ld_x + p.k);
+  const __amdgpu_buffer_rsrc_t wb = rsrc(W + j0 * p.ld_w, (rows_w - 1) * p.ld_w + p.k);
+  // a lane's row and chunk in each of the wave's loads; rows past the end repeat the last
+  const int ch = ((lane & 7) ^ (lane >> 3)) * 16;
+  uint32_t xo[kXLoads], wo[kWLoads];
+#pragma unroll
+  for (int j = 0; j < kXLoads; ++j) {
+    const int r = min((w * kXLoads + j) * 8 + (lane >> 3), rows_x - 1);
+    xo[j] = (uint32_t)((gathered ? row_of(p, g.i0 + r) : r) * p.ld_x) + ch;
+  }
+#pragma unroll
+  for (int j = 0; j < kWLoads; ++j)
+    wo[j] = (uint32_t)(min((w * kWLoads + j) * 8 + (lane >> 3), rows_w - 1) * p.ld_w) + ch;
+  const auto fetch_one = [&](Stage<BT>& x, Stage<BN>& s, int b, int l) {
+    if (l < kXLoads) load16_to_lds(xb, x.rows + (w * kXLoads + l) * 8 * kBlk, xo[l], b * kBlk);
+    else load16_to_lds(wb, s.rows + (w * kWLoads + l - kXLoads) * 8 * kBlk, wo[l - kXLoads], b * kBlk);
+  };
+  const auto fetch = [&](auto i, int b) {
+#pragma unroll
+    for (int l = 0; l < kLoads; ++l) fetch_one(stage_x<BT, WK, i.value>()[grp], stage_w<BN, WK, i.value>()[grp], b, l);
+  };
+  Sums acc[TT][TN];
+#pragma unroll
+  for (int c = 0; c < TT; ++c)
+#pragma unroll
+    for (int a = 0; a < TN; ++a) acc[c][a] = Sums(0);
+  // a lane's first chunk of its row in the wave's first tile of each operand; the others by xor
+  const uint32_t x0 = (uint32_t)((wi + lr) * kBlk + ((q ^ (lr & 7)) * 16));
+  const uint32_t w0 = (uint32_t)((wj + lr) * kBlk + ((q ^ (lr & 7)) * 16));
+  const auto pick = [&](const uint8_t* rows, uint32_t a, int tile, int step) {
+    return *(const u32x4*)(rows + (a ^ (step * (64 / M) * 16)) + tile * M * kBlk);
+  };
+  // a last block of fewer than 128 columns, through registers: all loads first, and LDS
+  // written once the next blocks' loads are under way
+  const bool tail = b1 == nblk && (p.k % kBlk) != 0;
+  constexpr int kAll = 64 * kWavesHere * WK, kTail = ((BT + BN) * 8 + kAll - 1) / kAll;
+  u32x4 tail_v[kTail];
+  if (tail) {
+#pragma unroll
+    for (int i = 0; i < kTail; ++i) {
+      const int id = t + i * kAll, r = min(id >> 3, BT + BN - 1);
+      const uint8_t* row = r < BT ? p.X + (GROUPED ? row_of(p, g.i0 + min(r, rows_x - 1)) : g.i0 + min(r, rows_x - 1)) * p.ld_x
+                                  : W + (j0 + min(r - BT, rows_w - 1)) * p.ld_w;
+      tail_v[i] = load_inside(row, (int64_t)(nblk - 1) * kBlk + 16 * (id & 7), p.k);
+    }
+  }
+  const auto put_tail = [&]() {
+    if (!tail) return;
+#pragma unroll
+    for (int i = 0; i < kTail; ++i) {
+      const int id = t + i * kAll, r = id >> 3, c = id & 7;
+      const u32x4 v = align_chunk(tail_v[i], (int64_t)(nblk - 1) * kBlk + 16 * c, p.k);
+      if (r < BT) *(u32x4*)(stage_x<BT, WK, 0>()[0].rows + r * kBlk + ((c ^ (r & 7)) * 16)) = v;
+      else if (r < BT + BN) *(u32x4*)(stage_w<BN, WK, 0>()[0].rows + (r - BT) * kBlk + ((c ^ (r & 7)) * 16)) = v;
+    }
+  };
+  // the groups take the blocks in turn
+  const int count = b1 - b0, steps = (count + WK - 1) / WK;
+  const auto block_of = [&](int at) { return !tail ? b0 + at : at == 0 ? nblk - 1 : b0 + at - 1; };
+  // behind the last block, block 0, which is not used: with a fetch on every path the
+  // counts of outstanding loads are known, and no read waits for a later block
+  const auto next = [&](int step) { return step * WK + grp < count ? block_of(step * WK + grp) : 0; };
+  if (!tail || grp > 0) fetch(std::integral_constant<int, 0>{}, next(0));
+  int step = 0;
+  // one(stage, whether the group has a block): only in the last step may it have none
+  const auto run = [&](auto&& one) {
+    while (step + S < steps) static_for<0, S>([&](auto i) { one(i, true); });
+    static_for<0, S>([&](auto i) {
+      if (step < steps) one(i, WK == 1 || step * WK + grp < count);
+    });
+  };
+  if constexpr (FLOW == kBlocks) {
+    static_for<1, S - 1>([&](auto i) { fetch(i, next(i.value)); });
+    put_tail();
+    run([&](auto i, bool has) {
+      constexpr int h = i.value, to = (h + S - 1) % S;
+      // this block has arrived, and every wave is done with the buffer that is filled next
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S - 2) * kLoads) : "memory");
+      const int b = next(step + S - 1);
+      ++step;
+      if (!has) return;           // nothing follows: nothing to fetch
+      const uint8_t* xs = stage_x<BT, WK, h>()[grp].rows;
+      const uint8_t* ws = stage_w<BN, WK, h>()[grp].rows;
+      constexpr int kSpread = TT * TN >= 8 ? KS / 2 : 0;      // steps beside which the next loads are issued
+      if constexpr (kSpread == 0) fetch(std::integral_constant<int, to>{}, b);
+      u32x4 wv[2][TN], xv[2][TT];
+      const auto read = [&](int set, int k) {
+#pragma unroll
+        for (int a = 0; a < TN; ++a) wv[set][a] = pick(ws, w0, a, k);
+#pragma unroll
+        for (int c = 0; c < TT; ++c) xv[set][c] = pick(xs, x0, c, k);
+      };
+      read(0, 0);
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        if (k + 1 < KS) read((k + 1) & 1, k + 1);
+        if constexpr (kSpread > 0) {
+#pragma unroll
+          for (int l = 0; l < kLoads; ++l)
+            if (l * kSpread / kLoads == k) fetch_one(stage_x<BT, WK, to>()[grp], stage_w<BN, WK, to>()[grp], b, l);
+        }
+#pragma unroll
+        for (int c = 0; c < TT; ++c)
+#pragma unroll
+          for (int a = 0; a < TN; ++a) acc[c][a] = Tile<M>::product(wv[k & 1][a], xv[k & 1][c], acc[c][a]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    });
+  } else {
+    static_assert(S % 2 == 0, "two sets of registers in turn");
+    static_for<1, S>([&](auto i) { fetch(i, next(i.value)); });
+    put_tail();
+    u32x4 wv[2][KS][TN], xv[2][KS][TT];
+    const auto read = [&](int set, const Stage<BT>& x, const Stage<BN>& s, int k) {
+#pragma unroll
+      for (int a = 0; a < TN; ++a) wv[set][k][a] = pick(s.rows, w0, a, k);
+#pragma unroll
+      for (int c = 0; c < TT; ++c) xv[set][k][c] = pick(x.rows, x0, c, k);
+    };
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S - 1) * kLoads) : "memory");
+#pragma unroll
+    for (int k = 0; k < KS; ++k) read(0, stage_x<BT, WK, 0>()[grp], stage_w<BN, WK, 0>()[grp], k);
+    run([&](auto i, bool has) {
+      constexpr int h = i.value, set = h & 1, nx = (h + 1) % S;
+      // the next block has arrived, and every wave has read this one
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S - 2) * kLoads) : "memory");
+      const int b = next(step + S);
+      ++step;
+      if (!has) return;
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        read(set ^ 1, stage_x<BT, WK, nx>()[grp], stage_w<BN, WK, nx>()[grp], k);
+#pragma unroll
+        for (int l = 0; l < kLoads; ++l)
+          if (l * KS / kLoads == k) fetch_one(stage_x<BT, WK, h>()[grp], stage_w<BN, WK, h>()[grp], b, l);
+#pragma unroll
+        for (int c = 0; c < TT; ++c)
+#pragma unroll
+          for (int a = 0; a < TN; ++a) acc[c][a] = Tile<M>::product(wv[set][k][a], xv[set][k][c], acc[c][a]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    });
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // unused fetches write LDS: not after this work-group's end
+  if constexpr (WK > 1) {
+    // group 1's sums are added to group 0's through stage 0's rows of X, as many fours of each
+    // lane at a time as fit
+    constexpr int kG = Tile<M>::kGroups, kSums = TT * TN * kG;
+    constexpr int kFit = WK * (int)sizeof(Stage<BT>::rows) / (16 * 64 * kWavesHere);
+    static_assert(WK == 2 && kFit >= 1, "two groups");
+    i32x4* const sums = (i32x4*)stage_x<BT, WK, 0>()[0].rows + w * kFit * 64 + lane;
+#pragma unroll
+    for (int e0 = 0; e0 < kSums; e0 += kFit) {
+      // every wave's reads are done: of the last block, then of the sums before
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      if (grp == 1) {
+#pragma unroll
+        for (int e = e0; e < e0 + kFit && e < kSums; ++e) sums[(e - e0) * 64] = group<M>(acc[e / kG / TN][e / kG % TN], e % kG);
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      if (grp == 0) {
+#pragma unroll
+        for (int e = e0; e < e0 + kFit && e < kSums; ++e) {
+          const i32x4 other = sums[(e - e0) * 64];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[e / kG / TN][e / kG % TN][4 * (e % kG) + r] += other[r];
+        }
+      }
+    }
+    if (grp == 1) return;
+  }
+  if constexpr (SPLIT) {
+    int* const mine = parts + (int64_t)part * p.m * p.n;
+#pragma unroll
+    for (int c = 0; c < TT; ++c)
+#pragma unroll
+      for (int a = 0; a < TN; ++a)
+#pragma unroll
+        for (int e = 0; e < 4 * Tile<M>::kGroups; ++e) {
+          const int64_t i = g.i0 + wi + M * c + lr, j = j0 + wj + M * a + 8 * (e / 4) + 4 * q + e % 4;
+          if (i < p.m && j < p.n) mine[i * p.n + j] = acc[c][a][e];
+        }
+    return;
+  }
+  const float* const sw = p.sw + (int64_t)g.expert * p.n;
+  float sx[TT];
+#pragma unroll
+  for (int c = 0; c < TT; ++c) sx[c] = scale_of(p, min(g.i0 + wi + M * c + lr, g.end - 1));
+  with_type(p.y_dtype, [&](auto zero) {
+    typedef decltype(zero) T;
+    const T* const bias = p.bias ? (const T*)p.bias + (int64_t)g.expert * p.n : nullptr;
+    const bool stream = (uint64_t)p.m * (uint64_t)p.n * sizeof(T) > (uint64_t)80 << 20;
+    constexpr int kLine = 128 / (int)sizeof(T);         // outputs of a store_lines
+    constexpr bool kLines = M == 32 && (BN / WN) % kLine == 0;
+    if constexpr (kLines) {
+      if (j0 + wj + BN / WN <= p.n) {         // the same for the whole wave
+        constexpr int kPer = kLine / 32;      // tiles
+#pragma unroll
+        for (int a = 0; a < TN; a += kPer) {
+          f32x4 s[4 * kPer], b[4 * kPer];
+#pragma unroll
+          for (int e = 0; e < 4 * kPer; ++e) load_channels_inside<T>(sw, bias, j0 + wj + 32 * a + 8 * e + 4 * q, s[e], b[e]);
+#pragma unroll
+          for (int c = 0; c < TT; ++c) {
+            f32x4 v[4 * kPer];
+#pragma unroll
+            for (int e = 0; e < 4 * kPer; ++e) v[e] = outputs(group<M>(acc[c][a + e / 4], e % 4), sx[c], s[e], b[e]);
+            store_lines<T>((T*)p.Y, p.ld_y, g.i0 + wi + 32 * c, j0 + wj + 32 * a, lane, g.end, stream, v);
+          }
+        }
+        return;
+      }
+    }
+#pragma unroll
+    for (int a = 0; a < TN; ++a)
+#pragma unroll
+      for (int e = 0; e < Tile<M>::kGroups; ++e) {
+        const int64_t j = j0 + wj + M * a + 8 * e + 4 * q;
+        f32x4 s, b;
+        load_channels<T>(sw, bias, j, p.n, s, b);
+#pragma unroll
+        for (int c = 0; c < TT; ++c)
+          store4<T>((T*)p.Y, p.ld_y, nullptr, g.i0 + wi + M * c + lr, j, g.end, p.n,
+                    outputs(group<M>(acc[c][a], e), sx[c], s, b));
+      }
+  });
+}
+
+// Y from the parts of a product split over k
+__global__ __launch_bounds__(256) void int8_sum_kernel(Int8Args p, int splits, const int* __restrict__ parts) {
+  const int64_t size = p.m * p.n;
+  with_type(p.y_dtype, [&](auto zero) {
+    typedef decltype(zero) T;
+    for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < size; id += (int64_t)gridDim.x * 256) {
+      const int64_t i = id / p.n, j = id - i * p.n;
+      int v = parts[id];
+      for (int s = 1; s < splits; ++s) v += parts[s * size + id];
+      ((T*)p.Y)[i * p.ld_y + j] = (T)output(v, p.sx[i], p.sw[j], p.bias ? (float)((const T*)p.bias)[j] : -0.f);
+    }
+  });
 }
 
 // tiles of `bt` positions that the experts' parts of m positions can have at most
@@ -178,33 +751,108 @@ int64_t most_tiles(int64_t m, int64_t experts, int bt) {
   return (m + used * (bt - 1)) / bt;
 }
 
-template <typename T>
-hipError_t launch(const Int8Plan& plan, const Int8Args& p, void* ws, hipStream_t s) {
-  int8_tile_kernel<T, false><<<dim3((unsigned)cdiv(p.n, kTile), (unsigned)cdiv(p.m, kTile)), 256, 0, s>>>(p);
+// the direct loads need 16-byte rows, 32-bit offsets and a whole block
+bool direct(const Int8Args& p) {
+  const bool one_x = p.rows ? p.rows_x <= 1 : p.m <= 1;
+  const uint64_t ld_x = one_x ? 0 : (uint64_t)p.ld_x, ld_w = p.n > 1 ? (uint64_t)p.ld_w : 0;
+  const uint64_t st = p.experts > 1 ? (uint64_t)p.stride_w : 0;
+  return p.k >= kBlk && (((uintptr_t)p.X | (uintptr_t)p.W | ld_x | ld_w | st) & 15) == 0 &&
+         std::max(ld_x, ld_w) <= (uint64_t(1) << 22) &&
+         (!p.rows || (uint64_t)p.rows_x * (uint64_t)p.ld_x <= uint64_t(1) << 31);
+}
+
+template <bool GROUPED, int BT, int BN, int WT, int WN, int WK, int S, Flow FLOW>
+hipError_t launch_dma(const Int8Plan& plan, const Int8Args& p, int* ws, hipStream_t s) {
+  const int tt = (int)(GROUPED ? most_tiles(p.m, p.experts, BT) : cdiv(p.m, BT)), tn = (int)cdiv(p.n, BN);
+  const int per = (int)cdiv(cdiv(p.k, kBlk), plan.splits);
+  if constexpr (BT == 64 && BN == 32 && !GROUPED) {       // the only tiles of products that are split
+    if (plan.splits > 1) {
+      int8_dma_kernel<BT, BN, WT, WN, WK, S, FLOW, true, false>
+          <<<tt * tn * plan.splits, 64 * WT * WN * WK, 0, s>>>(p, tt, tn, per, ws);
+      int8_sum_kernel<<<(unsigned)std::min<int64_t>(cdiv(p.m * p.n, 256), 2048), 256, 0, s>>>(p, plan.splits, ws);
+      return hipGetLastError();
+    }
+  }
+  int8_dma_kernel<BT, BN, WT, WN, WK, S, FLOW, false, GROUPED>
+      <<<tt * tn, 64 * WT * WN * WK, 0, s>>>(p, tt, tn, per, nullptr);
   return hipGetLastError();
 }
 
-template <typename T>
-hipError_t launch_grouped(const Int8Args& p, hipStream_t s) {
-  int8_tile_kernel<T, true>
-      <<<dim3((unsigned)cdiv(p.n, kTile), (unsigned)most_tiles(p.m, p.experts, kTile)), 256, 0, s>>>(p);
-  return hipGetLastError();
+template <bool GROUPED>
+hipError_t launch(const Int8Plan& plan, const Int8Args& p, void* ws, hipStream_t s) {
+  const bool dma = direct(p);
+  const auto slots = [&](int bt) { return (unsigned)(GROUPED ? most_tiles(p.m, p.experts, bt) : 1); };
+  const unsigned few = (unsigned)cdiv(p.n, 16);
+  switch (plan.kind) {
+    case kInt8Few16:
+      if (dma) int8_few_kernel<1, 2, true, GROUPED><<<dim3(few, slots(16)), 64 * kFewWaves, 0, s>>>(p);
+      else int8_few_kernel<1, 1, false, GROUPED><<<dim3(few, slots(16)), 64 * kFewWaves, 0, s>>>(p);
+      return hipGetLastError();
+    case kInt8Few32:
+      if (dma) int8_few_kernel<2, 2, true, GROUPED><<<dim3(few, slots(32)), 64 * kFewWaves, 0, s>>>(p);
+      else int8_few_kernel<2, 1, false, GROUPED><<<dim3(few, slots(32)), 64 * kFewWaves, 0, s>>>(p);
+      return hipGetLastError();
+    case kInt8Few64:
+      if (dma) int8_few_kernel<4, 2, true, GROUPED><<<dim3(few, slots(64)), 64 * kFewWaves, 0, s>>>(p);
+      else int8_few_kernel<4, 1, false, GROUPED><<<dim3(few, slots(64)), 64 * kFewWaves, 0, s>>>(p);
+      return hipGetLastError();
+    default: break;
+  }
+  if (!dma) {
+    int8_tile_kernel<GROUPED>
+        <<<dim3((unsigned)cdiv(p.n, kTile), GROUPED ? slots(kTile) : (unsigned)cdiv(p.m, kTile)), 256, 0, s>>>(p);
+    return hipGetLastError();
+  }
+  int* const parts = (int*)ws;
+  switch (plan.kind) {
+    case kInt8T64x32: return launch_dma<GROUPED, 64, 32, 2, 2, 2, 4, kAhead>(plan, p, parts, s);
+    case kInt8T64x64: return launch_dma<GROUPED, 64, 64, 2, 2, 2, 4, kAhead>(plan, p, parts, s);
+    case kInt8T96x64: return launch_dma<GROUPED, 96, 64, 2, 2, 2, 3, kBlocks>(plan, p, parts, s);
+    case kInt8T128x64: return launch_dma<GROUPED, 128, 64, 2, 2, 2, 3, kBlocks>(plan, p, parts, s);
+    case kInt8T128x128Two: return launch_dma<GROUPED, 128, 128, 2, 2, 2, 2, kBlocks>(plan, p, parts, s);
+    case kInt8T256x256: return launch_dma<GROUPED, 256, 256, 2, 4, 1, 2, kBlocks>(plan, p, parts, s);
+    default: return launch_dma<GROUPED, 128, 128, 2, 2, 1, 2, kBlocks>(plan, p, parts, s);
+  }
 }
 
 }  // namespace
 
-Int8Plan int8_plan(int64_t m, int64_t n, int64_t k) { return Int8Plan{0, 1, 0}; }
+Int8Plan int8_plan(int64_t m, int64_t n, int64_t k) {
+  Int8Plan p{kInt8T128x128, 1, 0};
+  const bool few = k > 8192 && n <= 1024 ? false : m <= 16 ? true : m <= 32 ? n <= 8192 : m <= 64 && n <= 4096 && k <= 4096;
+  if (few) {
+    p.kind = m <= 16 ? kInt8Few16 : m <= 32 ? kInt8Few32 : kInt8Few64;
+    return p;
+  }
+  const struct { int kind, bt, bn; } small[] = {
+      {kInt8T64x32, 64, 32}, {kInt8T64x64, 64, 64}, {kInt8T96x64, 96, 64}, {kInt8T128x64, 128, 64},
+      {kInt8T128x128Two, 128, 128}};
+  for (const auto& c : small) {
+    const int64_t tiles = cdiv(m, c.bt) * cdiv(n, c.bn);
+    if (tiles > 256) continue;
+    p.kind = c.kind;
+    if (c.kind == kInt8T64x32) {         // the larger ones are taken from 129 tiles on: nothing to split
+      const int64_t nblk = cdiv(k, kBlk), splits = std::max<int64_t>(1, std::min<int64_t>(256 / tiles, nblk / 16));
+      p.splits = (int)cdiv(nblk, cdiv(nblk, splits));     // none empty
+      if (p.splits > 1) p.ws_bytes = (size_t)p.splits * m * n * sizeof(int);
+    }
+    return p;
+  }
+  const int64_t t128 = cdiv(m, 128) * cdiv(n, 128), t256 = cdiv(m, 256) * cdiv(n, 256), rest = t256 % 256;
+  const double nblk = (double)cdiv(k, kBlk), rounds = (double)(t256 / 256) + (rest > 0 ? 0.38 + 0.62 * rest / 256 : 0.0);
+  p.kind = rounds * (9.1 + 1.78 * nblk) < t128 * (0.0064 + 0.00216 * nblk) ? kInt8T256x256 : kInt8T128x128;
+  return p;
+}
+
+static Int8Plan grouped_plan(const Int8Args& p) {
+  const int64_t each = cdiv(p.m, std::min<int64_t>(p.m, p.experts));
+  return Int8Plan{each <= 16 ? kInt8Few16 : each <= 32 ? kInt8Few32 : each <= 64 ? kInt8T64x64 : each <= 200 ? kInt8T128x128 : kInt8T256x256, 1, 0};
+}
 
 hipError_t int8_matmul_launch(const Int8Plan& plan, const Int8Args& p, void* ws, hipStream_t s) {
-  if (p.y_dtype == kF32) return launch<float>(plan, p, ws, s);
-  if (p.y_dtype == kF16) return launch<_Float16>(plan, p, ws, s);
-  return launch<bf16>(plan, p, ws, s);
+  return launch<false>(plan, p, ws, s);
 }
 
-hipError_t int8_grouped_launch(const Int8Args& p, hipStream_t s) {
-  if (p.y_dtype == kF32) return launch_grouped<float>(p, s);
-  if (p.y_dtype == kF16) return launch_grouped<_Float16>(p, s);
-  return launch_grouped<bf16>(p, s);
-}
+hipError_t int8_grouped_launch(const Int8Args& p, hipStream_t s) { return launch<true>(grouped_plan(p), p, nullptr, s); }
 
 }  // namespace gptq

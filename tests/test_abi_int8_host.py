@@ -72,7 +72,7 @@ def test_grouped_refusals():
 
     assert call(m=-1) == SIZE and call(rx=-1) == SIZE and call(e=0) == SIZE and call(n=0) == SIZE and call(k=0) == SIZE
     assert call(rx=0) == SIZE and call(r=None) == SIZE                 # fewer rows than positions
-    assert call(m=1 << 21) == LARGE and call(rx=1 << 21) == LARGE and call(e=1 << 17) == LARGE
+    assert call(m=1 << 21) == LARGE and call(rx=1 << 21) == LARGE and call(e=4097) == LARGE
     assert call(k=1 << 17, ldx=1 << 17, ldw=1 << 17) == LARGE
     assert call(dt=3) == DTYPE
     for p in ("x", "sx", "off", "w", "sw", "y"):
