@@ -456,6 +456,7 @@ __device__ __forceinline__ void store_lines(T* __restrict__ Y, int64_t ld_y, int
 // how a work-group keeps its buffers full
 enum Flow {
   kBlocks,      // S buffers; one barrier per block
+  kHalves,      // 2 buffers; half a block's codes are read into registers while the half before is multiplied
   kAhead        // S buffers; a block's codes are read into registers while the one before is multiplied
 };
 
@@ -610,6 +611,50 @@ int8_dma_kernel(Int8Args p, int tiles_t, int tiles_n, int blocks_per_split, int*
           for (int a = 0; a < TN; ++a) acc[c][a] = Tile<M>::product(wv[k & 1][a], xv[k & 1][c], acc[c][a]);
         __builtin_amdgcn_sched_barrier(0);
       }
+    });
+  } else if constexpr (FLOW == kHalves) {
+    static_assert(S == 2 && WK == 1, "two buffers, one group");
+    constexpr int kHalf = KS / 2, kReads = kHalf * (TN + TT), kSlots = kHalf * TN * TT;
+    u32x4 wv[2][kHalf][TN], xv[2][kHalf][TT];
+    // read l of the half `set` of a block
+    const auto read = [&](int set, const Stage<BT>& x, const Stage<BN>& s, int l) {
+      const int k = l / (TN + TT), i = l % (TN + TT);
+      if (i < TN) wv[set][k][i] = pick(s.rows, w0, i, set * kHalf + k);
+      else xv[set][k][i - TN] = pick(x.rows, x0, i - TN, set * kHalf + k);
+    };
+    const auto half = [&](int set, auto&& meanwhile) {
+#pragma unroll
+      for (int e = 0; e < kSlots; ++e) {
+        const int k = e / (TN * TT), c = e % (TN * TT) / TN, a = e % TN;
+        meanwhile(e);
+        acc[c][a] = Tile<M>::product(wv[set][k][a], xv[set][k][c], acc[c][a]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    put_tail();
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    fetch(std::integral_constant<int, 1>{}, next(1));
+#pragma unroll
+    for (int l = 0; l < kReads; ++l) read(0, stage_x<BT, WK, 0>()[grp], stage_w<BN, WK, 0>()[grp], l);
+    run([&](auto i, bool) {
+      constexpr int h = i.value, to = h ^ 1;
+      half(0, [&](int e) {
+#pragma unroll
+        for (int l = 0; l < kReads; ++l)
+          if (l * kSlots / kReads == e) read(1, stage_x<BT, WK, h>()[grp], stage_w<BN, WK, h>()[grp], l);
+      });
+      // the next block has arrived, and every wave has read this one
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      const int b = next(step + 2);
+      ++step;
+      half(1, [&](int e) {
+#pragma unroll
+        for (int l = 0; l < kLoads; ++l)
+          if (l * kSlots / 2 / kLoads == e) fetch_one(stage_x<BT, WK, h>()[grp], stage_w<BN, WK, h>()[grp], b, l);
+#pragma unroll
+        for (int l = 0; l < kReads; ++l)
+          if (l * kSlots / kReads == e) read(0, stage_x<BT, WK, to>()[grp], stage_w<BN, WK, to>()[grp], l);
+      });
     });
   } else {
     static_assert(S % 2 == 0, "two sets of registers in turn");
@@ -810,7 +855,7 @@ hipError_t launch(const Int8Plan& plan, const Int8Args& p, void* ws, hipStream_t
     case kInt8T96x64: return launch_dma<GROUPED, 96, 64, 2, 2, 2, 3, kBlocks>(plan, p, parts, s);
     case kInt8T128x64: return launch_dma<GROUPED, 128, 64, 2, 2, 2, 3, kBlocks>(plan, p, parts, s);
     case kInt8T128x128Two: return launch_dma<GROUPED, 128, 128, 2, 2, 2, 2, kBlocks>(plan, p, parts, s);
-    case kInt8T256x256: return launch_dma<GROUPED, 256, 256, 2, 4, 1, 2, kBlocks>(plan, p, parts, s);
+    case kInt8T256x256: return launch_dma<GROUPED, 256, 256, 2, 4, 1, 2, kHalves>(plan, p, parts, s);
     default: return launch_dma<GROUPED, 128, 128, 2, 2, 1, 2, kBlocks>(plan, p, parts, s);
   }
 }
