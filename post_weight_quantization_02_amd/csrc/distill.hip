@@ -15,7 +15,16 @@
 //
 // Which vectors of a row hold listed tokens stands in LDS: a byte for each 16-byte vector,
 // the last listed token in it plus one, with a chain through the others.  All but a few
-// vectors cost one LDS byte.
+// vectors cost one LDS byte.  What of the listed tokens does not depend on the others is
+// worked out while the row is on its way; after its sums no step crosses lanes any more.
+//
+// HBM-bound on long texts: the gradient's row stays in registers between its two passes (1024
+// threads hold 256 KB; of a longer row the rest is read again), so 4096 x 65536 bf16 takes 220
+// us, 4.9 TB/s of the 5.15 that a large copy reaches (read twice: 259), 8192 x 32000 209, 1000 x
+// 128000 fp32 209 (298); the loss alone of 4096 x 65536 106 us, 5.0 TB/s.  517 x 50001 fp32
+// with 32 tokens 60 us: a row per CU, two rounds that read and write in step, and five rows
+// more.  Few short rows: a launch, and the chain of loads (ids, their logits), sums and logarithms: 5 us
+// for the loss, 8 with the gradient.
 #include "gptq_internal.h"
 
 namespace gptq {
@@ -33,14 +42,17 @@ typedef __bf16 b2 __attribute__((ext_vector_type(2)));
 struct F32 {
   typedef float elem;
   static constexpr int E = 4;           // elements of a 16-byte vector
+  static constexpr uint32_t kNone = 0xff800000u;      // a word of -inf
 };
 struct F16 {
   typedef _Float16 elem;
   static constexpr int E = 8;
+  static constexpr uint32_t kNone = 0xfc00fc00u;
 };
 struct BF16 {
   typedef __bf16 elem;
   static constexpr int E = 8;
+  static constexpr uint32_t kNone = 0xff80ff80u;
 };
 
 template <typename T>
@@ -73,16 +85,39 @@ __device__ __forceinline__ u32x4 pack(const float (&x)[T::E]) {
 
 __device__ __forceinline__ float fmaximum(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 __device__ __forceinline__ int lane_value(int v, int l) { return __builtin_amdgcn_readlane(v, l); }
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
-  return v;
+// a lane's v from a lane of its 16, `CTRL` lanes further (0x121: one, 0x122: two, ...)
+template <int CTRL>
+__device__ __forceinline__ float rotated(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
 }
-__device__ __forceinline__ float wave_maximum(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v = fmaximum(v, __shfl_xor(v, o, 64));
-  return v;
+template <int CTRL>
+__device__ __forceinline__ double rotated(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, 0xf, 0xf, true);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(b >> 32), CTRL, 0xf, 0xf, true);
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
+__device__ __forceinline__ float lane_value(float v, int l) {
+  return __builtin_bit_cast(float, lane_value(__builtin_bit_cast(int, v), l));
+}
+__device__ __forceinline__ double lane_value(double v, int l) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, ((uint64_t)(uint32_t)lane_value((int)(b >> 32), l) << 32) | (uint32_t)lane_value((int)(uint32_t)b, l));
+}
+// over the 64 lanes, the same in all of them, in one order whatever the values
+template <typename V, typename F>
+__device__ __forceinline__ V over_wave(V v, F&& f) {
+  v = f(v, rotated<0x128>(v));
+  v = f(v, rotated<0x124>(v));
+  v = f(v, rotated<0x122>(v));
+  v = f(v, rotated<0x121>(v));
+  return f(f(lane_value(v, 0), lane_value(v, 16)), f(lane_value(v, 32), lane_value(v, 48)));
+}
+template <typename V>
+__device__ __forceinline__ V wave_sum(V v) {
+  return over_wave(v, [](V a, V b) { return a + b; });
+}
+__device__ __forceinline__ float wave_maximum(float v) { return over_wave(v, [](float a, float b) { return fmaximum(a, b); }); }
 
 // maximum and sum over a part of the rest
 struct Sum {
@@ -107,51 +142,105 @@ struct Row {
   __device__ __forceinline__ u32x4 load(int i) const { return *(const u32x4_any*)(x + (int64_t)i * T::E); }
 };
 
-// The listed tokens of a row: lane j of a wave has token j.
+// What is known of a row's listed tokens before its sums are.
 struct Listed {
-  int id;               // negative: none
-  float z, t;           // its logit, and the teacher's value
-  bool out;             // some token of the row is not below v
-  bool any;             // some token is there
-  bool first;           // no earlier one is the same token
+  bool out, any;        // some token is not below v, is there
+  bool sound;           // the teacher's values are
+  float m;              // the maximum of their logits
+  double sum_u;         // e^((z - m) / T) over the tokens
+  double sum_q, terms;  // over the entries: q, and q (log q - (z - m) / T)
+  double rest, mass;    // q_r, Q
 };
 
-// What a work-group knows of the listed tokens.
+// What a work-group knows of them: in LDS, as the sums need the registers.
 template <int PLACES>
 struct Shared {
   uint8_t head[PLACES];
   int place[kMaxTop], element[kMaxTop], next[kMaxTop];      // next: the chain, 0 at its end
   float grad[kMaxTop];
+  double u[kMaxTop], given[kMaxTop];    // e^((z - m) / T), and the teacher's share of the token
   bool last[kMaxTop];   // the last one at its place
+  Listed listed;
 };
 
-template <typename T, int PLACES>
-__device__ __forceinline__ Listed read_listed(const DistillArgs& p, const Row<T>& r, int64_t row, int lane, Shared<PLACES>& sh) {
-  Listed l{-1, 0.f, -INFINITY, false, false, true};
+// Reads them, by one wave: lane j has token j.  Everything that does not depend on the row's
+// other tokens is taken here, while the row is on its way (ALL), or only where they are.
+template <bool ALL, typename T, int PLACES>
+__device__ __forceinline__ void read_listed(const DistillArgs& p, const Row<T>& r, int64_t row, int lane, Shared<PLACES>& sh) {
+  Listed l;
+  int id = -1;
+  float t = -INFINITY, z = -INFINITY;
   if (lane < p.top) {
-    l.id = p.ids[row * p.top + lane];
-    l.t = p.logprobs[row * p.top + lane];
+    id = p.ids[row * p.top + lane];
+    t = p.logprobs[row * p.top + lane];
   }
-  l.out = __any(l.id >= r.v);
-  l.any = __any(l.id >= 0);
-  if (l.id >= r.v) l.id = -1;
-  if (l.id >= 0) l.z = (float)r.x[l.id];
-  const int place = l.id >= 0 ? r.place(l.id) : -1;
+  l.out = __any(id >= r.v);
+  l.any = __any(id >= 0);
+  if (id >= r.v) id = -1;
+  const bool there = id >= 0;
+  if (there) z = (float)r.x[id];
+  else t = -INFINITY;
+  const int place = there ? r.place(id) : -1;
+  // two at one place, as good as never: chained, and the same token's entries joined
+  bool met = false;
+  int other = place;
+  for (int i = 1; i < p.top; ++i) {
+    other = __builtin_amdgcn_update_dpp(0, other, 0x13c, 0xf, 0xf, true);      // of the lane i before
+    met |= other == place;
+  }
+  // the teacher
+  const double inv = 1.0 / (double)p.temperature;
+  double lq = 0.0, q = 0.0;
+  l.rest = 0.0;
+  l.mass = 1.0;
+  if (!ALL) {
+  } else if (p.tail) {
+    lq = (double)t;
+    q = there ? exp(lq) : 0.0;
+    l.sum_q = wave_sum(q);
+    l.rest = l.sum_q < 1.0 ? 1.0 - l.sum_q : 0.0;
+    l.mass = l.sum_q + l.rest;
+    l.sound = l.sum_q < INFINITY;
+  } else {
+    const float top = wave_maximum(t);
+    lq = (double)(t - top) * inv;
+    q = there ? exp(lq) : 0.0;
+    const double sum = wave_sum(q);
+    q /= sum;
+    lq -= log(sum);
+    l.sum_q = 1.0;
+    l.sound = sum < INFINITY;
+  }
+  double given = q;
   int next = 0;
-  bool last = l.id >= 0;
-  for (int i = 0; i < p.top; ++i) {
-    const int other = lane_value(place, i);
-    if (other == place) {
-      if (i < lane) next = i + 1;
-      if (i > lane) last = false;
+  bool last = there, first = there;
+  if (__any(met && there)) {
+    given = 0.0;
+    for (int i = 0; i < p.top; ++i) {
+      const bool same = lane_value(id, i) == id;
+      const double o = lane_value(q, i);
+      if (lane_value(place, i) == place) {
+        if (i < lane) next = i + 1;
+        if (i > lane) last = false;
+      }
+      if (same && i < lane) first = false;
+      if (same) given += o;
     }
-    if (lane_value(l.id, i) == l.id && i < lane) l.first = false;
   }
   sh.place[lane] = place;
-  sh.element[lane] = l.id >= 0 ? r.element(l.id) : 0;
+  sh.element[lane] = there ? r.element(id) : 0;
   sh.next[lane] = next;
   sh.last[lane] = last;
-  return l;
+  if (!ALL) return;
+  // the student
+  l.m = fmaximum(wave_maximum(z), kLow);
+  const double d = ((double)z - (double)l.m) * inv;
+  const double u = there ? exp(d) : 0.0;
+  l.sum_u = wave_sum(first ? u : 0.0);
+  l.terms = wave_sum(there && q != 0.0 ? q * (lq - d) : 0.0);
+  sh.u[lane] = u;
+  sh.given[lane] = given;
+  if (lane == 0) sh.listed = l;
 }
 
 // head[i] for the places [first, last): every thread of the work-group takes part
@@ -198,7 +287,6 @@ __device__ __forceinline__ void add(Sum& a, const u32x4* ld, const int* heads, c
 }
 
 // an element alone
-template <int PLACES>
 __device__ __forceinline__ void add_one(Sum& a, float x, int head, float c) {
   if (head == 0) a = join(a, Sum{fmaximum(x, kLow), x > -INFINITY || x != x ? 1.f : 0.f}, c);
 }
@@ -208,9 +296,8 @@ __device__ __forceinline__ Sum over_threads(Sum a, float c) {
   __shared__ Sum part[THREADS / 64];
   const int t = threadIdx.x;
   const float m = wave_maximum(a.m);
-  float s = a.s * __builtin_amdgcn_exp2f((a.m - m) * c);
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o, 64);
+  const float s = wave_sum(a.s * __builtin_amdgcn_exp2f((a.m - m) * c));
+  if constexpr (THREADS == 64) return Sum{m, s};
   if ((t & 63) == 0) part[t >> 6] = Sum{m, s};
   __syncthreads();
   Sum r{kLow, 0.f};
@@ -227,56 +314,33 @@ struct Rest {
   bool constant;
 };
 
-// The row's loss and gradient from its sums, by one wave.  Rows without a teacher token have
-// loss and gradient 0, rows of weight 0 gradient 0, whatever their logits are.
+// The row's loss and gradient from its sums, by one wave.  With m the larger of the two
+// maxima, log p_j = (z_j - m) / T - log total, so the terms of the listed tokens are those
+// taken before, moved from their own maximum to m.  Rows without a teacher token have loss and
+// gradient 0, rows of weight 0 gradient 0, whatever their logits are.
 template <int PLACES>
-__device__ __forceinline__ Rest finish(const DistillArgs& p, int64_t row, const Listed& l, Sum r, bool store, Shared<PLACES>& sh) {
+__device__ __forceinline__ Rest finish(const DistillArgs& p, int64_t row, Sum r, bool store, Shared<PLACES>& sh) {
   const int lane = threadIdx.x & 63;
+  const Listed l = sh.listed;
   const double inv = 1.0 / (double)p.temperature;
-  const bool there = l.id >= 0;
-  // the teacher
-  double lq, q, rest = 0.0, mass = 1.0, sum;
-  if (p.tail) {
-    lq = there ? (double)l.t : -INFINITY;
-    q = there ? exp(lq) : 0.0;
-    sum = wave_sum(q);
-    rest = sum < 1.0 ? 1.0 - sum : 0.0;
-    mass = sum + rest;
-  } else {
-    const float top = wave_maximum(there ? l.t : -INFINITY);
-    lq = there ? (double)(l.t - top) * inv : -INFINITY;
-    q = there ? exp(lq) : 0.0;
-    sum = wave_sum(q);
-    q /= sum;
-    lq -= log(sum);
-  }
-  // the student
-  const float m = fmaximum(r.m, wave_maximum(there ? l.z : -INFINITY));
-  const double dz = ((double)l.z - (double)m) * inv, dr = ((double)r.m - (double)m) * inv;
-  const double u = there ? exp(dz) : 0.0, ur = exp(dr);
-  const double total = (double)r.s * ur + wave_sum(there && l.first ? u : 0.0);
-  const double log_total = log(total);
-  double term = there && q != 0.0 ? q * (lq - (dz - log_total)) : 0.0;
-  term = wave_sum(term);
-  if (rest > 0.0) term += rest * (log(rest) - (dr + log((double)r.s) - log_total));
-  const bool bad = l.out || !(fabsf(m) < INFINITY) || !(total > 0.0) || !(sum < INFINITY);
-  if (store && lane == 0) p.loss[row] = l.out ? NAN : !l.any ? 0.f : bad ? NAN : (float)term;
+  const float m = fmaximum(r.m, l.m);
+  const double dl = ((double)l.m - (double)m) * inv, dr = ((double)r.m - (double)m) * inv;
+  const double ul = exp(dl), ur = exp(dr);
+  const double total = (double)r.s * ur + l.sum_u * ul, log_total = log(total);
+  double loss = l.terms + l.sum_q * (log_total - dl);
+  if (l.rest > 0.0) loss += l.rest * (log(l.rest) - (dr + log((double)r.s) - log_total));
+  const bool bad = l.out || !(fabsf(m) < INFINITY) || !(total > 0.0) || !l.sound, none = !l.any;
+  if (store && lane == 0) p.loss[row] = none ? 0.f : bad ? NAN : (float)loss;
   if (!p.grad) return Rest{0.f, 0.f, true};
   const double w = (p.weights ? (double)p.weights[row] : 1.0) * inv;
-  if (w == 0.0 || (!l.any && !l.out) || bad) {
-    const float all = w == 0.0 || (!l.any && !l.out) ? 0.f : NAN;
+  if (none || bad || w == 0.0) {
+    const float all = none || w == 0.0 ? 0.f : NAN;
     sh.grad[lane] = all;
     return Rest{all, 0.f, true};
   }
-  double given = 0.0;           // by all entries of this token
-  for (int i = 0; i < p.top; ++i) {
-    const uint64_t b = __builtin_bit_cast(uint64_t, q);
-    const uint64_t o = ((uint64_t)(uint32_t)lane_value((int)(b >> 32), i) << 32) | (uint32_t)lane_value((int)(uint32_t)b, i);
-    if (lane_value(l.id, i) == l.id) given += __builtin_bit_cast(double, o);
-  }
-  sh.grad[lane] = (float)(w * (mass * u / total - given));
-  const double others = rest > 0.0 ? rest / (double)r.s : 0.0;
-  return Rest{(float)(w * (mass * ur / total - others)), r.m, false};
+  sh.grad[lane] = (float)(w * (l.mass * sh.u[lane] * ul / total - sh.given[lane]));
+  const double others = l.rest > 0.0 ? l.rest / (double)r.s : 0.0;
+  return Rest{(float)(w * (l.mass * ur / total - others)), r.m, false};
 }
 
 // the gradient of a vector
@@ -294,78 +358,168 @@ __device__ __forceinline__ typename T::elem gradient_one(typename T::elem x, Res
   return (typename T::elem)(g.constant ? g.factor : g.factor * __builtin_amdgcn_exp2f(((float)x - g.m) * c));
 }
 
-constexpr int kThreads = 256, kUnroll = 4;
+constexpr int kThreads = 256, kUnroll = 4;     // of a part; vectors under way per thread
 
 // sums of the rest over the places [first, last) of a row
-template <typename T>
+template <int THREADS, typename T>
 __device__ __forceinline__ Sum stream_sums(const Row<T>& r, int first, int last, float c, Shared<kSegment>& sh) {
   const int t = threadIdx.x;
   Sum a{kLow, 0.f};
   for (int lo = first; lo < last; lo += kSegment) {
     const int hi = min(lo + kSegment, last), vec = min(hi, r.nvec);
-    mark<kThreads>(sh, lo, hi);
-    for (int b = lo + t; b < vec; b += kThreads * kUnroll) {
+    mark<THREADS>(sh, lo, hi);
+    for (int b = lo + t; b < vec; b += THREADS * kUnroll) {
       u32x4 ld[kUnroll];
       int heads[kUnroll];
-      if (b + kThreads * (kUnroll - 1) < vec) {
+      if (b + THREADS * (kUnroll - 1) < vec) {
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-          ld[u] = r.load(b + kThreads * u);
-          heads[u] = sh.head[b + kThreads * u - lo];
+          ld[u] = r.load(b + THREADS * u);
+          heads[u] = sh.head[b + THREADS * u - lo];
         }
         add<T, kUnroll>(a, ld, heads, sh, c);
       } else {
-        for (int i = b; i < vec; i += kThreads) {
+        for (int i = b; i < vec; i += THREADS) {
           ld[0] = r.load(i);
           heads[0] = sh.head[i - lo];
           add<T, 1>(a, ld, heads, sh, c);
         }
       }
     }
-    for (int i = max(lo, r.nvec) + t; i < hi; i += kThreads)
-      add_one<kSegment>(a, (float)r.x[r.nvec * T::E + i - r.nvec], sh.head[i - lo], c);
+    for (int i = max(lo, r.nvec) + t; i < hi; i += THREADS)
+      add_one(a, (float)r.x[r.nvec * T::E + i - r.nvec], sh.head[i - lo], c);
   }
   return a;
 }
 
 // the gradient over the places [first, last)
-template <typename T>
+template <int THREADS, typename T>
 __device__ __forceinline__ void stream_grad(const DistillArgs& p, int64_t row, const Row<T>& r, int first, int last, Rest g,
                                             float c, Shared<kSegment>& sh) {
   const int t = threadIdx.x;
   auto* out = (typename T::elem*)p.grad + row * p.ld_grad;
   for (int lo = first; lo < last; lo += kSegment) {
     const int hi = min(lo + kSegment, last), vec = min(hi, r.nvec);
-    mark<kThreads>(sh, lo, hi);
-    for (int i = lo + t; i < vec; i += kThreads)
-      *(u32x4_any*)(out + (int64_t)i * T::E) = gradient<T>(r.load(i), sh.head[i - lo], g, sh, c);
-    for (int i = max(lo, r.nvec) + t; i < hi; i += kThreads) {
+    mark<THREADS>(sh, lo, hi);
+    for (int b = lo + t; b < vec; b += THREADS * kUnroll) {
+      u32x4 ld[kUnroll];
+      int heads[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int i = min(b + THREADS * u, vec - 1);
+        ld[u] = r.load(i);
+        heads[u] = sh.head[i - lo];
+      }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int i = b + THREADS * u;
+        const u32x4 o = gradient<T>(ld[u], heads[u], g, sh, c);
+        if (i < vec) __builtin_nontemporal_store(o, (u32x4_any*)(out + (int64_t)i * T::E));
+      }
+    }
+    for (int i = max(lo, r.nvec) + t; i < hi; i += THREADS) {
       const int e = r.nvec * T::E + i - r.nvec, h = sh.head[i - lo];
       out[e] = h != 0 ? (typename T::elem)sh.grad[h - 1] : gradient_one<T>(r.x[e], g, c);
     }
   }
 }
 
-// one work-group per row
-template <typename T, bool GRAD>
-__global__ __launch_bounds__(kThreads) void distill_row_kernel(DistillArgs p) {
+// a row per work-group, read from memory for its sums and again for its gradient
+template <typename T, int THREADS, bool GRAD>
+__global__ __launch_bounds__(THREADS) void distill_row_kernel(DistillArgs p) {
   __shared__ Shared<kSegment> sh;
   __shared__ Rest rest;
   const int t = threadIdx.x;
   const int64_t row = blockIdx.x;
   const float c = kLog2e / p.temperature;
   const Row<T> r(p, row);
-  Listed l{};
-  if (t < 64) l = read_listed<T>(p, r, row, t, sh);
-  const Sum a = over_threads<kThreads>(stream_sums<T>(r, 0, r.places(), c, sh), c);
+  if (t < 64) read_listed<true>(p, r, row, t, sh);
+  const Sum a = over_threads<THREADS>(stream_sums<THREADS>(r, 0, r.places(), c, sh), c);
   if (t < 64) {
-    const Rest g = finish(p, row, l, a, true, sh);
+    const Rest g = finish(p, row, a, true, sh);
     if (t == 0) rest = g;
   }
   if constexpr (GRAD) {
     __syncthreads();
-    stream_grad<T>(p, row, r, 0, r.places(), rest, c, sh);
+    stream_grad<THREADS>(p, row, r, 0, r.places(), rest, c, sh);
   }
+}
+
+// A row per work-group, kept in its registers: read once, written once.  MORE > 0: a longer
+// row, of which up to MORE vectors are read again, the last ones first.
+template <typename T, int VPT, int THREADS, int MORE>
+__global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(VPT == 16 ? 4 : VPT == 8 ? 5 : 6))) void
+distill_held_kernel(DistillArgs p) {
+  constexpr int kHeld = VPT * THREADS;
+  __shared__ Shared<kHeld + MORE + 16> sh;
+  __shared__ Rest rest;
+  const int t = threadIdx.x;
+  const int64_t row = blockIdx.x;
+  const float c = kLog2e / p.temperature;
+  const Row<T> r(p, row);
+  u32x4 ld[VPT];
+#pragma unroll
+  for (int u = 0; u < VPT; ++u)
+    ld[u] = __builtin_nontemporal_load((const u32x4_any*)(r.x + (int64_t)min(t + u * THREADS, r.nvec - 1) * T::E));
+  if (t < 64) read_listed<true>(p, r, row, t, sh);
+  mark<THREADS>(sh, 0, r.places());
+  Sum a{kLow, 0.f};
+  constexpr int kStep = 2;
+#pragma unroll
+  for (int u0 = 0; u0 < VPT; u0 += kStep) {
+    if (u0 * THREADS >= r.nvec) break;
+    int heads[kStep];
+#pragma unroll
+    for (int u = 0; u < kStep; ++u) {
+      const int i = t + (u0 + u) * THREADS;
+      if (i >= r.nvec) ld[u0 + u] = u32x4{T::kNone, T::kNone, T::kNone, T::kNone};
+      heads[u] = i < r.nvec ? sh.head[i] : 0;
+    }
+    add<T, kStep>(a, ld + u0, heads, sh, c);
+  }
+  const int behind = kHeld + (r.nvec - kHeld) / (2 * THREADS) * (2 * THREADS);      // no whole step from here on
+  if constexpr (MORE > 0) {
+    for (int i = kHeld + t; i < r.nvec; i += 2 * THREADS) {
+      const u32x4 two[2] = {r.load(i), r.load(min(i + THREADS, r.nvec - 1))};
+      const int heads[2] = {sh.head[i], sh.head[min(i + THREADS, r.nvec - 1)]};
+      if (i + THREADS < r.nvec) add<T, 2>(a, two, heads, sh, c);
+      else add<T, 1>(a, two, heads, sh, c);
+    }
+  }
+  const int e = r.nvec * T::E + t;
+  int head = 0;
+  float x = 0.f;
+  if (e < r.v) {
+    x = (float)r.x[e];
+    head = sh.head[r.nvec + t];
+    add_one(a, x, head, c);
+  }
+  const Sum sum = over_threads<THREADS>(a, c);
+  if (t < 64) {
+    const Rest g = finish(p, row, sum, true, sh);
+    if (t == 0) rest = g;
+  }
+  __syncthreads();
+  const Rest g = rest;
+  auto* out = (typename T::elem*)p.grad + row * p.ld_grad;
+  if constexpr (MORE > 0) {
+    for (int i = behind + t; i >= kHeld; i -= 2 * THREADS) {
+      const u32x4 two[2] = {r.load(min(i, r.nvec - 1)), r.load(min(i + THREADS, r.nvec - 1))};
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int at = i + u * THREADS;
+        if (at < r.nvec)
+          __builtin_nontemporal_store(gradient<T>(two[u], sh.head[at], g, sh, c), (u32x4_any*)(out + (int64_t)at * T::E));
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < VPT; ++u) {
+    const int i = t + u * THREADS;
+    if (i < r.nvec)
+      __builtin_nontemporal_store(gradient<T>(ld[u], sh.head[i], g, sh, c), (u32x4_any*)(out + (int64_t)i * T::E));
+  }
+  if (e < r.v) out[e] = head != 0 ? (typename T::elem)sh.grad[head - 1] : (typename T::elem)(g.constant ? g.factor : g.factor * __builtin_amdgcn_exp2f((x - g.m) * c));
 }
 
 // a part of a row per work-group: its sums ...
@@ -376,9 +530,9 @@ __global__ __launch_bounds__(kThreads) void distill_part_kernel(DistillArgs p, i
   const int64_t row = blockIdx.x / splits;
   const float c = kLog2e / p.temperature;
   const Row<T> r(p, row);
-  if (t < 64) read_listed<T>(p, r, row, t, sh);
+  if (t < 64) read_listed<false>(p, r, row, t, sh);
   const int part = (int)(blockIdx.x % splits), first = part * span, last = part == splits - 1 ? r.places() : first + span;
-  const Sum a = over_threads<kThreads>(stream_sums<T>(r, first, last, c, sh), c);
+  const Sum a = over_threads<kThreads>(stream_sums<kThreads>(r, first, last, c, sh), c);
   if (t == 0) parts[blockIdx.x] = a;
 }
 
@@ -393,29 +547,48 @@ __global__ __launch_bounds__(kThreads) void distill_join_kernel(DistillArgs p, i
   const float c = kLog2e / p.temperature;
   const Row<T> r(p, row);
   if (t < 64) {
-    const Listed l = read_listed<T>(p, r, row, t, sh);
+    read_listed<true>(p, r, row, t, sh);
     Sum a{kLow, 0.f};
     for (int i = t; i < splits; i += 64) a = join(a, parts[row * splits + i], c);
     const float m = wave_maximum(a.m);
-    a.s *= __builtin_amdgcn_exp2f((a.m - m) * c);
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) a.s += __shfl_xor(a.s, o, 64);
-    const Rest g = finish(p, row, l, Sum{m, a.s}, part == 0, sh);
+    const float sum = wave_sum(a.s * __builtin_amdgcn_exp2f((a.m - m) * c));
+    const Rest g = finish(p, row, Sum{m, sum}, part == 0, sh);
     if (t == 0) rest = g;
   }
   if constexpr (GRAD) {
     __syncthreads();
     const int first = part * span, last = part == splits - 1 ? r.places() : first + span;
-    stream_grad<T>(p, row, r, first, last, rest, c, sh);
+    stream_grad<kThreads>(p, row, r, first, last, rest, c, sh);
   }
 }
 
 template <typename T>
 hipError_t launch(const DistillPlan& plan, const DistillArgs& p, void* ws, hipStream_t s) {
   const unsigned n = (unsigned)p.n;
+  const int nvec = (int)(p.v / T::E);
+  // the smallest work-group and least registers that hold the row (8192 x 1500 bf16: 27 us by a
+  // wave, 40 by four)
+  if (plan.splits == 1 && p.grad && nvec > 0 && nvec <= 65536) {
+    const auto go = [&](auto vpt, auto threads, auto more) {
+      distill_held_kernel<T, vpt.value, threads.value, more.value><<<n, threads.value, 0, s>>>(p);
+    };
+    using std::integral_constant;
+    constexpr integral_constant<int, 0> none;
+    if (nvec <= 256) go(integral_constant<int, 4>{}, integral_constant<int, 64>{}, none);
+    else if (nvec <= 512) go(integral_constant<int, 8>{}, integral_constant<int, 64>{}, none);
+    else if (nvec <= 1024) go(integral_constant<int, 4>{}, integral_constant<int, 256>{}, none);
+    else if (nvec <= 2048) go(integral_constant<int, 8>{}, integral_constant<int, 256>{}, none);
+    else if (nvec <= 4096) go(integral_constant<int, 16>{}, integral_constant<int, 256>{}, none);
+    else if (nvec <= 8192) go(integral_constant<int, 16>{}, integral_constant<int, 512>{}, none);
+    else if (nvec <= 16384) go(integral_constant<int, 16>{}, integral_constant<int, 1024>{}, none);
+    else go(integral_constant<int, 16>{}, integral_constant<int, 1024>{}, integral_constant<int, 49152>{});
+    return hipGetLastError();
+  }
   if (plan.splits == 1) {
-    if (p.grad) distill_row_kernel<T, true><<<n, kThreads, 0, s>>>(p);
-    else distill_row_kernel<T, false><<<n, kThreads, 0, s>>>(p);
+    if (p.grad) distill_row_kernel<T, 1024, true><<<n, 1024, 0, s>>>(p);
+    // 200 x 128000 bf16: 14.5 us with 1024 threads, 20.2 with 256; 1 x 50001 and below the same
+    else if (nvec >= 8192) distill_row_kernel<T, 1024, false><<<n, 1024, 0, s>>>(p);
+    else distill_row_kernel<T, 256, false><<<n, 256, 0, s>>>(p);
     return hipGetLastError();
   }
   const int span = (int)(plan.span / T::E);
@@ -428,11 +601,17 @@ hipError_t launch(const DistillPlan& plan, const DistillArgs& p, void* ws, hipSt
 
 }  // namespace
 
-// Parts of a row: at least 2048 elements each, together some 1024 work-groups.
+// Parts of a row, of at least 4 KB and together at most 1024, where there are fewer long rows
+// than CUs to take them.  With a gradient, parts read the row twice: 64 x 33001 bf16 11.5 us
+// in parts, 14.6 whole, 1 x 40000 9.2 against 11.0, 1 x 128000 9.4 against 19.7; but 1 x 20000
+// 9.3 against 9.4, 64 x 3000 10.3 against 8.8, 200 x 33001 16.9 against 15.8.  The loss alone:
+// 1 x 40000 7.4 against 8.6, 64 x 128000 11.0 against 13.1; but 100 x 50001 fp32 11.6 against 9.0.
 DistillPlan distill_plan(int64_t n, int64_t v, int elem_bytes, bool grad) {
   DistillPlan p{1, v, 0};
-  const int64_t want = n >= 512 ? 1 : cdiv(1024, std::max<int64_t>(n, 1));
-  p.splits = (int)std::max<int64_t>(1, std::min(want, cdiv(v, 2048)));
+  const int64_t bytes = v * elem_bytes, least = (64 << 10) * (grad ? 1 : std::max<int64_t>(1, n / 20));
+  const int64_t want = n > 128 || bytes < least
+                           ? 1 : std::min(1024 / std::max<int64_t>(n, 1), bytes / ((4 << 10) * std::max<int64_t>(1, n / 16)));
+  p.splits = (int)std::max<int64_t>(1, want);
   if (p.splits > 1) {
     p.span = cdiv(cdiv(v, p.splits), 8) * 8;
     p.splits = (int)cdiv(v, p.span);
