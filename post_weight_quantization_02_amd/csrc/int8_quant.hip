@@ -11,13 +11,15 @@
 // HBM-bound: one read of X, one byte written per element.  A row lives in the registers of
 // one wave (short rows) or one work-group, in groups of 8 consecutive columns; magnitudes
 // are compared as bit patterns without the sign (two 16-bit ones per instruction).  Rounding
-// is an addition of 1.5 * 2^23, which leaves the code in the low byte.
+// is an addition of 1.5 * 2^23, which leaves the code in the low byte.  5003 x 11007 fp16, half
+// of its rows between words, 34.5 us, 4.8 TB/s, 93 % of what a large copy reaches (16-byte
+// loads at odd elements and a last group taken element by element cost 10 us more); 8192 x
+// 12288 fp16 56.5 us, 16384 x 4095 bf16 39.5; 1 x 4096 2.5 us, a launch.
 #include "gptq_internal.h"
 
 namespace gptq {
 namespace {
 
-constexpr int kThreads = 256;
 constexpr float kFloor = 0x1p-100f;
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef uint16_t us2 __attribute__((ext_vector_type(2)));
@@ -41,24 +43,32 @@ struct BF16 {
   static constexpr uint32_t kInf = 0x7f80u;
 };
 
-__device__ __forceinline__ int valid_from(int64_t left) { return left >= 8 ? 8 : left > 0 ? (int)left : 0; }
-
-// `valid` elements from p on, the others zero
+// 8 elements from p on.  odd: p lies between two 32-bit words, inside a row; such 16-byte
+// loads cost twice, so they start half a word before and are shifted.
 template <typename T>
-__device__ __forceinline__ void load8(const typename T::elem* __restrict__ p, int valid, uint32_t (&w)[T::kWords]) {
-  if (valid >= 8) {
-#pragma unroll
-    for (int q = 0; q < T::kWords / 4; ++q) {
-      const u32x4_any v = *(const u32x4_any*)((const uint32_t*)p + 4 * q);
-      w[4 * q] = v[0]; w[4 * q + 1] = v[1]; w[4 * q + 2] = v[2]; w[4 * q + 3] = v[3];
-    }
+__device__ __forceinline__ void load8(const typename T::elem* __restrict__ p, bool odd, uint32_t (&w)[T::kWords]) {
+  if (T::kWords == 4 && odd) {
+    const u32x4_any v = *(const u32x4_any*)(p - 1);
+    const uint32_t next = *(const uint32_t*)(p + 7);
+    w[0] = __builtin_amdgcn_alignbit(v[1], v[0], 16); w[1] = __builtin_amdgcn_alignbit(v[2], v[1], 16);
+    w[2] = __builtin_amdgcn_alignbit(v[3], v[2], 16); w[3] = __builtin_amdgcn_alignbit(next, v[3], 16);
     return;
   }
+#pragma unroll
+  for (int q = 0; q < T::kWords / 4; ++q) {
+    const u32x4_any v = *(const u32x4_any*)((const uint32_t*)p + 4 * q);
+    w[4 * q] = v[0]; w[4 * q + 1] = v[1]; w[4 * q + 2] = v[2]; w[4 * q + 3] = v[3];
+  }
+}
+
+// the first n < 8 from p on, the others zero
+template <typename T>
+__device__ __forceinline__ void load_few(const typename T::elem* __restrict__ p, int n, uint32_t (&w)[T::kWords]) {
 #pragma unroll
   for (int q = 0; q < T::kWords; ++q) w[q] = 0u;
 #pragma unroll
   for (int e = 0; e < 8; ++e)
-    if (e < valid) {
+    if (e < n) {
       if constexpr (T::kWords == 8) w[e] = __builtin_bit_cast(uint32_t, p[e]);
       else w[e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
     }
@@ -93,8 +103,8 @@ __device__ __forceinline__ float mag_value(uint32_t a) {
   else return __builtin_bit_cast(float, a << 16);
 }
 
-template <typename T>
-__device__ __forceinline__ void store8(const uint32_t (&w)[T::kWords], float inv, uint8_t* __restrict__ p, int valid) {
+template <typename T, bool FEW>
+__device__ __forceinline__ void store8(const uint32_t (&w)[T::kWords], float inv, uint8_t* __restrict__ p, int n) {
 #pragma clang fp contract(off)      // the product is rounded before it is rounded to a whole number
   uint32_t c[2];
 #pragma unroll
@@ -108,45 +118,71 @@ __device__ __forceinline__ void store8(const uint32_t (&w)[T::kWords], float inv
     const uint32_t lo = __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u), hi = __builtin_amdgcn_perm(b[3], b[2], 0x04000c0cu);
     c[h] = lo | hi;
   }
-  if (valid >= 8) {
+  if (!FEW) {
     *(u32x2_any*)p = u32x2_any{c[0], c[1]};
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      if (e < valid) p[e] = (uint8_t)(c[e >> 2] >> (8 * (e & 3)));
+      if (e < n) p[e] = (uint8_t)(c[e >> 2] >> (8 * (e & 3)));
   }
 }
 
-// One row per LANES threads (a wave, or the work-group), G groups of 8 columns each at a
-// time; a row of more is read again when its scale is known.
-template <typename T, int LANES, int G>
-__global__ __launch_bounds__(kThreads) void int8_rows_kernel(const typename T::elem* __restrict__ X, int64_t m, int64_t k,
-                                                             int64_t ld_x, uint8_t* __restrict__ codes, int64_t ld_codes,
-                                                             float* __restrict__ scales) {
+// largest over the LANES lanes of a row (16 or 64), in every lane of it
+template <int LANES>
+__device__ __forceinline__ uint32_t over_lanes(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xf, 0xf, true));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x124, 0xf, 0xf, true));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x122, 0xf, 0xf, true));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x121, 0xf, 0xf, true));
+  if constexpr (LANES == 64) {
+    const auto of = [&](int l) { return (uint32_t)__builtin_amdgcn_readlane((int)v, l); };
+    v = max(max(of(0), of(16)), max(of(32), of(48)));
+  }
+  return v;
+}
+
+// One row per LANES threads (a quarter of a wave, a wave, or the work-group), G groups of 8
+// columns each at a time; a row of more is read again when its scale is known.  A last group
+// of fewer columns is the row's last 8, so some codes are written twice, alike.  FEW: rows of
+// fewer than 8.
+template <typename T, int LANES, int G, bool FEW>
+__global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void int8_rows_kernel(
+    const typename T::elem* __restrict__ X, int64_t m, int k, int64_t ld_x, uint8_t* __restrict__ codes, int64_t ld_codes,
+    float* __restrict__ scales) {
+  constexpr int kThreads = LANES < 256 ? 256 : LANES, kSpan = LANES * G * 8;
   __shared__ uint32_t part[kThreads / 64];
   const int t = threadIdx.x, lane = t % LANES;
   const int64_t row = (int64_t)blockIdx.x * (kThreads / LANES) + t / LANES;
-  if (LANES == 64 && row >= m) return;
-  const auto* x = X + row * ld_x;
+  const bool there = LANES >= 256 || row < m;
+  const auto* x = X + (there ? row : 0) * ld_x;
   uint8_t* out = codes + row * ld_codes;
-  constexpr int64_t kSpan = (int64_t)LANES * G * 8;
+  const bool odd = T::kWords == 4 && ((uintptr_t)x & 2) != 0;
   uint32_t w[G][T::kWords], a = 0u;
-  const auto load = [&](int64_t c0) {
+  const auto column = [&](int c0, int g) { return c0 + (g * LANES + lane) * 8; };
+  // no lane of the work-group has columns
+  const auto none = [&](int c0, int g) { return g > 0 && c0 + g * LANES * 8 >= k; };
+  const auto load = [&](int c0) {
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      const int64_t col = c0 + (g * LANES + lane) * 8;
-      load8<T>(x + min(col, k - 1), valid_from(k - col), w[g]);
+      if (FEW) {
+        load_few<T>(x, k, w[g]);
+      } else if (none(c0, g)) {
+#pragma unroll
+        for (int q = 0; q < T::kWords; ++q) w[g][q] = 0u;
+      } else {
+        const int c = min(column(c0, g), k - 8);
+        load8<T>(x + c, odd && c > 0 && c + 8 < k, w[g]);
+      }
     }
   };
-  for (int64_t c0 = 0; c0 < k; c0 += kSpan) {
+  for (int c0 = 0; c0 < k; c0 += kSpan) {
     load(c0);
 #pragma unroll
     for (int g = 0; g < G; ++g) a = mag8<T>(w[g], a);
   }
   if constexpr (T::kWords == 4) a = max(a & 0xffffu, a >> 16);
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) a = max(a, (uint32_t)__shfl_xor((int)a, o, 64));
-  if constexpr (LANES == kThreads) {
+  a = over_lanes<LANES == 16 ? 16 : 64>(a);
+  if constexpr (LANES >= 256) {
     if ((t & 63) == 0) part[t >> 6] = a;
     __syncthreads();
 #pragma unroll
@@ -154,11 +190,11 @@ __global__ __launch_bounds__(kThreads) void int8_rows_kernel(const typename T::e
   }
   const bool sound = a < T::kInf;
   const float top = fmaxf(mag_value<T>(a), kFloor);
-  const float inv = 127.f * (1.f / top);
-  if (lane == 0) scales[row] = sound ? top / 127.f : NAN;
-  for (int64_t c0 = 0; c0 < k; c0 += kSpan) {
+  const float inv = sound ? 127.f * (1.f / top) : 0.f;
+  if (lane == 0 && there) scales[row] = sound ? top / 127.f : NAN;
+  for (int c0 = 0; c0 < k; c0 += kSpan) {
     if (k > kSpan) load(c0);
-    if (!sound) {
+    if (!sound) {             // nothing times 0 is NaN
 #pragma unroll
       for (int g = 0; g < G; ++g)
 #pragma unroll
@@ -166,32 +202,36 @@ __global__ __launch_bounds__(kThreads) void int8_rows_kernel(const typename T::e
     }
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      const int64_t col = c0 + (g * LANES + lane) * 8;
-      store8<T>(w[g], sound ? inv : 0.f, out + col, valid_from(k - col));
+      const int c = column(c0, g);
+      if (there && c < k && !none(c0, g)) store8<T, FEW>(w[g], inv, out + (FEW ? 0 : min(c, k - 8)), k);
     }
   }
-}
-
-template <typename T, int LANES, int G>
-void launch_rows(const void* X, int64_t m, int64_t k, int64_t ld_x, uint8_t* codes, int64_t ld_codes, float* scales,
-                 hipStream_t s) {
-  int8_rows_kernel<T, LANES, G><<<dim3((unsigned)cdiv(m, kThreads / LANES)), kThreads, 0, s>>>(
-      (const typename T::elem*)X, m, k, ld_x, codes, ld_codes, scales);
 }
 
 template <typename T>
 void launch(const void* X, int64_t m, int64_t k, int64_t ld_x, uint8_t* codes, int64_t ld_codes, float* scales,
             hipStream_t s) {
-  const auto go = [&](auto lanes, auto groups) {
-    launch_rows<T, lanes.value, groups.value>(X, m, k, ld_x, codes, ld_codes, scales, s);
+  const auto go = [&](auto lanes, auto groups, auto few) {
+    constexpr int kThreads = lanes.value < 256 ? 256 : lanes.value;
+    int8_rows_kernel<T, lanes.value, groups.value, few.value>
+        <<<dim3((unsigned)cdiv(m, kThreads / lanes.value)), kThreads, 0, s>>>((const typename T::elem*)X, m, (int)k, ld_x,
+                                                                             codes, ld_codes, scales);
   };
   using std::integral_constant;
-  if (k <= 512) go(integral_constant<int, 64>{}, integral_constant<int, 1>{});
-  else if (k <= 1024) go(integral_constant<int, 64>{}, integral_constant<int, 2>{});
-  else if (k <= 2048) go(integral_constant<int, 256>{}, integral_constant<int, 1>{});
-  else if (k <= 4096) go(integral_constant<int, 256>{}, integral_constant<int, 2>{});
-  else if (k <= 8192) go(integral_constant<int, 256>{}, integral_constant<int, 4>{});
-  else go(integral_constant<int, 256>{}, integral_constant<int, 8>{});
+  const std::false_type no;
+  // the fewest lanes and groups that hold the row: 16384 x 128 bf16 3.7 us by quarters of
+  // waves, 6.1 by waves; 16384 x 1000 10.9 by waves, 14.6 by work-groups of 256; 5003 x 11007
+  // fp16 34.5 by 512 threads, 36.7 by 256, whose six groups leave room for fewer waves
+  if (k < 8) return go(integral_constant<int, 16>{}, integral_constant<int, 1>{}, std::true_type{});
+  if (k <= 128) return go(integral_constant<int, 16>{}, integral_constant<int, 1>{}, no);
+  if (k <= 256) return go(integral_constant<int, 16>{}, integral_constant<int, 2>{}, no);
+  if (k <= 512) return go(integral_constant<int, 64>{}, integral_constant<int, 1>{}, no);
+  if (k <= 1024) return go(integral_constant<int, 64>{}, integral_constant<int, 2>{}, no);
+  if (k <= 2048) return go(integral_constant<int, 256>{}, integral_constant<int, 1>{}, no);
+  if (k <= 4096) return go(integral_constant<int, 256>{}, integral_constant<int, 2>{}, no);
+  if (k <= 8192) return go(integral_constant<int, 256>{}, integral_constant<int, 4>{}, no);
+  if (k <= 12288) return go(integral_constant<int, 512>{}, integral_constant<int, 3>{}, no);
+  return go(integral_constant<int, 512>{}, integral_constant<int, 4>{}, no);
 }
 
 }  // namespace
