@@ -105,8 +105,9 @@ hipError_t fp8_matmul_launch(const Fp8Plan& plan, const Fp8Args& p, void* ws, hi
 hipError_t int8_quantize_launch(const void* X, int x_dtype, int64_t m, int64_t k, int64_t ld_x, int8_t* codes,
                                 int64_t ld_codes, float* scales, hipStream_t s);
 
-enum { kInt8Few16, kInt8Few32, kInt8Few64, kInt8T64x32, kInt8T64x64, kInt8T96x64, kInt8T128x64, kInt8T128x128Two,
-       kInt8T128x128, kInt8T256x256 };      // positions (at most) x rows of W
+// positions (at most) x rows of W; few rows: waves along k, or with rows of W of their own
+enum { kInt8Few16, kInt8Few16Own, kInt8Few16OwnDeep, kInt8Few32, kInt8Few64, kInt8T64x32, kInt8T64x64, kInt8T96x64,
+       kInt8T128x64, kInt8T128x128Two, kInt8T128x128, kInt8T256x256 };
 struct Int8Plan {
   int kind;
   int splits;             // parts of k, summed by a second launch when more than one

@@ -77,20 +77,6 @@ __device__ __forceinline__ void load_channels(const float* __restrict__ sw, cons
     b[e] = bias ? (float)bias[at] : -0.f;
   }
 }
-// the same where all four are there
-template <typename T>
-__device__ __forceinline__ void load_channels_inside(const float* __restrict__ sw, const T* __restrict__ bias, int64_t j,
-                                                     f32x4& s, f32x4& b) {
-  typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
-  typedef T T4_any __attribute__((ext_vector_type(4), aligned(2)));
-  s = *(const f32x4_any*)(sw + j);
-  b = f32x4{-0.f, -0.f, -0.f, -0.f};
-  if (bias) {
-    const T4_any v = *(const T4_any*)(bias + j);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) b[e] = (float)v[e];
-  }
-}
 
 // The positions of one expert that a work-group takes: [i0, end), at most BT of them, and
 // the number of such tiles before.  Without experts, all rows are one's.
@@ -99,41 +85,60 @@ struct Rows {
   int expert;
 };
 
-// Tile `slot` of the experts' tiles of BT positions, each expert starting one of its own;
-// expert < 0: there are not so many.  Offsets are taken within [0, m], and an expert that
-// ends before it starts has none.  Every lane of a wave takes part; the result is uniform.
-template <int BT>
-__device__ __forceinline__ Rows find_rows(const Int8Args& p, int slot, int& total) {
-  const int lane = threadIdx.x & 63, m = (int)p.m;
-  const int per = (p.experts + 63) / 64, e0 = min(lane * per, p.experts), e1 = min(e0 + per, p.experts);
-  const auto at = [&](int e) { return min(max(p.offsets[e], 0), m); };
-  int mine = 0, from = at(e0);
-  for (int e = e0; e < e1; ++e) {
-    const int to = at(e + 1);
-    mine += (max(to - from, 0) + BT - 1) / BT;
-    from = to;
-  }
-  int upto = mine;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int v = __shfl_up(upto, o, 64);
-    if (lane >= o) upto += v;
-  }
-  total = __builtin_amdgcn_readlane(upto, 63);
-  if (slot >= total) return Rows{0, 0, -1};
-  const int l = __builtin_ctzll(__ballot(upto > slot));      // the first lane that has it
-  int before = __builtin_amdgcn_readlane(upto - mine, l);
-  int e = __builtin_amdgcn_readlane(e0, l);
-  for (; e < p.experts; ++e) {                                // within that lane's experts
-    const int a = at(e), b = at(e + 1), tiles = (max(b - a, 0) + BT - 1) / BT;
-    if (slot < before + tiles) {
-      const int i0 = a + (slot - before) * BT;
-      return Rows{i0, min(i0 + BT, b), e};
-    }
-    before += tiles;
-  }
-  return Rows{0, 0, -1};
+// sum over the lanes up to this one
+__device__ __forceinline__ int lanes_up_to(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, true);
+  return v;
 }
+
+// The experts' tiles of BT positions, each expert starting one of its own: a lane has the
+// experts [e0, e1).  Offsets are taken within [0, m], and an expert that ends before it starts
+// has none.  Every lane of a wave takes part, and results are uniform.
+template <int BT>
+struct Experts {
+  int e0, from, to;     // of the lane's first expert
+  int mine, upto;       // tiles of the lane's, and of all up to them
+  int total;
+  static __device__ __forceinline__ int at(const Int8Args& p, int e) { return min(max(p.offsets[e], 0), (int)p.m); }
+  static __device__ __forceinline__ int tiles(int a, int b) { return (max(b - a, 0) + BT - 1) / BT; }
+  __device__ __forceinline__ explicit Experts(const Int8Args& p) {
+    const int lane = threadIdx.x & 63, per = (p.experts + 63) / 64, e1 = min((lane + 1) * per, p.experts);
+    e0 = min(lane * per, p.experts);
+    from = at(p, e0);
+    to = at(p, min(e0 + 1, p.experts));
+    mine = e0 < e1 ? tiles(from, to) : 0;
+    int a = to;
+    for (int e = e0 + 1; e < e1; ++e) {
+      const int b = at(p, e + 1);
+      mine += tiles(a, b);
+      a = b;
+    }
+    upto = lanes_up_to(mine);
+    total = __builtin_amdgcn_readlane(upto, 63);
+  }
+  // tile `slot`; expert < 0: there are not so many
+  __device__ __forceinline__ Rows find(const Int8Args& p, int slot) const {
+    if (slot >= total) return Rows{0, 0, -1};
+    const int l = __builtin_ctzll(__ballot(upto > slot));      // the first lane that has it
+    int before = __builtin_amdgcn_readlane(upto - mine, l);
+    int a = __builtin_amdgcn_readlane(from, l), b = __builtin_amdgcn_readlane(to, l);
+    for (int e = __builtin_amdgcn_readlane(e0, l); e < p.experts; ++e) {      // within that lane's experts
+      if (slot < before + tiles(a, b)) {
+        const int i0 = a + (slot - before) * BT;
+        return Rows{i0, min(i0 + BT, b), e};
+      }
+      before += tiles(a, b);
+      a = b;
+      b = at(p, min(e + 2, p.experts));
+    }
+    return Rows{0, 0, -1};
+  }
+};
 
 // the row of X that position i takes, within X; a bad one is noted in its scale
 __device__ __forceinline__ int64_t row_of(const Int8Args& p, int64_t i) {
@@ -158,8 +163,7 @@ __global__ __launch_bounds__(256) void int8_tile_kernel(Int8Args p) {
   const int t = threadIdx.x, lane = t & 63, w = t >> 6;
   Rows g{(int64_t)blockIdx.y * kTile, p.m, 0};
   if constexpr (GROUPED) {
-    int total;
-    g = find_rows<kTile>(p, blockIdx.y, total);
+    g = Experts<kTile>(p).find(p, blockIdx.y);
     if (g.expert < 0) return;
   }
   const int64_t j0 = (int64_t)blockIdx.x * kTile, last = g.end - 1;
@@ -224,111 +228,141 @@ __global__ __launch_bounds__(256) void int8_tile_kernel(Int8Args p) {
 
 
 // ---------------------------------------------------------------- few rows
-// At most 16 TT positions.  A work-group takes 16 rows of W, its waves every fourth block of
-// 128 columns, and the waves' sums meet in LDS at the end.  Each wave streams its blocks of
-// W, and the rows of X with them, through a ring of R LDS slots of its own, filled by direct
-// loads R - 1 blocks ahead: no barriers, and nothing in flight holds registers.  HBM-bound on
-// W.  A last block of fewer than 128 columns goes through registers, asked for first and
+// At most 16 TT positions.  A wave takes 16 TN rows of W.  The four waves of a work-group take
+// every fourth block of 128 columns of the same rows, and their sums meet in LDS at the end
+// (KW = 4), or rows of their own (KW = 1).  Each wave streams its blocks of W, and the rows of
+// X with them, through a ring of R LDS slots of its own, filled by direct loads R - 1 blocks
+// ahead: no barriers, and nothing in flight holds registers.  HBM-bound on W.  A last block of fewer than 128 columns goes through registers, asked for first and
 // multiplied last.
 constexpr int kFewWaves = 4;
 
-template <int TT>
+template <int TT, int TN>
 struct __attribute__((aligned(16))) Slot {
-  uint8_t w[16 * kBlk];
+  uint8_t w[16 * TN * kBlk];
   uint8_t x[16 * TT * kBlk];
 };
-template <int TT, int I>
-__device__ __forceinline__ Slot<TT> (&slots())[kFewWaves] {
-  __shared__ Slot<TT> s[kFewWaves];
+template <int TT, int TN, int I>
+__device__ __forceinline__ Slot<TT, TN> (&slots())[kFewWaves] {
+  __shared__ Slot<TT, TN> s[kFewWaves];
   return s;
 }
 
-template <int TT, int R, bool DMA, bool GROUPED>
-__global__ __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_per_eu(TT == 4 ? 1 : 2))) void
+template <int TT, int TN, int KW, int R, bool DMA, bool GROUPED>
+__global__ __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_per_eu(TT * TN >= 4 ? 1 : 2))) void
 int8_few_kernel(Int8Args p) {
-  __shared__ i32x4 part[kFewWaves][TT][64];
+  static_assert(KW == 1 || KW == kFewWaves, "waves along the columns");
+  constexpr int kOwn = KW == 1 ? TT * TN : (TT * TN + KW - 1) / KW;      // tiles that a wave stores
+  __shared__ i32x4 part[KW][KW == 1 ? 1 : TT * TN][64];
   const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
-  const int lr = lane & 15, q = lane >> 4;
+  const int lr = lane & 15, q = lane >> 4, wk = KW == 1 ? 0 : w;
   Rows g{0, p.m, 0};
   if constexpr (GROUPED) {
-    int total;
-    g = find_rows<16 * TT>(p, blockIdx.y, total);
+    g = Experts<16 * TT>(p).find(p, blockIdx.y);
     if (g.expert < 0) return;
   }
   const uint8_t* W = p.W + g.expert * p.stride_w;
-  const int64_t j0 = (int64_t)blockIdx.x * 16;
-  const int rows_w = (int)min<int64_t>(16, p.n - j0), rows_x = (int)(g.end - g.i0);
-  const int full = (int)(p.k / kBlk), nblk = (int)((p.k + kBlk - 1) / kBlk);
-  i32x4 acc[TT];
+  const int64_t j0 = ((int64_t)blockIdx.x * (kFewWaves / KW) + (KW == 1 ? w : 0)) * (16 * TN);
+  if (KW == 1 && j0 >= p.n) return;
+  const int rows_w = (int)min<int64_t>(16 * TN, p.n - j0), rows_x = (int)(g.end - g.i0);
+  // the scales and biases of the tiles that this wave stores, asked for first
+  float sx[kOwn];
+  f32x4 sw[kOwn], bias[kOwn];
+  const auto own = [&](int o) { return KW == 1 ? o : o * KW + w; };
+  with_type(p.y_dtype, [&](auto zero) {
+    typedef decltype(zero) T;
 #pragma unroll
-  for (int c = 0; c < TT; ++c) acc[c] = i32x4{0, 0, 0, 0};
-  const uint8_t* const wrow = W + (j0 + min(lr, rows_w - 1)) * p.ld_w;
+    for (int o = 0; o < kOwn; ++o) {
+      const int e = min(own(o), TT * TN - 1);
+      load_channels<T>(p.sw + (int64_t)g.expert * p.n, p.bias ? (const T*)p.bias + (int64_t)g.expert * p.n : nullptr,
+                       j0 + 16 * (e % TN) + 4 * q, p.n, sw[o], bias[o]);
+      sx[o] = scale_of(p, min(g.i0 + 16 * (e / TN) + lr, g.end - 1));
+    }
+  });
+  const int full = (int)(p.k / kBlk), nblk = (int)((p.k + kBlk - 1) / kBlk);
+  i32x4 acc[TT][TN];
+#pragma unroll
+  for (int c = 0; c < TT; ++c)
+#pragma unroll
+    for (int a = 0; a < TN; ++a) acc[c][a] = i32x4{0, 0, 0, 0};
+  const auto wrow = [&](int a) { return W + (j0 + min(16 * a + lr, rows_w - 1)) * p.ld_w; };
   const auto xrow = [&](int c) { return p.X + row_of(p, g.i0 + min(16 * c + lr, rows_x - 1)) * p.ld_x; };
   if constexpr (!DMA) {
     // blocks through registers, where rows may start anywhere
-    for (int b = w; b < nblk; b += kFewWaves)
+    for (int b = wk; b < nblk; b += KW)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int64_t at = (int64_t)b * kBlk + 64 * h + 16 * q;
-        const u32x4 wv = load_chunk(wrow, at, p.k);
+        u32x4 xv[TT];
 #pragma unroll
-        for (int c = 0; c < TT; ++c) acc[c] = Tile<16>::product(wv, load_chunk(xrow(c), at, p.k), acc[c]);
+        for (int c = 0; c < TT; ++c) xv[c] = load_chunk(xrow(c), at, p.k);
+#pragma unroll
+        for (int a = 0; a < TN; ++a) {
+          const u32x4 wv = load_chunk(wrow(a), at, p.k);
+#pragma unroll
+          for (int c = 0; c < TT; ++c) acc[c][a] = Tile<16>::product(wv, xv[c], acc[c][a]);
+        }
       }
   } else {
-    const int mine = full > w ? (full - w + kFewWaves - 1) / kFewWaves : 0;      // whole blocks w, w + 4, ...
+    const int mine = full > wk ? (full - wk + KW - 1) / KW : 0;      // whole blocks wk, wk + KW, ...
     const __amdgpu_buffer_rsrc_t wb = rsrc(W + j0 * p.ld_w, (rows_w - 1) * p.ld_w + p.k);
     // gathered rows lie anywhere in X, others are neighbours
     const __amdgpu_buffer_rsrc_t xb = p.rows ? rsrc(p.X, (p.rows_x - 1) * p.ld_x + p.k)
                                              : rsrc(p.X + g.i0 * p.ld_x, (rows_x - 1) * p.ld_x + p.k);
     const int ch = ((lane & 7) ^ (lane >> 3)) * 16;
-    uint32_t wo[2], xo[2 * TT];
+    uint32_t wo[2 * TN], xo[2 * TT];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) wo[j] = (uint32_t)(min(8 * j + (lane >> 3), rows_w - 1) * p.ld_w) + ch;
+    for (int j = 0; j < 2 * TN; ++j) wo[j] = (uint32_t)(min(8 * j + (lane >> 3), rows_w - 1) * p.ld_w) + ch;
 #pragma unroll
     for (int j = 0; j < 2 * TT; ++j) {
       const int r = min(8 * j + (lane >> 3), rows_x - 1);
       xo[j] = (uint32_t)((p.rows ? row_of(p, g.i0 + r) : r) * p.ld_x) + ch;
     }
-    const auto block_of = [&](int i) { return i < mine ? w + kFewWaves * i : 0; };
-    const auto fetch = [&](Slot<TT>& s, int b) {
+    const auto block_of = [&](int i) { return i < mine ? wk + KW * i : 0; };
+    const auto fetch = [&](Slot<TT, TN>& s, int b) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) load16_to_lds(wb, s.w + 8 * j * kBlk, wo[j], b * kBlk);
+      for (int j = 0; j < 2 * TN; ++j) load16_to_lds(wb, s.w + 8 * j * kBlk, wo[j], b * kBlk);
 #pragma unroll
       for (int j = 0; j < 2 * TT; ++j) load16_to_lds(xb, s.x + 8 * j * kBlk, xo[j], b * kBlk);
     };
-    constexpr int kLoads = 2 + 2 * TT;
-    static_assert((R - 1) * kLoads < 64, "counted by vmcnt");
+    constexpr int kLoads = 2 * TN + 2 * TT;
+    static_assert(R > 1 && (R - 1) * kLoads < 64, "counted by vmcnt");
     const uint32_t a0 = (uint32_t)(lr * kBlk + ((q ^ (lr & 7)) * 16));
-    const auto use = [&](const Slot<TT>& s) {
+    const auto use = [&](const Slot<TT, TN>& s) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const u32x4 wv = *(const u32x4*)(s.w + (a0 ^ (64 * h)));
+        u32x4 xv[TT];
 #pragma unroll
-        for (int c = 0; c < TT; ++c)
-          acc[c] = Tile<16>::product(wv, *(const u32x4*)(s.x + 16 * c * kBlk + (a0 ^ (64 * h))), acc[c]);
+        for (int c = 0; c < TT; ++c) xv[c] = *(const u32x4*)(s.x + 16 * c * kBlk + (a0 ^ (64 * h)));
+#pragma unroll
+        for (int a = 0; a < TN; ++a) {
+          const u32x4 wv = *(const u32x4*)(s.w + 16 * a * kBlk + (a0 ^ (64 * h)));
+#pragma unroll
+          for (int c = 0; c < TT; ++c) acc[c][a] = Tile<16>::product(wv, xv[c], acc[c][a]);
+        }
       }
     };
     // a last block of fewer columns: asked for before the others, multiplied after them
-    const bool tail = full < nblk && full % kFewWaves == w;
+    const bool tail = full < nblk && full % KW == wk;
     const int64_t c0 = (int64_t)full * kBlk + 16 * q;
-    u32x4 tw[2], tx[TT][2];
+    u32x4 tw[TN][2], tx[TT][2];
     if (tail) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) tw[h] = load_inside(wrow, c0 + 64 * h, p.k);
+      for (int h = 0; h < 2; ++h) {
 #pragma unroll
-      for (int c = 0; c < TT; ++c)
+        for (int a = 0; a < TN; ++a) tw[a][h] = load_inside(wrow(a), c0 + 64 * h, p.k);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) tx[c][h] = load_inside(xrow(c), c0 + 64 * h, p.k);
+        for (int c = 0; c < TT; ++c) tx[c][h] = load_inside(xrow(c), c0 + 64 * h, p.k);
+      }
     }
     if (mine > 0) {
-      static_for<0, R - 1>([&](auto i) { fetch(slots<TT, i.value>()[w], block_of(i.value)); });
+      static_for<0, R - 1>([&](auto i) { fetch(slots<TT, TN, i.value>()[w], block_of(i.value)); });
       int i = 0;
       const auto one = [&](auto h) {
         // the reads of the slot that is refilled next are done; so is this slot's block once it alone is left out
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        fetch(slots<TT, (h.value + R - 1) % R>()[w], block_of(i + R - 1));
+        fetch(slots<TT, TN, (h.value + R - 1) % R>()[w], block_of(i + R - 1));
         asm volatile("s_waitcnt vmcnt(%0)" ::"n"((R - 1) * kLoads) : "memory");
-        use(slots<TT, h.value>()[w]);
+        use(slots<TT, TN, h.value>()[w]);
         ++i;
       };
       while (i + R <= mine) static_for<0, R>(one);
@@ -338,30 +372,41 @@ int8_few_kernel(Int8Args p) {
     }
     if (tail) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const u32x4 wv = align_chunk(tw[h], c0 + 64 * h, p.k);
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int c = 0; c < TT; ++c) acc[c] = Tile<16>::product(wv, align_chunk(tx[c][h], c0 + 64 * h, p.k), acc[c]);
-      }
+        for (int a = 0; a < TN; ++a) {
+          const u32x4 wv = align_chunk(tw[a][h], c0 + 64 * h, p.k);
+#pragma unroll
+          for (int c = 0; c < TT; ++c) acc[c][a] = Tile<16>::product(wv, align_chunk(tx[c][h], c0 + 64 * h, p.k), acc[c][a]);
+        }
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // unused fetches write LDS: not after this work-group's end
   }
+  if constexpr (KW > 1) {
 #pragma unroll
-  for (int c = 0; c < TT; ++c) part[w][c][lane] = acc[c];
-  __syncthreads();
-  if (w < TT) {         // TT <= 4 waves
-    i32x4 v = part[0][w][lane];
+    for (int c = 0; c < TT; ++c)
 #pragma unroll
-    for (int i = 1; i < kFewWaves; ++i) v += part[i][w][lane];
-    const int64_t i = g.i0 + 16 * w + lr, j = j0 + 4 * q;
-    const float sx = scale_of(p, min(i, g.end - 1));
-    with_type(p.y_dtype, [&](auto zero) {
-      typedef decltype(zero) T;
-      f32x4 s, b;
-      load_channels<T>(p.sw + (int64_t)g.expert * p.n, p.bias ? (const T*)p.bias + (int64_t)g.expert * p.n : nullptr, j, p.n, s, b);
-      store4<T>((T*)p.Y, p.ld_y, nullptr, i, j, g.end, p.n, outputs(v, sx, s, b));
-    });
+      for (int a = 0; a < TN; ++a) part[w][c * TN + a][lane] = acc[c][a];
+    __syncthreads();
   }
+  with_type(p.y_dtype, [&](auto zero) {
+    typedef decltype(zero) T;
+#pragma unroll
+    for (int o = 0; o < kOwn; ++o) {
+      const int e = own(o);
+      if (e >= TT * TN) break;
+      i32x4 v;
+      if constexpr (KW > 1) {
+        v = part[0][e][lane];
+#pragma unroll
+        for (int i = 1; i < KW; ++i) v += part[i][e][lane];
+      } else {
+        v = acc[o / TN][o % TN];
+      }
+      store4<T>((T*)p.Y, p.ld_y, nullptr, g.i0 + 16 * (e / TN) + lr, j0 + 16 * (e % TN) + 4 * q, g.end, p.n,
+                outputs(v, sx[o], sw[o], bias[o]));
+    }
+  });
 }
 
 // ---------------------------------------------------------------- tiles by LDS
@@ -478,13 +523,11 @@ int8_dma_kernel(Int8Args p, int tiles_t, int tiles_n, int blocks_per_split, int*
   int64_t j0;
   if constexpr (GROUPED) {
     // experts' tiles by columns: neighbouring work-groups of one XCD share rows of W
-    int total;
-    find_rows<BT>(p, 0, total);
-    if ((int)blockIdx.x >= total * tiles_n) return;
-    const int id = (int)xcd_remap(blockIdx.x, (int64_t)total * tiles_n);
-    const int band = id / (8 * tiles_n), in = id - band * 8 * tiles_n, high = min(8, total - 8 * band);
-    int ignored;
-    g = find_rows<BT>(p, 8 * band + in % high, ignored);
+    const Experts<BT> experts(p);
+    if ((int)blockIdx.x >= experts.total * tiles_n) return;
+    const int id = (int)xcd_remap(blockIdx.x, (int64_t)experts.total * tiles_n);
+    const int band = id / (8 * tiles_n), in = id - band * 8 * tiles_n, high = min(8, experts.total - 8 * band);
+    g = experts.find(p, 8 * band + in % high);
     if (g.expert < 0) return;
     j0 = (int64_t)(in / high) * BN;
   } else {
@@ -497,7 +540,7 @@ int8_dma_kernel(Int8Args p, int tiles_t, int tiles_n, int blocks_per_split, int*
     j0 = (int64_t)(in / high) * BN;
   }
   const uint8_t* const W = p.W + g.expert * p.stride_w;
-  const int wi = (w % WT) * (BT / WT), wj = (w / WT) * (BN / WN);
+  const int wi = (w / WN) * (BT / WT), wj = (w % WN) * (BN / WN);      // waves of few rows spread over the SIMDs
   const int nblk = (int)((p.k + kBlk - 1) / kBlk);
   const int b0 = part * blocks_per_split, b1 = min(b0 + blocks_per_split, nblk);
 
@@ -566,7 +609,24 @@ int8_dma_kernel(Int8Args p, int tiles_t, int tiles_n, int blocks_per_split, int*
   // behind the last block, block 0, which is not used: with a fetch on every path the
   // counts of outstanding loads are known, and no read waits for a later block
   const auto next = [&](int step) { return step * WK + grp < count ? block_of(step * WK + grp) : 0; };
+  // the scales and biases go to LDS: asked for before the first block, written while it comes
+  __shared__ __attribute__((aligned(16))) float sxs[SPLIT ? 1 : BT], sws[SPLIT ? 4 : BN], biases[SPLIT ? 4 : BN];
+  float sx_t = 0.f, sw_t = 0.f, bias_t = -0.f;
+  if constexpr (!SPLIT) {
+    static_assert(BT <= kAll && BN <= kAll, "one of each per thread");
+    const int64_t j = min(j0 + t, p.n - 1);
+    sx_t = scale_of(p, min(g.i0 + t, g.end - 1));
+    sw_t = p.sw[(int64_t)g.expert * p.n + j];
+    if (p.bias) with_type(p.y_dtype, [&](auto zero) { bias_t = (float)((const decltype(zero)*)p.bias)[(int64_t)g.expert * p.n + j]; });
+  }
   if (!tail || grp > 0) fetch(std::integral_constant<int, 0>{}, next(0));
+  if constexpr (!SPLIT) {
+    if (t < BT) sxs[t] = sx_t;
+    if (t < BN) {
+      sws[t] = sw_t;
+      biases[t] = bias_t;
+    }
+  }
   int step = 0;
   // one(stage, whether the group has a block): only in the last step may it have none
   const auto run = [&](auto&& one) {
@@ -605,10 +665,12 @@ int8_dma_kernel(Int8Args p, int tiles_t, int tiles_n, int blocks_per_split, int*
           for (int l = 0; l < kLoads; ++l)
             if (l * kSpread / kLoads == k) fetch_one(stage_x<BT, WK, to>()[grp], stage_w<BN, WK, to>()[grp], b, l);
         }
+        if (!GROUPED || wi < rows_x) {         // products of rows that there are
 #pragma unroll
-        for (int c = 0; c < TT; ++c)
+          for (int c = 0; c < TT; ++c)
 #pragma unroll
-          for (int a = 0; a < TN; ++a) acc[c][a] = Tile<M>::product(wv[k & 1][a], xv[k & 1][c], acc[c][a]);
+            for (int a = 0; a < TN; ++a) acc[c][a] = Tile<M>::product(wv[k & 1][a], xv[k & 1][c], acc[c][a]);
+        }
         __builtin_amdgcn_sched_barrier(0);
       }
     });
@@ -622,40 +684,46 @@ int8_dma_kernel(Int8Args p, int tiles_t, int tiles_n, int blocks_per_split, int*
       if (i < TN) wv[set][k][i] = pick(s.rows, w0, i, set * kHalf + k);
       else xv[set][k][i - TN] = pick(x.rows, x0, i - TN, set * kHalf + k);
     };
-    const auto half = [&](int set, auto&& meanwhile) {
-#pragma unroll
-      for (int e = 0; e < kSlots; ++e) {
-        const int k = e / (TN * TT), c = e % (TN * TT) / TN, a = e % TN;
-        meanwhile(e);
-        acc[c][a] = Tile<M>::product(wv[set][k][a], xv[set][k][c], acc[c][a]);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    };
     put_tail();
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     fetch(std::integral_constant<int, 1>{}, next(1));
 #pragma unroll
     for (int l = 0; l < kReads; ++l) read(0, stage_x<BT, WK, 0>()[grp], stage_w<BN, WK, 0>()[grp], l);
-    run([&](auto i, bool) {
-      constexpr int h = i.value, to = h ^ 1;
-      half(0, [&](int e) {
+    // tiles: those of the wave's rows that there are, where it is not all
+    const auto blocks = [&](auto all, int tiles) {
+      const auto half = [&](int set, auto&& meanwhile) {
 #pragma unroll
-        for (int l = 0; l < kReads; ++l)
-          if (l * kSlots / kReads == e) read(1, stage_x<BT, WK, h>()[grp], stage_w<BN, WK, h>()[grp], l);
+        for (int e = 0; e < kSlots; ++e) {
+          const int k = e / (TN * TT), c = e % (TN * TT) / TN, a = e % TN;
+          meanwhile(e);
+          if (all || c < tiles) acc[c][a] = Tile<M>::product(wv[set][k][a], xv[set][k][c], acc[c][a]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      };
+      run([&](auto i, bool) {
+        constexpr int h = i.value, to = h ^ 1;
+        half(0, [&](int e) {
+#pragma unroll
+          for (int l = 0; l < kReads; ++l)
+            if (l * kSlots / kReads == e) read(1, stage_x<BT, WK, h>()[grp], stage_w<BN, WK, h>()[grp], l);
+        });
+        // the next block has arrived, and every wave has read this one
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        const int b = next(step + 2);
+        ++step;
+        half(1, [&](int e) {
+#pragma unroll
+          for (int l = 0; l < kLoads; ++l)
+            if (l * kSlots / 2 / kLoads == e) fetch_one(stage_x<BT, WK, h>()[grp], stage_w<BN, WK, h>()[grp], b, l);
+#pragma unroll
+          for (int l = 0; l < kReads; ++l)
+            if (l * kSlots / kReads == e) read(0, stage_x<BT, WK, to>()[grp], stage_w<BN, WK, to>()[grp], l);
+        });
       });
-      // the next block has arrived, and every wave has read this one
-      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-      const int b = next(step + 2);
-      ++step;
-      half(1, [&](int e) {
-#pragma unroll
-        for (int l = 0; l < kLoads; ++l)
-          if (l * kSlots / 2 / kLoads == e) fetch_one(stage_x<BT, WK, h>()[grp], stage_w<BN, WK, h>()[grp], b, l);
-#pragma unroll
-        for (int l = 0; l < kReads; ++l)
-          if (l * kSlots / kReads == e) read(0, stage_x<BT, WK, to>()[grp], stage_w<BN, WK, to>()[grp], l);
-      });
-    });
+    };
+    const int tiles = GROUPED ? __builtin_amdgcn_readfirstlane((rows_x - wi + M - 1) / M) : TT;
+    if (!GROUPED || tiles >= TT) blocks(std::true_type{}, TT);
+    else blocks(std::false_type{}, tiles);
   } else {
     static_assert(S % 2 == 0, "two sets of registers in turn");
     static_for<1, S>([&](auto i) { fetch(i, next(i.value)); });
@@ -730,50 +798,43 @@ int8_dma_kernel(Int8Args p, int tiles_t, int tiles_n, int blocks_per_split, int*
           const int64_t i = g.i0 + wi + M * c + lr, j = j0 + wj + M * a + 8 * (e / 4) + 4 * q + e % 4;
           if (i < p.m && j < p.n) mine[i * p.n + j] = acc[c][a][e];
         }
-    return;
   }
-  const float* const sw = p.sw + (int64_t)g.expert * p.n;
-  float sx[TT];
+  if constexpr (!SPLIT) {
+    float sx[TT];
 #pragma unroll
-  for (int c = 0; c < TT; ++c) sx[c] = scale_of(p, min(g.i0 + wi + M * c + lr, g.end - 1));
-  with_type(p.y_dtype, [&](auto zero) {
-    typedef decltype(zero) T;
-    const T* const bias = p.bias ? (const T*)p.bias + (int64_t)g.expert * p.n : nullptr;
-    const bool stream = (uint64_t)p.m * (uint64_t)p.n * sizeof(T) > (uint64_t)80 << 20;
-    constexpr int kLine = 128 / (int)sizeof(T);         // outputs of a store_lines
-    constexpr bool kLines = M == 32 && (BN / WN) % kLine == 0;
-    if constexpr (kLines) {
-      if (j0 + wj + BN / WN <= p.n) {         // the same for the whole wave
-        constexpr int kPer = kLine / 32;      // tiles
+    for (int c = 0; c < TT; ++c) sx[c] = sxs[wi + M * c + lr];
+    with_type(p.y_dtype, [&](auto zero) {
+      typedef decltype(zero) T;
+      // Outputs of more than 80 MiB go past the caches' keeping.
+      const bool stream = (uint64_t)p.m * (uint64_t)p.n * sizeof(T) > (uint64_t)80 << 20;
+      constexpr int kLine = 128 / (int)sizeof(T);         // outputs of a store_lines
+      constexpr bool kLines = M == 32 && (BN / WN) % kLine == 0;
+      const bool lines = kLines && j0 + wj + BN / WN <= p.n;       // the same for the whole wave
+      constexpr int kPer = kLines ? kLine / 32 : 1, kV = kPer * Tile<M>::kGroups;      // tiles and fours at a time
 #pragma unroll
-        for (int a = 0; a < TN; a += kPer) {
-          f32x4 s[4 * kPer], b[4 * kPer];
+      for (int a = 0; a < TN; a += kPer)
 #pragma unroll
-          for (int e = 0; e < 4 * kPer; ++e) load_channels_inside<T>(sw, bias, j0 + wj + 32 * a + 8 * e + 4 * q, s[e], b[e]);
+        for (int c = 0; c < TT; ++c) {
+          asm volatile("" ::: "memory");        // scales and biases read anew: kept, they would cost 64 registers
+          f32x4 v[kV];
 #pragma unroll
-          for (int c = 0; c < TT; ++c) {
-            f32x4 v[4 * kPer];
-#pragma unroll
-            for (int e = 0; e < 4 * kPer; ++e) v[e] = outputs(group<M>(acc[c][a + e / 4], e % 4), sx[c], s[e], b[e]);
-            store_lines<T>((T*)p.Y, p.ld_y, g.i0 + wi + 32 * c, j0 + wj + 32 * a, lane, g.end, stream, v);
+          for (int e = 0; e < kV; ++e) {
+            const int at = wj + M * a + 8 * e + 4 * q;
+            v[e] = outputs(group<M>(acc[c][a + e / Tile<M>::kGroups], e % Tile<M>::kGroups), sx[c], *(const f32x4*)(sws + at),
+                           *(const f32x4*)(biases + at));
           }
+          if constexpr (kLines) {
+            if (lines) {
+              store_lines<T>((T*)p.Y, p.ld_y, g.i0 + wi + 32 * c, j0 + wj + 32 * a, lane, g.end, stream, v);
+              continue;
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < kV; ++e)
+            store4<T>((T*)p.Y, p.ld_y, nullptr, g.i0 + wi + M * c + lr, j0 + wj + M * a + 8 * e + 4 * q, g.end, p.n, v[e]);
         }
-        return;
-      }
-    }
-#pragma unroll
-    for (int a = 0; a < TN; ++a)
-#pragma unroll
-      for (int e = 0; e < Tile<M>::kGroups; ++e) {
-        const int64_t j = j0 + wj + M * a + 8 * e + 4 * q;
-        f32x4 s, b;
-        load_channels<T>(sw, bias, j, p.n, s, b);
-#pragma unroll
-        for (int c = 0; c < TT; ++c)
-          store4<T>((T*)p.Y, p.ld_y, nullptr, g.i0 + wi + M * c + lr, j, g.end, p.n,
-                    outputs(group<M>(acc[c][a], e), sx[c], s, b));
-      }
-  });
+    });
+  }
 }
 
 // Y from the parts of a product split over k
@@ -823,36 +884,44 @@ hipError_t launch_dma(const Int8Plan& plan, const Int8Args& p, int* ws, hipStrea
   return hipGetLastError();
 }
 
+template <int TT, int TN, int KW, int R, bool GROUPED>
+hipError_t launch_few(const Int8Args& p, bool dma, hipStream_t s) {
+  const auto grid = [&](int tn, int kw) {
+    return dim3((unsigned)cdiv(p.n, 16 * tn * (kFewWaves / kw)), (unsigned)(GROUPED ? most_tiles(p.m, p.experts, 16 * TT) : 1));
+  };
+  if (dma) int8_few_kernel<TT, TN, KW, R, true, GROUPED><<<grid(TN, KW), 64 * kFewWaves, 0, s>>>(p);
+  else int8_few_kernel<TT, 1, kFewWaves, 1, false, GROUPED><<<grid(1, kFewWaves), 64 * kFewWaves, 0, s>>>(p);
+  return hipGetLastError();
+}
+
 template <bool GROUPED>
 hipError_t launch(const Int8Plan& plan, const Int8Args& p, void* ws, hipStream_t s) {
   const bool dma = direct(p);
-  const auto slots = [&](int bt) { return (unsigned)(GROUPED ? most_tiles(p.m, p.experts, bt) : 1); };
-  const unsigned few = (unsigned)cdiv(p.n, 16);
   switch (plan.kind) {
-    case kInt8Few16:
-      if (dma) int8_few_kernel<1, 2, true, GROUPED><<<dim3(few, slots(16)), 64 * kFewWaves, 0, s>>>(p);
-      else int8_few_kernel<1, 1, false, GROUPED><<<dim3(few, slots(16)), 64 * kFewWaves, 0, s>>>(p);
-      return hipGetLastError();
-    case kInt8Few32:
-      if (dma) int8_few_kernel<2, 2, true, GROUPED><<<dim3(few, slots(32)), 64 * kFewWaves, 0, s>>>(p);
-      else int8_few_kernel<2, 1, false, GROUPED><<<dim3(few, slots(32)), 64 * kFewWaves, 0, s>>>(p);
-      return hipGetLastError();
+    case kInt8Few16: return launch_few<1, 1, kFewWaves, 2, GROUPED>(p, dma, s);
+    case kInt8Few16Own:
+      if constexpr (GROUPED) return launch_few<1, 1, 1, 2, GROUPED>(p, dma, s);
+    case kInt8Few16OwnDeep: return launch_few<1, 1, 1, 4, GROUPED>(p, dma, s);
+    case kInt8Few32: return launch_few<2, 2, kFewWaves, 2, GROUPED>(p, dma, s);
     case kInt8Few64:
-      if (dma) int8_few_kernel<4, 2, true, GROUPED><<<dim3(few, slots(64)), 64 * kFewWaves, 0, s>>>(p);
-      else int8_few_kernel<4, 1, false, GROUPED><<<dim3(few, slots(64)), 64 * kFewWaves, 0, s>>>(p);
-      return hipGetLastError();
+      if constexpr (!GROUPED) return launch_few<4, 1, kFewWaves, 2, GROUPED>(p, dma, s);
     default: break;
   }
   if (!dma) {
-    int8_tile_kernel<GROUPED>
-        <<<dim3((unsigned)cdiv(p.n, kTile), GROUPED ? slots(kTile) : (unsigned)cdiv(p.m, kTile)), 256, 0, s>>>(p);
+    int8_tile_kernel<GROUPED><<<dim3((unsigned)cdiv(p.n, kTile), (unsigned)(GROUPED ? most_tiles(p.m, p.experts, kTile) : cdiv(p.m, kTile))),
+                                256, 0, s>>>(p);
     return hipGetLastError();
   }
   int* const parts = (int*)ws;
+  if constexpr (!GROUPED) {
+    switch (plan.kind) {
+      case kInt8T64x32: return launch_dma<GROUPED, 64, 32, 2, 2, 2, 4, kAhead>(plan, p, parts, s);
+      case kInt8T64x64: return launch_dma<GROUPED, 64, 64, 2, 2, 2, 4, kAhead>(plan, p, parts, s);
+      case kInt8T96x64: return launch_dma<GROUPED, 96, 64, 2, 2, 2, 3, kBlocks>(plan, p, parts, s);
+      default: break;
+    }
+  }
   switch (plan.kind) {
-    case kInt8T64x32: return launch_dma<GROUPED, 64, 32, 2, 2, 2, 4, kAhead>(plan, p, parts, s);
-    case kInt8T64x64: return launch_dma<GROUPED, 64, 64, 2, 2, 2, 4, kAhead>(plan, p, parts, s);
-    case kInt8T96x64: return launch_dma<GROUPED, 96, 64, 2, 2, 2, 3, kBlocks>(plan, p, parts, s);
     case kInt8T128x64: return launch_dma<GROUPED, 128, 64, 2, 2, 2, 3, kBlocks>(plan, p, parts, s);
     case kInt8T128x128Two: return launch_dma<GROUPED, 128, 128, 2, 2, 2, 2, kBlocks>(plan, p, parts, s);
     case kInt8T256x256: return launch_dma<GROUPED, 256, 256, 2, 4, 1, 2, kHalves>(plan, p, parts, s);
@@ -862,11 +931,26 @@ hipError_t launch(const Int8Plan& plan, const Int8Args& p, void* ws, hipStream_t
 
 }  // namespace
 
+// Which kernel (times: bf16 outputs, k = 4096 unless given, graph replays).
+//   few rows: up to 16 in waves that share rows of W (1 x 1536 4.2 us, with rows of their own
+//     6.0), in waves with rows of their own where those fill the card (1 x 11008 9.9 against
+//     11.0); up to 32 by 32 (29 x 5001 7.7, in tiles 8.0; but 32 x 11008 12.4 against 10.9); up to
+//     64 only where small tiles would not fill the card either (64 x 4096 7.8 against 8.2).
+//     Along k > 8192 few work-groups are too slow: split tiles.
+//   the smallest tiles that one round of 256 CUs covers: 128 x 4096 8.5 us in 64 x 32 tiles
+//     against 11.5 in the next; 320 x 4096 12.4 (96 x 64) against 21.3 and 14.6; 512 x 4096
+//     16.4 (128 x 64) against 21.7 and 20.7; 1024 x 4096 24.0 (128 x 128, two groups) against
+//     31.8 and 26.5 (one group).
+//   k in parts where one round is less than half full.
+//   beyond one round, 128 x 128 or 256 x 256, by their times in us: a 128 x 128 tile adds
+//     0.0064 + 0.00216 per block of k, a round of the larger ones takes 9.1 + 1.78, one of r
+//     tiles 0.38 + 0.62 r / 256 of that.  2048 x 4096 40 against 47 us, 4096 x 4096 78 against
+//     61, 4096 x 12288 209 against 171.
 Int8Plan int8_plan(int64_t m, int64_t n, int64_t k) {
   Int8Plan p{kInt8T128x128, 1, 0};
   const bool few = k > 8192 && n <= 1024 ? false : m <= 16 ? true : m <= 32 ? n <= 8192 : m <= 64 && n <= 4096 && k <= 4096;
   if (few) {
-    p.kind = m <= 16 ? kInt8Few16 : m <= 32 ? kInt8Few32 : kInt8Few64;
+    p.kind = m <= 16 ? (n > 8192 ? kInt8Few16OwnDeep : kInt8Few16) : m <= 32 ? kInt8Few32 : kInt8Few64;
     return p;
   }
   const struct { int kind, bt, bn; } small[] = {
@@ -889,9 +973,29 @@ Int8Plan int8_plan(int64_t m, int64_t n, int64_t k) {
   return p;
 }
 
+// By the mean part of the experts that can have one, as the parts themselves are known on the
+// device alone (times as above, experts x n; k = 4096 and 1500).
+//   few rows: waves of 16 with rows of W of their own (8 x 1536, 6 each: 8.6 us with k = 1500,
+//     256 x 256 tiles 24), with more blocks under way along a long k (2 of 8 x 4096, one each: 9.4
+//     against 11.4); where a long k and many rows of W leave each CU many waves anyway, waves that
+//     share them (64 x 1536, 4 each: 70 against 75), of 32 positions from 7 on (32 x 2048, 16
+//     each: 62 against 68).  They pay up to 16 positions each (32 x 2048, 24: 27 against 24 in 128 x
+//     128 tiles), up to 24 where such tiles do not fill the card (8 x 1536: 9.5 against 15.9), and
+//     those of 32 up to 32 (32 x 2048, 24: 68 against 72; 40: 82 against 83).
+//   tiles: 128 x 64, 128 x 128 by two groups of waves, 128 x 128 as one, two or more rounds of
+//     CUs take them (8 x 1536, 100 each: 13.6, 16.0 and 17.1; 200: 22.4, 16.4 and 17.3; 400: 32, 28
+//     and 21); 256 x 256 for large parts that fill the card, whose last tiles cost less as waves
+//     without rows leave out their products (16 x 4096, 512: 183 against 212; 200: 124 and 128).
 static Int8Plan grouped_plan(const Int8Args& p) {
-  const int64_t each = cdiv(p.m, std::min<int64_t>(p.m, p.experts));
-  return Int8Plan{each <= 16 ? kInt8Few16 : each <= 32 ? kInt8Few32 : each <= 64 ? kInt8T64x64 : each <= 200 ? kInt8T128x128 : kInt8T256x256, 1, 0};
+  const int64_t used = std::min<int64_t>(p.m, p.experts), each = cdiv(p.m, used);
+  const int64_t t128 = used * cdiv(each, 128) * cdiv(p.n, 128), t256 = used * cdiv(each, 256) * cdiv(p.n, 256);
+  int kind = kInt8T128x128;
+  if (p.k > 2048 && used * p.n >= 49152 && each <= 32) kind = each <= 6 ? kInt8Few16 : kInt8Few32;
+  else if (each <= 16 || (each <= 24 && t128 < 256)) kind = p.k > 2048 ? kInt8Few16OwnDeep : kInt8Few16Own;
+  else if (t128 <= 128) kind = kInt8T128x64;
+  else if (t128 <= 256) kind = kInt8T128x128Two;
+  else if (each >= 300 && t256 >= 192) kind = kInt8T256x256;
+  return Int8Plan{kind, 1, 0};
 }
 
 hipError_t int8_matmul_launch(const Int8Plan& plan, const Int8Args& p, void* ws, hipStream_t s) {
