@@ -21,9 +21,14 @@ model.  Biases are left as they are.
 
 Beside it, without calibration: ``quantize_model_fp8`` puts an ``Fp8Linear`` in the place
 of every nn.Linear (e4m3 weights in 128 x 128 tiles, inputs quantized per row on every
-call).  ``evaluate`` scores a model, quantized or not, on given texts: mean negative log
-probability and perplexity (the pages' loss and perplexity before and after), entropy,
-and how often the given token was the most probable one.
+call), ``quantize_model_int8`` an ``Int8Linear`` (int8 weights with a scale per channel, inputs
+with one per row), and an ``Int8Experts`` holds a stack of such layers of which every row
+chooses its own.  ``evaluate`` scores a model, quantized or not, on given texts: mean
+negative log probability and perplexity (the pages' loss and perplexity before and after),
+entropy, how often the given token was the most probable one, and how far its distributions
+are from those of the model before, of which ``top_logprobs`` keeps the top tokens.
+``distill_loss`` is that divergence for autograd, to tune what quantization leaves in
+floating point (norms, biases, the head) towards the model before.
 """
 from __future__ import annotations
 
@@ -33,9 +38,10 @@ from typing import Dict, List, Optional, Sequence
 
 import torch as _t
 
-from . import (NotPositiveDefinite, _torch, gptq_act_order_perm, gptq_dequantize, gptq_fp8_matmul, gptq_fp8_quantize,
-               gptq_hessian_accumulate, gptq_prepare_hinv, gptq_prepare_hinv_perm, gptq_quantize_layer,
-               gptq_quantize_layer_perm, gptq_token_logprobs)
+from . import (NotPositiveDefinite, _torch, gptq_act_order_perm, gptq_dequantize, gptq_distill_loss, gptq_fp8_matmul,
+               gptq_fp8_quantize, gptq_hessian_accumulate, gptq_int8_matmul, gptq_int8_matmul_grouped, gptq_int8_quantize,
+               gptq_prepare_hinv, gptq_prepare_hinv_perm, gptq_quantize_layer, gptq_quantize_layer_perm,
+               gptq_token_logprobs)
 
 
 @dataclasses.dataclass
@@ -136,19 +142,14 @@ def _own_rows(t):
     return t.clone(memory_format=_t.contiguous_format)
 
 
-class Fp8Linear(_t.nn.Module):
-    """A linear layer with e4m3 weights: y = dequantized(x) dequantized(W)^T + bias in
-    x's dtype (fp32, fp16 or bf16; with fp32 the sums are fp32 too, see gptq_fp8_matmul),
-    x's rows quantized on every call.  For inference: inputs that ask for a gradient are
-    refused."""
+class _CodedLayer(_t.nn.Module):
+    """What the layers of 8-bit codes share: buffers ``codes`` (bit patterns, which a cast of
+    the model leaves alone), ``scales`` and ``bias``; for inference."""
 
-    def __init__(self, weight, bias=None):
-        super().__init__()
-        self.out_features, self.in_features = weight.shape
-        codes, scales = gptq_fp8_quantize(_own_rows(weight.detach()), 128)
-        self.register_buffer("codes", codes.view(_t.uint8))      # bit patterns: a cast of the model leaves them alone
+    def _keep(self, codes, scales, bias):
+        self.register_buffer("codes", codes)
         self.register_buffer("scales", scales)
-        self.register_buffer("bias", None if bias is None else bias.detach().clone())
+        self.register_buffer("bias", None if bias is None else bias.detach().clone(memory_format=_t.contiguous_format))
 
     def _apply(self, fn, recurse=True):
         scales = self.scales
@@ -165,32 +166,136 @@ class Fp8Linear(_t.nn.Module):
     def _align_rows(self):
         """Rows of codes a multiple of 128 bytes apart again, which the product's fast kernels
         want: a move to another device and some ways of loading close the gaps."""
-        n, k = self.codes.shape
-        if self.codes.stride(0) % 16 or self.codes.stride(1) != 1:
-            codes = self.codes.new_zeros(n, (k + 127) // 128 * 128)[:, :k]
+        k = self.codes.shape[-1]
+        if any(s % 16 for s in self.codes.stride()[:-1]) or self.codes.stride(-1) != 1:
+            codes = self.codes.new_zeros(*self.codes.shape[:-1], (k + 127) // 128 * 128)[..., :k]
             self.codes = codes.copy_(self.codes)
 
-    def forward(self, x):
+    def _refuse_gradients(self, x):
         if x.requires_grad and _t.is_grad_enabled():
-            raise ValueError("Fp8Linear has no backward pass: detach its input or call it under torch.no_grad()")
-        codes, scales = gptq_fp8_quantize(_own_rows(x.reshape(-1, self.in_features)))
-        bias = self.bias if self.bias is None or self.bias.dtype == x.dtype else self.bias.to(x.dtype)
-        y = gptq_fp8_matmul(codes, scales, self.codes, self.scales, bias, out_dtype=x.dtype)
+            raise ValueError(f"{type(self).__name__} has no backward pass: detach its input or call it under torch.no_grad()")
+
+    def _bias_as(self, x):
+        return self.bias if self.bias is None or self.bias.dtype == x.dtype else self.bias.to(x.dtype)
+
+
+class _CodedLinear(_CodedLayer):
+    def __init__(self, weight, bias=None):
+        super().__init__()
+        self.out_features, self.in_features = weight.shape
+        self._keep(*self._code(_own_rows(weight.detach())), bias)
+
+    def forward(self, x):
+        self._refuse_gradients(x)
+        y = self._product(_own_rows(x.reshape(-1, self.in_features)), self._bias_as(x))
         return y.reshape(*x.shape[:-1], self.out_features)
 
     def extra_repr(self) -> str:
         return f"in_features={self.in_features}, out_features={self.out_features}, bias={self.bias is not None}"
 
 
-def _in_place_of(child):
-    """The Fp8Linear of a Linear, with its mode and its forward hooks: the same tables, so a
+class Fp8Linear(_CodedLinear):
+    """A linear layer with e4m3 weights: y = dequantized(x) dequantized(W)^T + bias in
+    x's dtype (fp32, fp16 or bf16; with fp32 the sums are fp32 too, see gptq_fp8_matmul),
+    x's rows quantized on every call.  For inference: inputs that ask for a gradient are
+    refused."""
+
+    @staticmethod
+    def _code(weight):
+        codes, scales = gptq_fp8_quantize(weight, 128)
+        return codes.view(_t.uint8), scales
+
+    def _product(self, x, bias):
+        return gptq_fp8_matmul(*gptq_fp8_quantize(x), self.codes, self.scales, bias, out_dtype=x.dtype)
+
+
+class Int8Linear(_CodedLinear):
+    """A linear layer with int8 weights, one scale per output channel: y = dequantized(x)
+    dequantized(W)^T + bias in x's dtype (fp32, fp16 or bf16), x's rows quantized on every call
+    with a scale each, sums exact.  A row with a NaN or an infinity gives a row of NaN.  For
+    inference: inputs that ask for a gradient are refused."""
+
+    @staticmethod
+    def _code(weight):
+        return gptq_int8_quantize(weight)
+
+    def _product(self, x, bias):
+        return gptq_int8_matmul(*gptq_int8_quantize(x), self.codes, self.scales, bias, out_dtype=x.dtype)
+
+
+class Int8Experts(_CodedLayer):
+    """A stack of int8 linear layers (weight [experts x out x in], bias [experts x out]) of
+    which every row chooses its own.  ``forward(x, experts)``: experts [... x top] (int32 or
+    int64) are each row's choices; x [... x in] gives one row for all of its choices, x [...
+    x top x in] one for each; the result is [... x top x out] in x's dtype.  A choice that is no
+    expert (negative, or too large) gives zeros.  Nothing is waited for: the sizes of the
+    experts' parts stay on the device.  For inference, as Int8Linear."""
+
+    def __init__(self, weight, bias=None):
+        super().__init__()
+        self.experts, self.out_features, self.in_features = weight.shape
+        codes, scales = gptq_int8_quantize(_own_rows(weight.detach().reshape(-1, self.in_features)))
+        self._keep(codes.view(weight.shape), scales.view(weight.shape[:2]), bias)
+
+    @classmethod
+    def of(cls, linears: Sequence):
+        """From nn.Linear layers of one shape, all with a bias or none."""
+        biases = [m.bias for m in linears]
+        if any(b is None for b in biases) != all(b is None for b in biases):
+            raise ValueError("some of the layers have a bias and some have none")
+        return cls(_t.stack([m.weight.detach() for m in linears]),
+                   None if biases[0] is None else _t.stack([b.detach() for b in biases]))
+
+    def forward(self, x, experts):
+        self._refuse_gradients(x)
+        if experts.dtype not in (_t.int32, _t.int64):
+            raise TypeError(f"experts: unsupported dtype {experts.dtype}")
+        each = x.shape[:-1] == experts.shape
+        if not each and x.shape[:-1] != experts.shape[:-1]:
+            raise ValueError(f"choices of shape {tuple(experts.shape)} for rows of shape {tuple(x.shape)}")
+        chosen, order = experts.reshape(-1).sort(stable=True)
+        offsets = _t.searchsorted(chosen, _t.arange(self.experts + 1, device=chosen.device, dtype=chosen.dtype), out_int32=True)
+        rows = (order if each else order // max(experts.shape[-1], 1)).to(_t.int32)
+        sorted_y = x.new_zeros(order.shape[0], self.out_features)       # rows of no expert stay zero
+        if order.shape[0]:
+            codes, scales = gptq_int8_quantize(_own_rows(x.reshape(-1, self.in_features)))
+            gptq_int8_matmul_grouped(codes, scales, self.codes, self.scales, offsets, rows, self._bias_as(x), Y=sorted_y)
+        y = _t.empty_like(sorted_y)
+        y[order] = sorted_y
+        return y.reshape(*experts.shape, self.out_features)
+
+    def extra_repr(self) -> str:
+        return (f"experts={self.experts}, in_features={self.in_features}, out_features={self.out_features}, "
+                f"bias={self.bias is not None}")
+
+
+def _in_place_of(child, kind):
+    """The layer of codes of a Linear, with its mode and its forward hooks: the same tables, so a
     hook's handle still removes it.  Backward hooks have nothing to wait for."""
-    layer = Fp8Linear(child.weight, child.bias)
+    layer = kind(child.weight, child.bias)
     layer.training = child.training
     for table in ("_forward_pre_hooks", "_forward_pre_hooks_with_kwargs", "_forward_hooks",
                   "_forward_hooks_with_kwargs", "_forward_hooks_always_called"):
         setattr(layer, table, getattr(child, table))
     return layer
+
+
+def _quantize_model_with(blocks: Sequence, kind) -> List[List[str]]:
+    names, made, places = [], {}, []
+    for block in blocks:
+        if isinstance(block, _t.nn.Linear):
+            raise ValueError(f"a block that is itself a Linear cannot be replaced in place: use {kind.__name__}")
+        names.append([])
+        for parent_name, parent in list(block.named_modules()):
+            for name, child in list(parent._modules.items()):     # under every name, a shared layer's too
+                if type(child) is _t.nn.Linear and {"weight", "bias"} <= child._parameters.keys():
+                    if id(child) not in made:
+                        made[id(child)] = _in_place_of(child, kind)
+                    places.append((parent, name, made[id(child)]))
+                    names[-1].append(f"{parent_name}.{name}" if parent_name else name)
+    for parent, name, layer in places:
+        setattr(parent, name, layer)
+    return names
 
 
 def quantize_model_fp8(blocks: Sequence) -> List[List[str]]:
@@ -201,21 +306,68 @@ def quantize_model_fp8(blocks: Sequence) -> List[List[str]]:
     every call (weight_norm, prune).  A layer's mode and forward hooks move to its Fp8Linear.  All
     layers are coded before the first one is replaced.  Returns the names of the replaced
     layers, block by block."""
-    names, made, places = [], {}, []
-    for block in blocks:
-        if isinstance(block, _t.nn.Linear):
-            raise ValueError("a block that is itself a Linear cannot be replaced in place: use Fp8Linear")
-        names.append([])
-        for parent_name, parent in list(block.named_modules()):
-            for name, child in list(parent._modules.items()):     # under every name, a shared layer's too
-                if type(child) is _t.nn.Linear and {"weight", "bias"} <= child._parameters.keys():
-                    if id(child) not in made:
-                        made[id(child)] = _in_place_of(child)
-                    places.append((parent, name, made[id(child)]))
-                    names[-1].append(f"{parent_name}.{name}" if parent_name else name)
-    for parent, name, layer in places:
-        setattr(parent, name, layer)
-    return names
+    return _quantize_model_with(blocks, Fp8Linear)
+
+
+def quantize_model_int8(blocks: Sequence) -> List[List[str]]:
+    """The same with an Int8Linear in the place of every nn.Linear (see quantize_model_fp8)."""
+    return _quantize_model_with(blocks, Int8Linear)
+
+
+class _DistillLoss(_t.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, ids, logprobs, temperature, tail):
+        ctx.save_for_backward(logits, ids, logprobs)
+        ctx.args = temperature, tail
+        return gptq_distill_loss(logits.detach(), ids, logprobs, temperature, tail)[0]
+
+    @staticmethod
+    @_t.autograd.function.once_differentiable
+    def backward(ctx, grad_loss):
+        logits, ids, logprobs = ctx.saved_tensors
+        _, grad = gptq_distill_loss(logits.detach(), ids, logprobs, *ctx.args, weights=grad_loss.contiguous(), want_grad=True)
+        return grad, None, None, None, None
+
+
+def distill_loss(logits, ids, logprobs, temperature: float = 1.0, tail: bool = False):
+    """gptq_distill_loss for autograd: the divergence of every row of logits [... x v] from the
+    teacher's top tokens (ids int32, logprobs fp32, both [... x top]), fp32 [...].  Reduce it as
+    you like; rows whose loss gets no gradient have none.  The logits are read again for the
+    gradient; nothing of their size is kept in between."""
+    if logprobs.requires_grad and _t.is_grad_enabled():
+        raise ValueError("distill_loss has no gradient for the teacher: detach logprobs")
+    if ids.shape != logprobs.shape or ids.shape[:-1] != logits.shape[:-1]:
+        raise ValueError(f"ids of shape {tuple(ids.shape)} and logprobs of shape {tuple(logprobs.shape)} for logits of "
+                         f"shape {tuple(logits.shape)}")
+    rows = _own_rows(logits.reshape(-1, logits.shape[-1]))
+    top = ids.shape[-1]
+    loss = _DistillLoss.apply(rows, ids.reshape(-1, top).contiguous(), logprobs.reshape(-1, top).contiguous(),
+                              float(temperature), bool(tail))
+    return loss.reshape(logits.shape[:-1])
+
+
+def top_logprobs(blocks: Sequence, head, x_batches: Sequence, top_k: int = 20, rows_per_call: int = 8192) -> List:
+    """A model's top_k tokens and their log probabilities at every position of ``x_batches``,
+    as ``evaluate`` and ``distill_loss`` take them of the model before quantization: per batch
+    (ids int32 [S x T x top_k], logprobs fp32 [S x T x top_k])."""
+    if rows_per_call < 1:
+        raise ValueError("rows_per_call must be at least 1")
+    kept = []
+    with _t.no_grad():
+        for x in x_batches:
+            shape = x.shape[:-1]
+            for block in blocks:
+                x = block(x)
+            hidden = x.reshape(-1, x.shape[-1])
+            none = _t.full((hidden.shape[0],), -1, dtype=_t.int64, device=x.device)
+            parts = []
+            for i in range(0, hidden.shape[0], rows_per_call):
+                rows = head(hidden[i:i + rows_per_call])
+                parts.append(gptq_token_logprobs(rows, none[i:i + rows_per_call], top_k)[2:])
+            if not parts:
+                parts = [(_t.empty(0, top_k, dtype=_t.int32, device=x.device), _t.empty(0, top_k, device=x.device))]
+            kept.append(tuple(_t.cat(p).reshape(*shape, top_k) for p in zip(*parts)))
+    return kept
 
 
 @dataclasses.dataclass
@@ -225,45 +377,58 @@ class Evaluation:
     perplexity: float        # e^nll
     entropy: float           # mean entropy of the model's distributions there, in nats
     accuracy: float          # share of positions whose most probable token is the given one
+    divergence: Optional[float] = None   # mean divergence from the teacher there, in nats
 
 
 def evaluate(blocks: Sequence, head, x_batches: Sequence, token_batches: Sequence,
-             rows_per_call: int = 8192) -> Evaluation:
+             rows_per_call: int = 8192, teacher: Optional[Sequence] = None) -> Evaluation:
     """Score a model on given texts.  ``blocks`` map each batch of ``x_batches`` [S x T x d]
     on, ``head`` (an nn.Linear, an Fp8Linear, any module) maps hidden rows [rows x d] to
     logits [rows x v] (fp32, fp16 or bf16); ``token_batches`` hold the tokens to be
     predicted there, int64 [S x T], negative where there is none (padding, a text's last
-    position).  The head and the scores run on at most ``rows_per_call`` rows at a time.  The
+    position).  ``teacher``: what top_logprobs gave for the same batches of another model; the
+    divergence from it is gptq_distill_loss with the tail, at the scored positions.  The head and the scores run on at most ``rows_per_call`` rows at a time.  The
     modules run in the mode they are in: call eval() on those with dropout first.  The device
     is waited for once, at the end."""
     if len(x_batches) != len(token_batches):
         raise ValueError("x_batches and token_batches differ in number")
+    if teacher is not None and len(teacher) != len(x_batches):
+        raise ValueError("x_batches and teacher differ in number")
     if rows_per_call < 1:
         raise ValueError("rows_per_call must be at least 1")
     sums, width = None, 0
     with _t.no_grad():
-        for x, tokens in zip(x_batches, token_batches):
+        for batch, (x, tokens) in enumerate(zip(x_batches, token_batches)):
             if tokens.shape != x.shape[:-1]:
                 raise ValueError(f"tokens of shape {tuple(tokens.shape)} for a batch of shape {tuple(x.shape)}")
             for block in blocks:
                 x = block(x)
             hidden, tok = x.reshape(-1, x.shape[-1]), tokens.reshape(-1).contiguous()
+            if teacher is not None:
+                if any(t.shape[:-1] != tokens.shape for t in teacher[batch]):
+                    raise ValueError(f"a teacher of shape {tuple(teacher[batch][0].shape)} for tokens of shape {tuple(tokens.shape)}")
+                best, best_lp = (t.reshape(-1, t.shape[-1]).contiguous() for t in teacher[batch])
             if sums is None:
-                sums = _t.zeros(5, dtype=_t.float64, device=x.device)
+                sums, nothing = _t.zeros(6, dtype=_t.float64, device=x.device), _t.zeros((), dtype=_t.float64, device=x.device)
             for i in range(0, hidden.shape[0], rows_per_call):
                 t = tok[i:i + rows_per_call]
                 logits = head(hidden[i:i + rows_per_call])
                 width = logits.shape[1]
                 lp, entropy, ids, _ = gptq_token_logprobs(logits, t, 1)
                 scored = t >= 0
+                apart = nothing
+                if teacher is not None:
+                    d, _ = gptq_distill_loss(logits, best[i:i + rows_per_call], best_lp[i:i + rows_per_call], tail=True)
+                    apart = d.double().masked_fill(~scored, 0.0).sum()
                 sums += _t.stack([scored.sum().double(), lp.double().sum(),
                                   entropy.double().masked_fill(~scored, 0.0).sum(),
                                   ((ids[:, 0] == t) & scored).sum().double(),
-                                  (t >= width).sum().double()])       # scored as NaN, refused below
-    n, lp, entropy, hits, above = [0.0] * 5 if sums is None else sums.tolist()
+                                  (t >= width).sum().double(), apart])       # scored as NaN, refused below
+    n, lp, entropy, hits, above, apart = [0.0] * 6 if sums is None else sums.tolist()
     if above > 0:
         raise ValueError(f"a token is not below the {width} logits")
     if n == 0:
         raise ValueError("no position holds a token to be scored")
     nll = -lp / n
-    return Evaluation(int(n), nll, math.inf if nll >= 700 else math.exp(nll), entropy / n, hits / n)
+    return Evaluation(int(n), nll, math.inf if nll >= 700 else math.exp(nll), entropy / n, hits / n,
+                      None if teacher is None else apart / n)
