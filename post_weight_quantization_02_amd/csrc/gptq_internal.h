@@ -114,6 +114,7 @@ struct Int8Plan {
   size_t ws_bytes;
 };
 Int8Plan int8_plan(int64_t m, int64_t n, int64_t k);
+Int8Plan int8_grouped_plan(int64_t m, int64_t n, int64_t k, int64_t experts);
 struct Int8Args {
   const uint8_t* X;
   int64_t ld_x;

@@ -986,12 +986,12 @@ Int8Plan int8_plan(int64_t m, int64_t n, int64_t k) {
 //     CUs take them (8 x 1536, 100 each: 13.6, 16.0 and 17.1; 200: 22.4, 16.4 and 17.3; 400: 32, 28
 //     and 21); 256 x 256 for large parts that fill the card, whose last tiles cost less as waves
 //     without rows leave out their products (16 x 4096, 512: 183 against 212; 200: 124 and 128).
-static Int8Plan grouped_plan(const Int8Args& p) {
-  const int64_t used = std::min<int64_t>(p.m, p.experts), each = cdiv(p.m, used);
-  const int64_t t128 = used * cdiv(each, 128) * cdiv(p.n, 128), t256 = used * cdiv(each, 256) * cdiv(p.n, 256);
+Int8Plan int8_grouped_plan(int64_t m, int64_t n, int64_t k, int64_t experts) {
+  const int64_t used = std::min(m, experts), each = cdiv(m, used);
+  const int64_t t128 = used * cdiv(each, 128) * cdiv(n, 128), t256 = used * cdiv(each, 256) * cdiv(n, 256);
   int kind = kInt8T128x128;
-  if (p.k > 2048 && used * p.n >= 49152 && each <= 32) kind = each <= 6 ? kInt8Few16 : kInt8Few32;
-  else if (each <= 16 || (each <= 24 && t128 < 256)) kind = p.k > 2048 ? kInt8Few16OwnDeep : kInt8Few16Own;
+  if (k > 2048 && used * n >= 49152 && each <= 32) kind = each <= 6 ? kInt8Few16 : kInt8Few32;
+  else if (each <= 16 || (each <= 24 && t128 < 256)) kind = k > 2048 ? kInt8Few16OwnDeep : kInt8Few16Own;
   else if (t128 <= 128) kind = kInt8T128x64;
   else if (t128 <= 256) kind = kInt8T128x128Two;
   else if (each >= 300 && t256 >= 192) kind = kInt8T256x256;
@@ -1002,6 +1002,8 @@ hipError_t int8_matmul_launch(const Int8Plan& plan, const Int8Args& p, void* ws,
   return launch<false>(plan, p, ws, s);
 }
 
-hipError_t int8_grouped_launch(const Int8Args& p, hipStream_t s) { return launch<true>(grouped_plan(p), p, nullptr, s); }
+hipError_t int8_grouped_launch(const Int8Args& p, hipStream_t s) {
+  return launch<true>(int8_grouped_plan(p.m, p.n, p.k, p.experts), p, nullptr, s);
+}
 
 }  // namespace gptq

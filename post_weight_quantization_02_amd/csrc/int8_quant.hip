@@ -152,8 +152,9 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void int8_rows_kernel(
   constexpr int kThreads = LANES < 256 ? 256 : LANES, kSpan = LANES * G * 8;
   __shared__ uint32_t part[kThreads / 64];
   const int t = threadIdx.x, lane = t % LANES;
-  const int64_t row = (int64_t)blockIdx.x * (kThreads / LANES) + t / LANES;
-  const bool there = LANES >= 256 || row < m;
+  const int64_t row = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * (kThreads / LANES) + t / LANES;
+  const bool there = row < m;
+  if (LANES >= 256 && !there) return;
   const auto* x = X + (there ? row : 0) * ld_x;
   uint8_t* out = codes + row * ld_codes;
   const bool odd = T::kWords == 4 && ((uintptr_t)x & 2) != 0;
@@ -213,9 +214,9 @@ void launch(const void* X, int64_t m, int64_t k, int64_t ld_x, uint8_t* codes, i
             hipStream_t s) {
   const auto go = [&](auto lanes, auto groups, auto few) {
     constexpr int kThreads = lanes.value < 256 ? 256 : lanes.value;
-    int8_rows_kernel<T, lanes.value, groups.value, few.value>
-        <<<dim3((unsigned)cdiv(m, kThreads / lanes.value)), kThreads, 0, s>>>((const typename T::elem*)X, m, (int)k, ld_x,
-                                                                             codes, ld_codes, scales);
+    const int64_t blocks = cdiv(m, kThreads / lanes.value), x = std::min<int64_t>(blocks, 1 << 20);
+    int8_rows_kernel<T, lanes.value, groups.value, few.value><<<dim3((unsigned)x, (unsigned)cdiv(blocks, x)), kThreads, 0, s>>>(
+        (const typename T::elem*)X, m, (int)k, ld_x, codes, ld_codes, scales);
   };
   using std::integral_constant;
   const std::false_type no;
