@@ -1,7 +1,9 @@
 """Build libgptq.so (gfx950) in-tree with hipcc.
 
 Every HIP source is compiled for gfx950 only, with packed-fp32 instruction
-selection disabled, then linked into ``_lib/libgptq.so`` next to this file.
+selection disabled, then linked into ``_lib/libgptq.so`` next to this file.  Beside
+it, ``_lib/_calls.so``: the binding's short way to some calls, host C++ against torch's
+headers.
 """
 from __future__ import annotations
 
@@ -18,6 +20,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIBDIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(LIBDIR, "libgptq.so")
+CALLS = os.path.join(LIBDIR, "_calls.so")
 
 SOURCES = ["panel_row_group.hip", "panel_row_grid.hip", "abi.cpp", "hessian.hip", "factor.hip", "gemm.hip",
            "quantize.hip", "packed.hip", "gptq2d.hip", "fp8_quant.hip", "fp8_matmul.hip", "logprobs.hip",
@@ -49,11 +52,33 @@ def _compile(src: str) -> str:
     return obj
 
 
+def build_calls() -> str:
+    """The extension of csrc/calls.cpp, which takes the library's addresses when it is loaded."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], INCLUDE]
+    lib = os.path.join(root, "lib")
+    tmp = CALLS + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", *("-isystem" + i for i in inc[:3]), f"-I{INCLUDE}",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", os.path.join(CSRC, "calls.cpp"), "-o", tmp,
+           f"-L{lib}", f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed for calls.cpp:\n{res.stdout}{res.stderr}")
+    os.replace(tmp, CALLS)
+    return CALLS
+
+
 def build(verbose: bool = True) -> str:
     os.makedirs(BUILD, exist_ok=True)
     os.makedirs(LIBDIR, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 4)) as ex:
+        calls = ex.submit(build_calls)
         objs = list(ex.map(_compile, SOURCES))
+        calls.result()
     tmp = LIB + ".tmp"
     cmd = [hipcc(), "-shared", f"--offload-arch={ARCH}", "-o", tmp, *objs]
     res = subprocess.run(cmd, capture_output=True, text=True)
