@@ -414,9 +414,30 @@ int8_few_kernel(Int8Args p) {
 // blocks in turn).  Each block of 128 columns goes to LDS without passing through registers
 // (16-byte direct loads, a wave's load filling 8 rows of 128 bytes), S - 1 blocks ahead of the
 // products, in S buffers that are variables of their own so that reading one does not wait for
-// the others' loads.  Row r keeps its 16-byte chunk c at place c ^ (r & 7): the rows that a
-// fragment load takes at one chunk then spread over all banks.  A last block of fewer than
+// the others' loads.  Row r keeps its 16-byte chunk c at place c ^ turn(r).  A last block of fewer than
 // 128 columns is taken first, through registers, with zeros behind column k.
+// 4096 x 12288 x 4096, fp16 outputs: 164 to 178 us from card to card, 2.3 to 2.5 POPS (the
+// library's int8 product 194, 2.1).  Matrix units busy 71 % of the cycles, at 1.6 of 2.4 GHz: a loop
+// of this instruction alone on random codes reaches 3.3 POPS (4.7 on zeros; 16 x 16 x 64
+// tiles 3.0), this kernel without loads and LDS reads 144 us where it takes 177, without loads
+// 151, without stores 169.  16 experts of 512 positions, 4096 x 4096, take 170 us where one of
+// 8192 takes 129: sixteen times the weights from HBM.  320 x 4096 x 4096 12.4 us: a work-group
+// fetches 655 KB through L2.  Not kept, no gain or slower: half blocks read ahead in the 128
+// x 128 tiles, 128 x 256 and 256 x 128 tiles, lines of later blocks touched ahead (5 to 8 %
+// slower), experts' whole tiles before their last ones (4 to 12 % slower: weights are read
+// twice), experts' tiles made alike.
+
+// LDS serves 16-byte reads of 16 lanes at a time, lanes 0 to 3, 12 to 15 and 20 to 27, then
+// 4 to 11, 16 to 19 and 28 to 31, and so on from 32, from 64 banks of 4 bytes: two rows of 128.
+// Lanes hold 16 rows at two chunks or 32 at one; of either, rows of one parity among those
+// lanes take eight different places (with r & 7 for 32 rows they met in pairs: 19e6 cycles of
+// conflicts in the CUs' 71e6 at 4096 x 12288 x 4096, now none; 175.2 us became 174.2, as what
+// holds that case is the power of its products).
+template <int M>
+__device__ __forceinline__ int turn(int r) {
+  return M == 32 ? (r >> 1) & 7 : r & 7;
+}
+
 template <int ROWS>
 struct __attribute__((aligned(16))) Stage {
   uint8_t rows[ROWS * kBlk];
@@ -550,16 +571,16 @@ int8_dma_kernel(Int8Args p, int tiles_t, int tiles_n, int blocks_per_split, int*
                                              : rsrc(p.X + g.i0 * p.ld_x, (rows_x - 1) * p.ld_x + p.k);
   const __amdgpu_buffer_rsrc_t wb = rsrc(W + j0 * p.ld_w, (rows_w - 1) * p.ld_w + p.k);
   // a lane's row and chunk in each of the wave's loads; rows past the end repeat the last
-  const int ch = ((lane & 7) ^ (lane >> 3)) * 16;
+  const auto chunk_of = [&](int l) { return (uint32_t)((lane & 7) ^ turn<M>(8 * l + (lane >> 3))) * 16; };
   uint32_t xo[kXLoads], wo[kWLoads];
 #pragma unroll
   for (int j = 0; j < kXLoads; ++j) {
     const int r = min((w * kXLoads + j) * 8 + (lane >> 3), rows_x - 1);
-    xo[j] = (uint32_t)((gathered ? row_of(p, g.i0 + r) : r) * p.ld_x) + ch;
+    xo[j] = (uint32_t)((gathered ? row_of(p, g.i0 + r) : r) * p.ld_x) + chunk_of(w * kXLoads + j);
   }
 #pragma unroll
   for (int j = 0; j < kWLoads; ++j)
-    wo[j] = (uint32_t)(min((w * kWLoads + j) * 8 + (lane >> 3), rows_w - 1) * p.ld_w) + ch;
+    wo[j] = (uint32_t)(min((w * kWLoads + j) * 8 + (lane >> 3), rows_w - 1) * p.ld_w) + chunk_of(w * kWLoads + j);
   const auto fetch_one = [&](Stage<BT>& x, Stage<BN>& s, int b, int l) {
     if (l < kXLoads) load16_to_lds(xb, x.rows + (w * kXLoads + l) * 8 * kBlk, xo[l], b * kBlk);
     else load16_to_lds(wb, s.rows + (w * kWLoads + l - kXLoads) * 8 * kBlk, wo[l - kXLoads], b * kBlk);
@@ -574,8 +595,8 @@ int8_dma_kernel(Int8Args p, int tiles_t, int tiles_n, int blocks_per_split, int*
 #pragma unroll
     for (int a = 0; a < TN; ++a) acc[c][a] = Sums(0);
   // a lane's first chunk of its row in the wave's first tile of each operand; the others by xor
-  const uint32_t x0 = (uint32_t)((wi + lr) * kBlk + ((q ^ (lr & 7)) * 16));
-  const uint32_t w0 = (uint32_t)((wj + lr) * kBlk + ((q ^ (lr & 7)) * 16));
+  const uint32_t x0 = (uint32_t)((wi + lr) * kBlk + ((q ^ turn<M>(lr)) * 16));
+  const uint32_t w0 = (uint32_t)((wj + lr) * kBlk + ((q ^ turn<M>(lr)) * 16));
   const auto pick = [&](const uint8_t* rows, uint32_t a, int tile, int step) {
     return *(const u32x4*)(rows + (a ^ (step * (64 / M) * 16)) + tile * M * kBlk);
   };
@@ -599,8 +620,8 @@ int8_dma_kernel(Int8Args p, int tiles_t, int tiles_n, int blocks_per_split, int*
     for (int i = 0; i < kTail; ++i) {
       const int id = t + i * kAll, r = id >> 3, c = id & 7;
       const u32x4 v = align_chunk(tail_v[i], (int64_t)(nblk - 1) * kBlk + 16 * c, p.k);
-      if (r < BT) *(u32x4*)(stage_x<BT, WK, 0>()[0].rows + r * kBlk + ((c ^ (r & 7)) * 16)) = v;
-      else if (r < BT + BN) *(u32x4*)(stage_w<BN, WK, 0>()[0].rows + (r - BT) * kBlk + ((c ^ (r & 7)) * 16)) = v;
+      if (r < BT) *(u32x4*)(stage_x<BT, WK, 0>()[0].rows + r * kBlk + ((c ^ turn<M>(r)) * 16)) = v;
+      else if (r < BT + BN) *(u32x4*)(stage_w<BN, WK, 0>()[0].rows + (r - BT) * kBlk + ((c ^ turn<M>(r - BT)) * 16)) = v;
     }
   };
   // the groups take the blocks in turn
