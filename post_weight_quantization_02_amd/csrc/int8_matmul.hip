@@ -232,8 +232,11 @@ __global__ __launch_bounds__(256) void int8_tile_kernel(Int8Args p) {
 // every fourth block of 128 columns of the same rows, and their sums meet in LDS at the end
 // (KW = 4), or rows of their own (KW = 1).  Each wave streams its blocks of W, and the rows of
 // X with them, through a ring of R LDS slots of its own, filled by direct loads R - 1 blocks
-// ahead: no barriers, and nothing in flight holds registers.  HBM-bound on W.  A last block of fewer than 128 columns goes through registers, asked for first and
-// multiplied last.
+// ahead: no barriers, and nothing in flight holds registers.  A last block of fewer than 128
+// columns goes through registers, asked for first and multiplied last.  HBM-bound on W: 1 x
+// 11008 x 4096 9.5 us, 4.7 TB/s of codes with a launch's 2.5 us in it; 29 x 5001 x 4163 7.9;
+// one token's 8 of 64 experts, 1536 x 4096 each, 11.2; 303 positions of 24 experts, 1999 x
+// 1111 each, 13.2.
 constexpr int kFewWaves = 4;
 
 template <int TT, int TN>
