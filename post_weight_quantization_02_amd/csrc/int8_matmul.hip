@@ -156,7 +156,8 @@ constexpr int kTile = 128;
 
 // ---------------------------------------------------------------- rows at any address
 // 128 x 128 outputs per work-group, 4 waves of 64 x 64, LDS filled through registers by
-// unaligned loads, block after block.
+// unaligned loads, block after block: 4096 x 12288 x 4096 with rows 4101 bytes apart 707 us, 320
+// x 4096 x 4096 94, bound by those loads (16-byte rows by direct loads 188 and 12.4).
 template <bool GROUPED>
 __global__ __launch_bounds__(256) void int8_tile_kernel(Int8Args p) {
   __shared__ u32x4 xt[kTile * 8], wt[kTile * 8];
@@ -419,16 +420,16 @@ int8_few_kernel(Int8Args p) {
 // products, in S buffers that are variables of their own so that reading one does not wait for
 // the others' loads.  Row r keeps its 16-byte chunk c at place c ^ turn(r).  A last block of fewer than
 // 128 columns is taken first, through registers, with zeros behind column k.
-// 4096 x 12288 x 4096, fp16 outputs: 164 to 178 us from card to card, 2.3 to 2.5 POPS (the
-// library's int8 product 194, 2.1).  Matrix units busy 71 % of the cycles, at 1.6 of 2.4 GHz: a loop
+// 4096 x 12288 x 4096, fp16 outputs: 164 to 197 us from card to card, 2.1 to 2.5 POPS (the
+// library's int8 product 194, 2.1).  Matrix units busy 72 % of the cycles, at 1.6 of 2.4 GHz: a loop
 // of this instruction alone on random codes reaches 3.3 POPS (4.7 on zeros; 16 x 16 x 64
 // tiles 3.0), this kernel without loads and LDS reads 144 us where it takes 177, without loads
 // 151, without stores 169.  16 experts of 512 positions, 4096 x 4096, take 170 us where one of
 // 8192 takes 129: sixteen times the weights from HBM.  320 x 4096 x 4096 12.4 us: a work-group
 // fetches 655 KB through L2.  Not kept, no gain or slower: half blocks read ahead in the 128
 // x 128 tiles, 128 x 256 and 256 x 128 tiles, lines of later blocks touched ahead (5 to 8 %
-// slower), experts' whole tiles before their last ones (4 to 12 % slower: weights are read
-// twice), experts' tiles made alike.
+// slower), experts' whole tiles before their last ones (4 to 12 % slower), experts' tiles
+// made alike.
 
 // LDS serves 16-byte reads of 16 lanes at a time, lanes 0 to 3, 12 to 15 and 20 to 27, then
 // 4 to 11, 16 to 19 and 28 to 31, and so on from 32, from 64 banks of 4 bytes: two rows of 128.
@@ -829,8 +830,12 @@ int8_dma_kernel(Int8Args p, int tiles_t, int tiles_n, int blocks_per_split, int*
     for (int c = 0; c < TT; ++c) sx[c] = sxs[wi + M * c + lr];
     with_type(p.y_dtype, [&](auto zero) {
       typedef decltype(zero) T;
-      // Outputs of more than 80 MiB go past the caches' keeping.
-      const bool stream = (uint64_t)p.m * (uint64_t)p.n * sizeof(T) > (uint64_t)80 << 20;
+      // Outputs of more than 80 MiB go past the caches' keeping where rows start at 64 bytes:
+      // 4096 x 12288 x 4096 fp16 188 us against 205, 1000 x 50000 x 1536 fp32 126 against 163.
+      // Other rows share lines: 1000 x 50001 x 1536 fp32 196 against 171, 4096 x 12289 x 4096
+      // fp16 216 against 222.  64 MiB: 4096 x 8192 x 1024 fp16 47 against 44.
+      const bool stream = (uint64_t)p.m * (uint64_t)p.n * sizeof(T) > (uint64_t)80 << 20 &&
+                          ((uintptr_t)p.Y | (uintptr_t)p.ld_y * sizeof(T)) % 64 == 0;
       constexpr int kLine = 128 / (int)sizeof(T);         // outputs of a store_lines
       constexpr bool kLines = M == 32 && (BN / WN) % kLine == 0;
       const bool lines = kLines && j0 + wj + BN / WN <= p.n;       // the same for the whole wave
