@@ -250,6 +250,8 @@ class Int8Experts(_CodedLayer):
         self._refuse_gradients(x)
         if experts.dtype not in (_t.int32, _t.int64):
             raise TypeError(f"experts: unsupported dtype {experts.dtype}")
+        if x.dim() < 1 or x.shape[-1] != self.in_features:
+            raise ValueError(f"rows of shape {tuple(x.shape)} for {self.in_features} features")
         each = x.shape[:-1] == experts.shape
         if not each and x.shape[:-1] != experts.shape[:-1]:
             raise ValueError(f"choices of shape {tuple(experts.shape)} for rows of shape {tuple(x.shape)}")

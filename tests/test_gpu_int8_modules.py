@@ -121,6 +121,16 @@ def test_experts_refuse_and_take_what_they_say():
     assert (e(x, c - 1) == 0).all() and "experts=3" in repr(e)
 
 
+@pytest.mark.parametrize("width", [16, 64, 33])
+def test_experts_refuse_rows_of_another_width(width):
+    """Rows of twice or half the width would be cut and joined to rows of the right one."""
+    e = P.Int8Experts(torch.randn(3, 20, 32, device="cuda"))
+    c = torch.zeros(4, 2, dtype=torch.int64, device="cuda")
+    for x in (torch.randn(4, width, device="cuda"), torch.randn(4, 2, width, device="cuda")):
+        with pytest.raises(ValueError, match="features"):
+            e(x, c)
+
+
 def test_layers_captured():
     """A block of an Int8Linear and experts in a graph: replays follow new inputs and choices."""
     q, e = P.Int8Linear(linear(64, 96).weight), P.Int8Experts(torch.randn(6, 64, 64, device="cuda"))
