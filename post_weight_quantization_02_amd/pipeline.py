@@ -350,10 +350,10 @@ def distill_loss(logits, ids, logprobs, temperature: float = 1.0, tail: bool = F
 
 def top_logprobs(blocks: Sequence, head, x_batches: Sequence, top_k: int = 20, rows_per_call: int = 8192) -> List:
     """A model's top_k tokens and their log probabilities at every position of ``x_batches``,
-    as ``evaluate`` and ``distill_loss`` take them of the model before quantization: per batch
-    (ids int32 [S x T x top_k], logprobs fp32 [S x T x top_k])."""
-    if rows_per_call < 1:
-        raise ValueError("rows_per_call must be at least 1")
+    as ``evaluate`` (with fewer of them than logits) and ``distill_loss`` take them of the model
+    before quantization: per batch (ids int32 [S x T x top_k], logprobs fp32 [S x T x top_k])."""
+    if rows_per_call < 1 or top_k < 1:
+        raise ValueError("rows_per_call and top_k must be at least 1")
     kept = []
     with _t.no_grad():
         for x in x_batches:
@@ -389,9 +389,10 @@ def evaluate(blocks: Sequence, head, x_batches: Sequence, token_batches: Sequenc
     logits [rows x v] (fp32, fp16 or bf16); ``token_batches`` hold the tokens to be
     predicted there, int64 [S x T], negative where there is none (padding, a text's last
     position).  ``teacher``: what top_logprobs gave for the same batches of another model; the
-    divergence from it is gptq_distill_loss with the tail, at the scored positions.  The head and the scores run on at most ``rows_per_call`` rows at a time.  The
-    modules run in the mode they are in: call eval() on those with dropout first.  The device
-    is waited for once, at the end."""
+    divergence from it is gptq_distill_loss with the tail, at the scored positions.  The head
+    and the scores run on at most ``rows_per_call`` rows at a time.  The modules run in the mode
+    they are in: call eval() on those with dropout first.  The device is waited for once, at the
+    end."""
     if len(x_batches) != len(token_batches):
         raise ValueError("x_batches and token_batches differ in number")
     if teacher is not None and len(teacher) != len(x_batches):

@@ -130,3 +130,10 @@ def test_refusals_are_clean_under_asan_and_ubsan():
     out = res.stdout + res.stderr
     assert "AddressSanitizer" not in out and "runtime error:" not in out, out[-4000:]
     assert res.returncode == 0 and "4 passed" in out, out[-4000:]
+
+
+def test_top_logprobs_refusals():
+    from post_weight_quantization_02_amd import pipeline as P
+    for kw in (dict(top_k=0), dict(top_k=-3), dict(rows_per_call=0)):
+        with pytest.raises(ValueError, match="at least 1"):
+            P.top_logprobs([], torch.nn.Linear(4, 6), [torch.zeros(1, 2, 4)], **kw)
