@@ -132,7 +132,7 @@ def test_refusals_are_clean_under_asan_and_ubsan():
     assert res.returncode == 0 and "4 passed" in out, out[-4000:]
 
 
-def test_top_logprobs_refusals():
+def test_top_logprobs_wants_a_token_at_least():
     from post_weight_quantization_02_amd import pipeline as P
     for kw in (dict(top_k=0), dict(top_k=-3), dict(rows_per_call=0)):
         with pytest.raises(ValueError, match="at least 1"):
