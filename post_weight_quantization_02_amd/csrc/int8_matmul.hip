@@ -549,9 +549,10 @@ int8_dma_kernel(Int8Args p, int tiles_t, int tiles_n, int blocks_per_split, int*
   if constexpr (GROUPED) {
     // experts' tiles by columns: neighbouring work-groups of one XCD share rows of W
     const Experts<BT> experts(p);
-    if ((int)blockIdx.x >= experts.total * tiles_n) return;
-    const int id = (int)xcd_remap(blockIdx.x, (int64_t)experts.total * tiles_n);
-    const int band = id / (8 * tiles_n), in = id - band * 8 * tiles_n, high = min(8, experts.total - 8 * band);
+    const int total = min(experts.total, tiles_t);      // offsets that decrease may ask for more
+    if ((int)blockIdx.x >= total * tiles_n) return;
+    const int id = (int)xcd_remap(blockIdx.x, (int64_t)total * tiles_n);
+    const int band = id / (8 * tiles_n), in = id - band * 8 * tiles_n, high = min(8, total - 8 * band);
     g = experts.find(p, 8 * band + in % high);
     if (g.expert < 0) return;
     j0 = (int64_t)(in / high) * BN;

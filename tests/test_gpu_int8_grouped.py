@@ -137,6 +137,23 @@ def test_bad_rows_and_offsets_stay_where_they_are(m):
     assert torch.equal(wide[1:1 + m // 4], ref[:m // 4]) and (wide[0] == 7.0).all() and (wide[-1] == 7.0).all()
 
 
+@pytest.mark.parametrize("m,n,experts", [(400, 300, 40), (3000, 1100, 12), (5000, 4100, 12)])
+def test_offsets_to_and_fro(m, n, experts):
+    """Offsets that ask for many times as many tiles as there are: rows unspecified, what lies
+    around Y as it is, and the next call right."""
+    k = 256
+    xc, sx = inputs(m, k, 15)
+    wc, sw = stack(experts, n, k, 16)
+    off = torch.tensor([0, m] * (experts // 2) + [0], dtype=torch.int32, device="cuda")
+    wide = torch.full((m + 2, n), 7.0, device="cuda")
+    G.gptq_int8_matmul_grouped(xc, sx, wc, sw, off, Y=wide[1:1 + m])
+    torch.cuda.synchronize()
+    assert (wide[0] == 7.0).all() and (wide[-1] == 7.0).all()
+    off = torch.tensor([0] * experts + [m], dtype=torch.int32, device="cuda")
+    y = G.gptq_int8_matmul_grouped(xc, sx, wc, sw, off)
+    assert torch.equal(y, G.gptq_int8_matmul(xc, sx, wc[-1], sw[-1]))
+
+
 def test_random_parts():
     rng = random.Random(7)
     for _ in range(25):
