@@ -314,6 +314,19 @@ def test_two_streams_and_given_workspaces():
     assert torch.equal(a, ref[0][0]) and torch.equal(b, ref[0][1]) and (ws[need:] == 0x5A).all()
 
 
+@pytest.mark.parametrize("at", [0, 8, 77, 1001])
+def test_workspace_at_any_address(at):
+    case = tuple(t.cuda() for t in make(3, 20000, 6, 9, "f32"))
+    need = G.gptq_distill_loss_workspace_size(3, 20000)
+    assert need > 0
+    ws = torch.full((at + need + 64,), 0x5A, dtype=torch.uint8, device="cuda")
+    got = G.gptq_distill_loss(*case, 1.0, True, want_grad=True, ws=ws[at:at + need])
+    ref = G.gptq_distill_loss(*case, 1.0, True, want_grad=True)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+    assert (ws[at + need:] == 0x5A).all() and (ws[:at] == 0x5A).all()
+
+
 @pytest.mark.parametrize("n,v", [(2, 30000), (5, 600), (600, 9000)])
 def test_graph_replays_match_eager(n, v):
     z, ids, lp = (t.cuda() for t in make(n, v, 6, 12, "bf16"))
