@@ -54,11 +54,11 @@ typedef enum {
   GPTQ_ERR_BAD_GROUP = 7,       /* group_size not 0 / 16k aligned with B  */
   GPTQ_ERR_WORKSPACE = 8,       /* ws NULL or smaller than the query      */
   GPTQ_ERR_BAD_DAMP = 9,        /* percdamp negative or not finite        */
+                                /* (a temperature: outside [1e-4, 1e4])    */
   GPTQ_ERR_LAUNCH = 10,         /* a HIP launch or runtime call failed    */
   GPTQ_ERR_TOO_LARGE = 11,      /* a size exceeds the library's limits    */
-  GPTQ_ERR_SCRATCH = 12,        /* shape too large for the no-allocation  */
+  GPTQ_ERR_SCRATCH = 12         /* shape too large for the no-allocation  */
                                 /* entry point's fixed workspace          */
-  GPTQ_ERR_BAD_TEMPERATURE = 13 /* temperature outside [1e-4, 1e4]        */
 } gptq_status;
 
 typedef enum {

@@ -433,7 +433,7 @@ gptq_status gptq_distill_loss(const void* logits, int32_t dtype, int64_t n, int6
   if (n < 0 || v <= 0 || top_k <= 0 || top_k > GPTQ_MAX_TOP || top_k > (tail ? v - 1 : v)) return GPTQ_ERR_BAD_SIZE;
   if (n > kMaxDim || v > kMaxDim) return GPTQ_ERR_TOO_LARGE;
   if (!elem_ok(dtype)) return GPTQ_ERR_BAD_DTYPE;
-  if (!(temperature >= 1e-4f && temperature <= 1e4f)) return GPTQ_ERR_BAD_TEMPERATURE;
+  if (!(temperature >= 1e-4f && temperature <= 1e4f)) return GPTQ_ERR_BAD_DAMP;
   if (n == 0) return GPTQ_OK;
   if (logits == nullptr || ids == nullptr || logprobs == nullptr || loss == nullptr) return GPTQ_ERR_NULL_POINTER;
   if (ld < v || (grad != nullptr && ld_grad < v)) return GPTQ_ERR_BAD_LEADING_DIM;
@@ -486,13 +486,12 @@ const char* gptq_status_string(int32_t status) {
     case GPTQ_ERR_BAD_BLOCK: return "block_size must be 16, 32, 64 or 128 (block_rows of fp8 codes: 1 or 128)";
     case GPTQ_ERR_BAD_GROUP: return "group_size must be 0, or a multiple of 16 that divides or is divided by block_size";
     case GPTQ_ERR_WORKSPACE: return "workspace missing or smaller than the query";
-    case GPTQ_ERR_BAD_DAMP: return "percdamp must be finite and >= 0";
+    case GPTQ_ERR_BAD_DAMP: return "percdamp must be finite and >= 0, a temperature between 1e-4 and 1e4";
     case GPTQ_ERR_LAUNCH: return "a HIP launch or runtime call failed";
     case GPTQ_ERR_TOO_LARGE: return "a size exceeds the library limits";
     case GPTQ_ERR_SCRATCH:
       return "the shape needs more workspace than the no-allocation entry point holds "
              "(gptq_quantize_layer_workspace_size > GPTQ_NOALLOC_SCRATCH_BYTES)";
-    case GPTQ_ERR_BAD_TEMPERATURE: return "temperature must be between 1e-4 and 1e4";
     default: return "unknown status";
   }
 }

@@ -17,7 +17,7 @@ pytestmark = pytest.mark.skipif(not os.path.exists(G.lib_path()),
                                 reason="libgptq.so not built (run __graft_entry__.build())")
 
 FAKE = 0x1000  # never dereferenced: validation fails first
-OK, NULL, SIZE, LD, DTYPE, WS, LARGE, TEMPERATURE = 0, 1, 2, 3, 4, 8, 11, 13
+OK, NULL, SIZE, LD, DTYPE, WS, LARGE, TEMPERATURE = 0, 1, 2, 3, 4, 8, 11, 9
 
 
 def test_quantize_refusals():
