@@ -78,11 +78,15 @@ __device__ __forceinline__ void load_channels(const float* __restrict__ sw, cons
   }
 }
 
-// The positions of one expert that a work-group takes: [i0, end), at most BT of them, and
-// the number of such tiles before.  Without experts, all rows are one's.
+// The positions of one expert that a work-group takes: [i0, end), at most BT of them.  Without
+// experts, all rows are one's.
 struct Rows {
   int64_t i0, end;
   int expert;
+};
+// an expert's positions, and the number of tiles of the experts before
+struct Part {
+  int from, to, expert, before;
 };
 
 // sum over the lanes up to this one
@@ -121,22 +125,28 @@ struct Experts {
     upto = lanes_up_to(mine);
     total = __builtin_amdgcn_readlane(upto, 63);
   }
-  // tile `slot`; expert < 0: there are not so many
-  __device__ __forceinline__ Rows find(const Int8Args& p, int slot) const {
-    if (slot >= total) return Rows{0, 0, -1};
+  // the expert that has tile `slot`; expert < 0: there are not so many
+  __device__ __forceinline__ Part part(const Int8Args& p, int slot) const {
+    if (slot >= total) return Part{0, 0, -1, 0};
     const int l = __builtin_ctzll(__ballot(upto > slot));      // the first lane that has it
     int before = __builtin_amdgcn_readlane(upto - mine, l);
     int a = __builtin_amdgcn_readlane(from, l), b = __builtin_amdgcn_readlane(to, l);
     for (int e = __builtin_amdgcn_readlane(e0, l); e < p.experts; ++e) {      // within that lane's experts
-      if (slot < before + tiles(a, b)) {
-        const int i0 = a + (slot - before) * BT;
-        return Rows{i0, min(i0 + BT, b), e};
-      }
+      if (slot < before + tiles(a, b)) return Part{a, b, e, before};
       before += tiles(a, b);
       a = b;
       b = at(p, min(e + 2, p.experts));
     }
-    return Rows{0, 0, -1};
+    return Part{0, 0, -1, 0};
+  }
+  // its tile `t`
+  static __device__ __forceinline__ Rows tile(const Part& e, int t) {
+    const int i0 = e.from + t * BT;
+    return Rows{i0, min(i0 + BT, e.to), e.expert};
+  }
+  __device__ __forceinline__ Rows find(const Int8Args& p, int slot) const {
+    const Part e = part(p, slot);
+    return tile(e, slot - e.before);
   }
 };
 
@@ -547,14 +557,18 @@ int8_dma_kernel(Int8Args p, int tiles_t, int tiles_n, int blocks_per_split, int*
   int part = 0;
   int64_t j0;
   if constexpr (GROUPED) {
-    // experts' tiles by columns: neighbouring work-groups of one XCD share rows of W
+    // work-groups of one XCD take neighbouring tiles of one expert, in bands as below (16
+    // experts of 512 x 4096 x 4096 171 us, with bands across experts 179; 32 of 400 x 2048 143
+    // and 157)
     const Experts<BT> experts(p);
     const int total = min(experts.total, tiles_t);      // offsets that decrease may ask for more
     if ((int)blockIdx.x >= total * tiles_n) return;
     const int id = (int)xcd_remap(blockIdx.x, (int64_t)total * tiles_n);
-    const int band = id / (8 * tiles_n), in = id - band * 8 * tiles_n, high = min(8, total - 8 * band);
-    g = experts.find(p, 8 * band + in % high);
-    if (g.expert < 0) return;
+    const Part e = experts.part(p, id / tiles_n);
+    if (e.expert < 0) return;
+    const int of_e = id - e.before * tiles_n, band = of_e / (8 * tiles_n), in = of_e - band * 8 * tiles_n;
+    const int high = min(8, Experts<BT>::tiles(e.from, e.to) - 8 * band);
+    g = Experts<BT>::tile(e, 8 * band + in % high);
     j0 = (int64_t)(in / high) * BN;
   } else {
     // work-groups of one XCD take neighbouring tiles: bands of 8 tiles along X, W outermost
