@@ -22,8 +22,7 @@
 // threads hold 256 KB; of a longer row the rest is read again), so 4096 x 65536 bf16 takes 220
 // us, 4.9 TB/s of the 5.15 that a large copy reaches (read twice: 259), 8192 x 32000 209, 1000 x
 // 128000 fp32 209 (298); the loss alone of 4096 x 65536 106 us, 5.0 TB/s.  517 x 50001 fp32
-// with 32 tokens 60 us: a row per CU, two rounds that read and write in step, and five rows
-// more.  Few short rows: a launch, and the chain of loads (ids, their logits), sums and logarithms: 5 us
+// with 32 tokens 58 us: two rows per CU, and five rows more that cost 10 of them.  Few short rows: a launch, and the chain of loads (ids, their logits), sums and logarithms: 5 us
 // for the loss, 8 with the gradient.
 #include "gptq_internal.h"
 
@@ -566,8 +565,14 @@ template <typename T>
 hipError_t launch(const DistillPlan& plan, const DistillArgs& p, void* ws, hipStream_t s) {
   const unsigned n = (unsigned)p.n;
   const int nvec = (int)(p.v / T::E);
-  // the smallest work-group and least registers that hold the row (8192 x 1500 bf16: 27 us by a
-  // wave, 40 by four)
+  // The smallest work-group and least registers that hold the row (8192 x 1500 bf16: 27 us by a
+  // wave, 40 by four; 4096 x 64000 221 by 512 threads, 262 by 1024), twice the threads where each
+  // row has a CU to itself (256 x 32001 bf16 17.3 us by 512, 20.8 by 256; 256 x 64000 22.1 by 1024,
+  // 24.8 by 512).  A row for 1024 threads leaves its CU no other one to read while it writes:
+  // beyond a row per CU it goes to 512 that read up to 5120 vectors again (300 x 50001 fp32,
+  // 12500 vectors, 36 us against 41, 1030 rows 93 against 103, 4096 x 45000 315 against 322; but
+  // 2000 x 56000, 14000 vectors, 188 against 182, and 256 x 50001 30 against 27.5).
+  const bool alone = p.n <= 256;
   if (plan.splits == 1 && p.grad && nvec > 0 && nvec <= 65536) {
     const auto go = [&](auto vpt, auto threads, auto more) {
       distill_held_kernel<T, vpt.value, threads.value, more.value><<<n, threads.value, 0, s>>>(p);
@@ -577,9 +582,13 @@ hipError_t launch(const DistillPlan& plan, const DistillArgs& p, void* ws, hipSt
     if (nvec <= 256) go(integral_constant<int, 4>{}, integral_constant<int, 64>{}, none);
     else if (nvec <= 512) go(integral_constant<int, 8>{}, integral_constant<int, 64>{}, none);
     else if (nvec <= 1024) go(integral_constant<int, 4>{}, integral_constant<int, 256>{}, none);
+    else if (nvec <= 2048 && alone) go(integral_constant<int, 4>{}, integral_constant<int, 512>{}, none);
     else if (nvec <= 2048) go(integral_constant<int, 8>{}, integral_constant<int, 256>{}, none);
+    else if (nvec <= 4096 && alone) go(integral_constant<int, 8>{}, integral_constant<int, 512>{}, none);
     else if (nvec <= 4096) go(integral_constant<int, 16>{}, integral_constant<int, 256>{}, none);
+    else if (nvec <= 8192 && alone) go(integral_constant<int, 8>{}, integral_constant<int, 1024>{}, none);
     else if (nvec <= 8192) go(integral_constant<int, 16>{}, integral_constant<int, 512>{}, none);
+    else if (nvec <= 13312 && !alone) go(integral_constant<int, 16>{}, integral_constant<int, 512>{}, integral_constant<int, 5120>{});
     else if (nvec <= 16384) go(integral_constant<int, 16>{}, integral_constant<int, 1024>{}, none);
     else go(integral_constant<int, 16>{}, integral_constant<int, 1024>{}, integral_constant<int, 49152>{});
     return hipGetLastError();

@@ -314,6 +314,23 @@ def test_two_streams_and_given_workspaces():
     assert torch.equal(a, ref[0][0]) and torch.equal(b, ref[0][1]) and (ws[need:] == 0x5A).all()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [256, 257])
+@pytest.mark.parametrize("vectors", [300, 2047, 2048, 2049, 4096, 4097, 8192, 8193, 9216, 9217, 13311, 13312, 13313, 16384, 16385])
+def test_gradients_where_the_work_groups_change(n, vectors, dtype):
+    """Row lengths and numbers around which other work-groups take a row: three rows against the
+    oracle, and every copy of them bit by bit."""
+    v = vectors * (4 if dtype == "f32" else 8) + 3
+    z, ids, lp = (t.cuda() for t in make(3, v, 17, vectors, dtype))
+    of = torch.arange(n, device="cuda") % 3
+    ids[1, 0] = v - 1                                    # behind the vectors
+    ids[2, 1] = v - 5                                    # in the last one
+    loss, grad = G.gptq_distill_loss(z[of], ids[of], lp[of], 1.0, True, want_grad=True)
+    torch.cuda.synchronize()
+    check(z, ids, lp, 1.0, True, None, loss[:3], grad[:3])
+    assert torch.equal(loss, loss[of]) and torch.equal(grad, grad[of])
+
+
 @pytest.mark.parametrize("at", [0, 8, 77, 1001])
 def test_workspace_at_any_address(at):
     case = tuple(t.cuda() for t in make(3, 20000, 6, 9, "f32"))
