@@ -22,7 +22,8 @@
 // threads hold 256 KB; of a longer row the rest is read again), so 4096 x 65536 bf16 takes 220
 // us, 4.9 TB/s of the 5.15 that a large copy reaches (read twice: 259), 8192 x 32000 209, 1000 x
 // 128000 fp32 209 (298); the loss alone of 4096 x 65536 106 us, 5.0 TB/s.  517 x 50001 fp32
-// with 32 tokens 58 us: two rows per CU, and five rows more that cost 10 of them.  Few short rows: a launch, and the chain of loads (ids, their logits), sums and logarithms: 5 us
+// with 32 tokens 58 us: two rows per CU, and five rows more that cost 11 of them.  Few
+// short rows: a launch, and the chain of loads (ids, their logits), sums and logarithms: 5 us
 // for the loss, 8 with the gradient.
 #include "gptq_internal.h"
 
