@@ -546,13 +546,17 @@ __global__ __launch_bounds__(kThreads) void distill_join_kernel(DistillArgs p, i
   const int part = GRAD ? (int)(blockIdx.x % splits) : 0;
   const float c = kLog2e / p.temperature;
   const Row<T> r(p, row);
+  Sum all{kLow, 0.f};
   if (t < 64) {
     read_listed<true>(p, r, row, t, sh);
     Sum a{kLow, 0.f};
     for (int i = t; i < splits; i += 64) a = join(a, parts[row * splits + i], c);
-    const float m = wave_maximum(a.m);
-    const float sum = wave_sum(a.s * __builtin_amdgcn_exp2f((a.m - m) * c));
-    const Rest g = finish(p, row, Sum{m, sum}, part == 0, sh);
+    all.m = wave_maximum(a.m);
+    all.s = wave_sum(a.s * __builtin_amdgcn_exp2f((a.m - all.m) * c));
+  }
+  __syncthreads();              // what finish reads was left in LDS by one lane
+  if (t < 64) {
+    const Rest g = finish(p, row, all, part == 0, sh);
     if (t == 0) rest = g;
   }
   if constexpr (GRAD) {
