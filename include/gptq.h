@@ -462,9 +462,15 @@ gptq_status gptq_int8_matmul_grouped(const int8_t* x_codes, int64_t ld_x, const 
  *                do as well: a constant cancels); q_r = 0.
  *     tail != 0: q_j = exp(logprobs[i][j]), log probabilities at that temperature already;
  *                q_r = max(0, 1 - sum_j q_j) and p_r stand for all tokens that are not listed
- *                together (top_k < v).  The loss is then never negative, 0 where the models
- *                agree, and at most the divergence over all tokens.
- *   A token that is listed twice counts with both its entries in q and once in p.
+ *                together (top_k < v).  Of tokens listed once each, the exact loss is then
+ *                never negative, 0 where the models agree, and at most the divergence over
+ *                all tokens.  What is returned is off by the rounding of its fp32 sums, at
+ *                most 2^-23 (v / 256 + 170 + 6 s + |loss|), s the mean of |z - max z| /
+ *                temperature under p or over the tokens that are not listed alone: rows of
+ *                models that agree give small numbers of either sign.
+ *   A token that is listed twice counts with both its entries in q and once in p; each entry has
+ *   its own term, so the loss may be negative, by up to the token's share of q times the log of
+ *   the number of its entries.
  *   grad: NULL, or [device] [n x ld_grad] (ld_grad >= v) of the logits' type: weights[i] (1
  *   where weights is NULL; [device] float [n]) times the gradient of loss[i]:
  *     Q = sum_j q_j + q_r;  listed tokens (Q p - q) / temperature, others p (Q - q_r / p_r) /

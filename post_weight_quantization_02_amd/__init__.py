@@ -891,7 +891,8 @@ def gptq_distill_loss(logits, ids, logprobs, temperature: float = 1.0, tail: boo
     all other tokens together, what is missing to 1.  Returns (loss fp32 [n], grad): grad, of
     logits' shape and dtype, is the loss's gradient times weights (fp32 [n]; 1 if not given)
     where ``want_grad`` or a tensor for it is given, else None.  Rows without entries have loss
-    and gradient 0, rows of weight 0 gradient 0.  pipeline.distill_loss is the same for
+    and gradient 0, rows of weight 0 gradient 0.  Rounding can leave rows of models that agree
+    a loss just below 0.  pipeline.distill_loss is the same for
     autograd."""
     if loss is None and grad is None and ws is None and stream is None:
         done = (_CALLS or _calls()).distill_loss(logits, ids, logprobs, temperature, tail, weights, want_grad)

@@ -28,3 +28,47 @@ def test_rows_in_parts_have_their_own_lists(n, v, dtype, tail):
         a, b = G.gptq_distill_loss(z[of], ids[of], lp[of], 1.0, tail, weights[of], want_grad=True)
         c, _ = G.gptq_distill_loss(z[of], ids[of], lp[of], 1.0, tail)
         assert torch.equal(a, loss[of]) and torch.equal(b, grad[of]) and torch.equal(c, alone[of])
+
+
+@pytest.mark.parametrize("T", [1.0, 2.0])
+@pytest.mark.parametrize("n,v,top,dtype", [(60, 3001, 40, "f32"), (200, 50001, 20, "bf16"), (3, 128000, 64, "f16"), (40, 300, 5, "f32")])
+def test_models_that_agree(n, v, top, dtype, T):
+    """A teacher that is the student: with 2 D the rounding of the sums (see test_gpu_distill), the
+    loss is at least -2 D.  The log probabilities are fp32: with e the largest relative error of
+    a q_j, at most 2^-23 max |log q_j|, the exact divergence is at most the chi-squared one,
+    sum (q - p)^2 / p <= e^2 (1 + 1 / p_r).  Of any teacher it is at most that over all tokens."""
+    z, _, _ = make(n, v, top, 3, dtype)
+    logp = torch.log_softmax(z.double() / T, 1)
+    best = torch.topk(logp, top, 1)
+    ids, lp = best.indices.to(torch.int32), best.values.float()
+    rest = 1 - best.values.exp().sum(1)
+    d = (z.double().amax(1, keepdim=True) - z.double()) / T
+    others = logp.scatter(1, best.indices, -torch.inf).softmax(1)
+    s = torch.maximum((logp.exp() * d).sum(1), (others * (d - d.scatter(1, best.indices, torch.inf).amin(1, keepdim=True))).sum(1))
+    two_d = 2.0 ** -23 * (v / 256 + 170 + 6 * s)
+    e = 2.0 ** -23 * lp.abs().amax(1).double()
+    assert (rest > 1e-3).all()
+    for loss, grad in (G.gptq_distill_loss(z.cuda(), ids.cuda(), lp.cuda(), T, True),
+                       G.gptq_distill_loss(z.cuda(), ids.cuda(), lp.cuda(), T, True, want_grad=True)):
+        got = loss.double().cpu()
+        assert (got >= -two_d * (1 + 1e-6)).all() and (got <= two_d * (1 + 1e-6) + e * e * (1 + 1 / rest)).all()
+        if grad is not None:        # p_v - q_v: the sums' rounding and e; to 16 bits at most twice that
+            assert (grad.double().cpu().abs().sum(1) <= 2 * (2 * two_d + 4 * e) / T).all()
+    other = (z.double() + torch.randn(n, v, generator=torch.Generator().manual_seed(1), dtype=torch.float64) * 0.1).to(z.dtype)
+    loss, _ = G.gptq_distill_loss(other.cuda(), ids.cuda(), lp.cuda(), T, True)
+    full = (logp.exp() * (logp - torch.log_softmax(other.double() / T, 1))).sum(1)
+    most = torch.maximum(s, ((other.double().amax(1, keepdim=True) - other.double()) / T).amax(1))
+    assert (loss.double().cpu() <= full * (1 + 2.0 ** -22) + 2.0 ** -23 * (v / 256 + 170 + 6 * most) + 2 * e * (1 + full)).all()
+
+
+def test_a_token_listed_twice_may_take_the_loss_below_0():
+    """Both entries have half of the token's probability: log 2 of its share below the divergence."""
+    z, ids, lp = (t.cuda() for t in make(5, 400, 3, 4, "f32", noise=0.0))
+    once, _ = G.gptq_distill_loss(z, ids, lp, 1.0, True)
+    half = lp - torch.log(torch.tensor(2.0, device="cuda"))
+    loss, grad = G.gptq_distill_loss(z, torch.cat([ids, ids], 1), torch.cat([half, half], 1), 1.0, True, want_grad=True)
+    share = lp.double().exp().sum(1) * torch.log(torch.tensor(2.0, dtype=torch.float64))
+    # lp is off by 2^-24 of itself from the half's, twice: a share of 2^-22 |lp|
+    assert ((loss.double() - once.double() + share.cuda()).abs() <= 2.0 ** -22 * (400 / 256 + 170 + 300) + 2.0 ** -22 * lp.abs().sum(1)).all()
+    assert (loss < 0).all()
+    check(z, torch.cat([ids, ids], 1), torch.cat([half, half], 1), 1.0, True, None, loss, grad)
