@@ -72,3 +72,41 @@ def test_a_token_listed_twice_may_take_the_loss_below_0():
     assert ((loss.double() - once.double() + share.cuda()).abs() <= 2.0 ** -22 * (400 / 256 + 170 + 300) + 2.0 ** -22 * lp.abs().sum(1)).all()
     assert (loss < 0).all()
     check(z, torch.cat([ids, ids], 1), torch.cat([half, half], 1), 1.0, True, None, loss, grad)
+
+
+@pytest.mark.parametrize("T,tail", [(1.0, True), (2.0, False)])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("n,v,top", [(9, 17, 5), (128, 50001, 20), (130, 20011, 9), (300, 33001, 8), (530, 70001, 5),
+                                     (515, 131072, 4), (514, 140005, 3), (600, 1003, 6), (12, 1 << 20, 10)])
+def test_equal_rows_have_equal_bits(n, v, top, dtype, T, tail):
+    """Three rows again and again: every copy's loss and gradient, bit by bit, and against the oracle."""
+    z, ids, lp = (t.cuda() for t in make(3, v, top, v, dtype, T=T))
+    of = torch.arange(n, device="cuda") % 3
+    weights = torch.tensor([1.5, -0.25, 0.75], device="cuda")
+    loss, grad = G.gptq_distill_loss(z[of], ids[of], lp[of], T, tail, weights[of], want_grad=True)
+    alone, _ = G.gptq_distill_loss(z[of], ids[of], lp[of], T, tail)
+    check(z, ids, lp, T, tail, weights, loss[:3], grad[:3])
+    check(z, ids, lp, T, tail, None, alone[:3], None)
+    assert torch.equal(loss, loss[:3][of]) and torch.equal(alone, alone[:3][of]) and torch.equal(grad, grad[:3][of])
+
+
+@pytest.mark.parametrize("T", [1e-4, 1e4])
+@pytest.mark.parametrize("n,v", [(5, 3000), (3, 40001), (257, 9001)])
+def test_gradients_at_extreme_temperatures(n, v, T):
+    """T = 1e-4: all but a row's largest token have probability 0; 1e4: all have nearly the same."""
+    z, ids, lp = make(n, v, 5, 4, "f32", T=T)
+    for tail in (False, True):
+        loss, grad = G.gptq_distill_loss(z.cuda(), ids.cuda(), lp.cuda(), T, tail, want_grad=True)
+        check(z, ids, lp, T, tail, None, loss, grad, range(min(n, 5)))
+        if T == 1e4:
+            assert (grad != 0).all(1).sum() == n
+        else:
+            # a gap of 0.02 to the second token is e^-200 of the first's probability, 0 in fp32 also as
+            # a gradient (e^-200 / T = 1e-83): rows of one most probable token have gradient 0, and
+            # others 1 / T at both models'
+            best, gap = z.argmax(1), (z.topk(2, 1).values @ torch.tensor([1.0, -1.0])) > 0.02
+            sure = gap & (lp[:, 0] - lp[:, 1] > 0.02 / T)
+            same, other = sure & (best == ids[:, 0]), sure & (best != ids[:, 0])
+            g, top = grad.cpu().double(), torch.stack([best, ids[:, 0].long()], 1)
+            assert (g[same] == 0).all() and ((g != 0).sum(1)[other] == 2).all() and other.any()
+            assert torch.allclose(g.gather(1, top)[other], torch.tensor([1 / T, -1 / T], dtype=torch.float64), rtol=2.0 ** -20)
