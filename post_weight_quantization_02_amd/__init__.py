@@ -151,27 +151,45 @@ def library() -> ctypes.CDLL:
 _CALLS = None
 
 
+class _NoCalls:
+    """In the place of the extension where there is none: leaves every call to the binding's own path."""
+    int8_quantize = int8_matmul = int8_matmul_grouped = distill_loss = staticmethod(lambda *args: None)
+
+
+def _load_calls(path: str):
+    """The extension at ``path``, if it was built for this torch (its functions take tensors apart)."""
+    import importlib.machinery
+    import importlib.util
+    torch = _torch()
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is missing: build it with __graft_entry__.build() "
+                          "(python -m post_weight_quantization_02_amd._build)")
+    loader = importlib.machinery.ExtensionFileLoader("_calls", path)
+    calls = importlib.util.module_from_spec(importlib.util.spec_from_loader("_calls", loader))
+    loader.exec_module(calls)
+    here = f"{torch.__version__} {torch.version.git_version}"
+    if calls.torch_version != here:
+        raise ImportError(f"{path} was built for torch {calls.torch_version}, this is {here}")
+    lib = library()
+    names = ("gptq_int8_quantize", "gptq_int8_matmul_workspace_size", "gptq_int8_matmul", "gptq_int8_matmul_grouped",
+             "gptq_distill_loss_workspace_size", "gptq_distill_loss")
+    calls.bind({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names}, torch._C._get_tracing_state,
+               torch.autograd.forward_ad, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+    return calls
+
+
 def _calls():
     """The extension that does the ordinary forms of some calls in one step (csrc/calls.cpp):
-    its functions return None where a call is not such a one.  Built with the library."""
+    its functions return None where a call is not such a one.  Built with the library; where it
+    is missing or another torch's, that is said once and the binding's own path takes all calls."""
     global _CALLS
     if _CALLS is None:
-        import importlib.machinery
-        import importlib.util
-        torch = _torch()
-        path = os.path.join(_HERE, "_lib", "_calls.so")
-        if not os.path.exists(path):
-            raise RuntimeError(f"{path} is missing: build it with __graft_entry__.build() "
-                               "(python -m post_weight_quantization_02_amd._build)")
-        loader = importlib.machinery.ExtensionFileLoader("_calls", path)
-        calls = importlib.util.module_from_spec(importlib.util.spec_from_loader("_calls", loader))
-        loader.exec_module(calls)
-        lib = library()
-        names = ("gptq_int8_quantize", "gptq_int8_matmul_workspace_size", "gptq_int8_matmul", "gptq_int8_matmul_grouped",
-                 "gptq_distill_loss_workspace_size", "gptq_distill_loss")
-        calls.bind({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names}, torch._C._get_tracing_state,
-                   torch.autograd.forward_ad, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
-        _CALLS = calls
+        try:
+            _CALLS = _load_calls(os.path.join(_HERE, "_lib", "_calls.so"))
+        except ImportError as e:
+            import warnings
+            _CALLS = _NoCalls
+            warnings.warn(f"the int8 and distillation calls take 3 to 7 us more of the host each: {e}", RuntimeWarning, stacklevel=3)
     return _CALLS
 
 

@@ -64,7 +64,8 @@ def build_calls() -> str:
     lib = os.path.join(root, "lib")
     tmp = CALLS + ".tmp"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", *("-isystem" + i for i in inc[:3]), f"-I{INCLUDE}",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", os.path.join(CSRC, "calls.cpp"), "-o", tmp,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DBUILT_FOR_TORCH="{torch.__version__} {torch.version.git_version}"', os.path.join(CSRC, "calls.cpp"), "-o", tmp,
            f"-L{lib}", f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:

@@ -5,7 +5,8 @@
 // Each function returns None where anything is not as it takes it -- a tensor's device, type,
 // shape or strides, a gradient or tangent that is asked for, a trace, another current device,
 // a status that is not ok -- and the binding's own path then does the call or says what is
-// wrong with it.  Nothing is refused here.
+// wrong with it.  Nothing is refused here.  Tensors are taken apart by the headers of the
+// torch that this was built for, BUILT_FOR_TORCH, so the binding uses it with no other.
 #include <torch/csrc/python_headers.h>
 
 #include <ATen/core/Tensor.h>
@@ -264,4 +265,11 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nul
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__calls(void) { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__calls(void) {
+  PyObject* m = PyModule_Create(&module);
+  if (m != nullptr && PyModule_AddStringConstant(m, "torch_version", BUILT_FOR_TORCH) < 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}
