@@ -403,7 +403,8 @@ gptq_status gptq_token_logprobs(const void* logits, int32_t dtype, int64_t n, in
  *   column k are left as they are) and scales [device] float [m], with X ~ scale * code.
  *   Per row: a = max(max |x|, 2^-100), scale = a / 127, code = x * (127 * (1 / a)) to the
  *   nearest whole number, halves to even, each quotient and product rounded to fp32 first;
- *   |code| <= 127.  A row that holds a NaN or an infinity has scale NaN and codes 0.
+ *   |code| <= 127 and |x / scale - code| < 1/2 + 2^-15 (2^-14 where a passes 2^126).
+ *   A row that holds a NaN or an infinity has scale NaN and codes 0.
  *   m == 0 is a no-op.
  *
  * gptq_int8_matmul: Y [device] [m x n] (y_dtype GPTQ_F32, GPTQ_F16 or GPTQ_BF16, leading

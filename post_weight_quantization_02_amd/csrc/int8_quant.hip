@@ -2,10 +2,14 @@
 //
 // Per row: a = max |x|, a' = max(a, 2^-100), scale = a' / 127, code = rint(x (127 (1 / a'))),
 // to nearest even.  1 / a' and 127 times it are rounded to fp32 once per row and the product
-// with x once per element (a division per element would cost ten instructions where there is
-// time for four), so a code is x / scale to nearest, but for quotients within 2^-15 of a
-// half, and |code| <= 127 as 127 (1 + 2^-21) rounds to 127.  The floor keeps 127 / a' finite;
-// rows below it, zeros among them, get small codes or none.  A row with a NaN or an infinity has
+// with x once per element (a division of each element by the scale would cost ten instructions
+// where there is time for four).  With u = 2^-24 and the scale's own rounding a code is x / scale
+// to nearest but for quotients within 4 u 127 < 2^-15 of a half, or 7 u 127 < 2^-14 where a' passes
+// 2^126: 1 / a' is subnormal there and off by up to 4 u.  |code| <= 127, as the largest element's
+// product is at most 127 (1 + 6 u).  fl(127 / a') would be one rounding nearer and is not the
+// definition: it gives other codes in 4 places of a million (16-bit elements, 5003 x 11007).  The
+// floor keeps 127 / a' finite; rows below it, zeros among them, get small codes or none.  A row
+// with a NaN or an infinity has
 // no grid: its scale is NaN, which the product carries on, and its codes are 0.
 //
 // HBM-bound: one read of X, one byte written per element.  A row lives in the registers of
