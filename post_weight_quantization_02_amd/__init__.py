@@ -905,8 +905,9 @@ def gptq_distill_loss(logits, ids, logprobs, temperature: float = 1.0, tail: boo
     """Per row of logits [n x v] (fp32, fp16 or bf16) the divergence from a teacher's top
     tokens, ids int32 [n x top] (negative: no entry) and logprobs fp32 [n x top] as
     gptq_token_logprobs gives them: sum_j q_j (log q_j - log p(ids_j)), p = softmax(logits /
-    temperature).  q is softmax(logprobs / temperature); with ``tail`` exp(logprobs) and, for
-    all other tokens together, what is missing to 1.  Returns (loss fp32 [n], grad): grad, of
+    temperature).  q is softmax(logprobs / temperature); with ``tail`` exp(logprobs), log
+    probabilities at that temperature already, and, for all other tokens together, what is
+    missing to 1.  Returns (loss fp32 [n], grad): grad, of
     logits' shape and dtype, is the loss's gradient times weights (fp32 [n]; 1 if not given)
     where ``want_grad`` or a tensor for it is given, else None.  Rows without entries have loss
     and gradient 0, rows of weight 0 gradient 0.  Rounding can leave rows of models that agree

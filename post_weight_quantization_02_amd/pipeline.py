@@ -333,9 +333,12 @@ class _DistillLoss(_t.autograd.Function):
 
 def distill_loss(logits, ids, logprobs, temperature: float = 1.0, tail: bool = False):
     """gptq_distill_loss for autograd: the divergence of every row of logits [... x v] from the
-    teacher's top tokens (ids int32, logprobs fp32, both [... x top]), fp32 [...].  Reduce it as
-    you like; rows whose loss gets no gradient have none.  The logits are read again for the
-    gradient; nothing of their size is kept in between."""
+    teacher's top tokens (ids int32, logprobs fp32, both [... x top]), fp32 [...].  With ``tail``
+    logprobs are the teacher's at that same temperature: nothing here can tell those of another
+    one, which give another divergence (top_logprobs says how to get them); without, they are
+    taken at temperature 1 (or are logits) and divided by it.  Reduce it as you like; rows whose
+    loss gets no gradient have none.  The logits are read again for the gradient; nothing of their
+    size is kept in between."""
     if logprobs.requires_grad and _t.is_grad_enabled():
         raise ValueError("distill_loss has no gradient for the teacher: detach logprobs")
     if ids.shape != logprobs.shape or ids.shape[:-1] != logits.shape[:-1]:
@@ -351,7 +354,9 @@ def distill_loss(logits, ids, logprobs, temperature: float = 1.0, tail: bool = F
 def top_logprobs(blocks: Sequence, head, x_batches: Sequence, top_k: int = 20, rows_per_call: int = 8192) -> List:
     """A model's top_k tokens and their log probabilities at every position of ``x_batches``,
     as ``evaluate`` (with fewer of them than logits) and ``distill_loss`` take them of the model
-    before quantization: per batch (ids int32 [S x T x top_k], logprobs fp32 [S x T x top_k])."""
+    before quantization: per batch (ids int32 [S x T x top_k], logprobs fp32 [S x T x top_k]).
+    They are at temperature 1; for ``distill_loss`` with the tail at another temperature t, divide
+    the logits: ``head=lambda h: head(h).float() / t``."""
     if rows_per_call < 1 or top_k < 1:
         raise ValueError("rows_per_call and top_k must be at least 1")
     kept = []
