@@ -27,8 +27,10 @@ chooses its own.  ``evaluate`` scores a model, quantized or not, on given texts:
 negative log probability and perplexity (the pages' loss and perplexity before and after),
 entropy, how often the given token was the most probable one, and how far its distributions
 are from those of the model before, of which ``top_logprobs`` keeps the top tokens.
-``distill_loss`` is that divergence for autograd, to tune what quantization leaves in
-floating point (norms, biases, the head) towards the model before.
+``distill_loss`` is that divergence for autograd, to tune what ``quantize_model`` leaves in
+floating point (norms, biases, the head) towards the model before.  The layers of 8-bit codes
+have no backward pass and refuse inputs that ask for one: of a model with such layers only what
+lies behind the last of them can be tuned.
 """
 from __future__ import annotations
 
