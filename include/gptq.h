@@ -433,7 +433,9 @@ gptq_status gptq_token_logprobs(const void* logits, int32_t dtype, int64_t n, in
  *   values of y_dtype.  Rows of Y before offsets[0] and from offsets[experts] on are left as
  *   they are.  A rows[i] outside [0, rows_x) gives a row of NaN; offsets outside [0, m] are
  *   taken as the nearer end, and where they decrease the rows concerned are unspecified.
- *   The sizes of the experts' parts are not needed on the host.  No workspace.
+ *   The sizes of the experts' parts are not needed on the host.  No workspace.  Fast under the
+ *   conditions of gptq_int8_matmul, stride_w too a multiple of 16 and, with rows, X of at most
+ *   2^31 bytes (rows_x * ld_x).
  */
 gptq_status gptq_int8_quantize(const void* X, int32_t x_dtype, int64_t m, int64_t k, int64_t ld_x, int8_t* codes,
                                int64_t ld_codes, float* scales, void* stream);

@@ -21,7 +21,10 @@
 // HBM-bound on long texts: the gradient's row stays in registers between its two passes (1024
 // threads hold 256 KB; of a longer row the rest is read again), so 4096 x 65536 bf16 takes 220
 // us, 4.9 TB/s of the 5.15 that a large copy reaches (read twice: 259), 8192 x 32000 209, 1000 x
-// 128000 fp32 209 (298); the loss alone of 4096 x 65536 106 us, 5.0 TB/s.  517 x 50001 fp32
+// 128000 fp32 209 (298); the loss alone of 4096 x 65536 106 us, 5.0 TB/s.  The forms of 16 vectors a
+// thread are held to 128 registers, four waves a SIMD, and spill a few: fp32 4 to 8 (20 bytes of
+// scratch a thread), 16-bit types 16 (36 bytes) with 256 and 512 threads, 4 or 5 (20 to 24) with 1024;
+// those of 4 and 8 vectors spill none.  517 x 50001 fp32
 // with 32 tokens 58 us: two rows per CU, and five rows more that cost 11 of them.  Few
 // short rows: a launch, and the chain of loads (ids, their logits), sums and logarithms: 5 us
 // for the loss, 8 with the gradient.
@@ -445,7 +448,7 @@ __global__ __launch_bounds__(THREADS) void distill_row_kernel(DistillArgs p) {
   }
 }
 
-// A row per work-group, kept in its registers: read once, written once.  MORE > 0: a longer
+// A row per work-group, kept in its registers (but for a few spilled ones): read once, written once.  MORE > 0: a longer
 // row, of which up to MORE vectors are read again, the last ones first.
 template <typename T, int VPT, int THREADS, int MORE>
 __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(VPT == 16 ? 4 : VPT == 8 ? 5 : 6))) void

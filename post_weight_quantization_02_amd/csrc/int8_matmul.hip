@@ -1027,6 +1027,10 @@ Int8Plan int8_plan(int64_t m, int64_t n, int64_t k) {
 //     each: 62 against 68).  They pay up to 16 positions each (32 x 2048, 24: 27 against 24 in 128 x
 //     128 tiles), up to 24 where such tiles do not fill the card (8 x 1536: 9.5 against 15.9), and
 //     those of 32 up to 32 (32 x 2048, 24: 68 against 72; 40: 82 against 83).
+//     Narrow stacks, used * n of some thousands and k > 2048, have too few waves of rows of their own
+//     to fill the card and would do better with the ones that share them: one position each of 2 x
+//     1536 9.9 against 6.8, of 8 x 512 9.7 against 7.2, of 8 x 1536 13.5 and 13.4; with k = 1500 both
+//     take 5.6 at 2 x 1536.  The rule has no such border.
 //   tiles: 128 x 64, 128 x 128 by two groups of waves, 128 x 128 as one, two or more rounds of
 //     CUs take them (8 x 1536, 100 each: 13.6, 16.0 and 17.1; 200: 22.4, 16.4 and 17.3; 400: 32, 28
 //     and 21); 256 x 256 for large parts that fill the card, whose last tiles cost less as waves
