@@ -168,8 +168,10 @@ struct Shared {
 
 // Reads them, by one wave: lane j has token j.  Everything that does not depend on the row's
 // other tokens is taken here, while the row is on its way (ALL), or only where they are.
+// Every lane gets what finish needs of it; one lane leaves it in LDS too, for the kernels that
+// have a barrier before finish and would rather have the registers meanwhile.
 template <bool ALL, typename T, int PLACES>
-__device__ __forceinline__ void read_listed(const DistillArgs& p, const Row<T>& r, int64_t row, int lane, Shared<PLACES>& sh) {
+__device__ __forceinline__ Listed read_listed(const DistillArgs& p, const Row<T>& r, int64_t row, int lane, Shared<PLACES>& sh) {
   Listed l;
   int id = -1;
   float t = -INFINITY, z = -INFINITY;
@@ -234,7 +236,7 @@ __device__ __forceinline__ void read_listed(const DistillArgs& p, const Row<T>& 
   sh.element[lane] = there ? r.element(id) : 0;
   sh.next[lane] = next;
   sh.last[lane] = last;
-  if (!ALL) return;
+  if (!ALL) return l;
   // the student
   l.m = fmaximum(wave_maximum(z), kLow);
   const double d = ((double)z - (double)l.m) * inv;
@@ -244,6 +246,7 @@ __device__ __forceinline__ void read_listed(const DistillArgs& p, const Row<T>& 
   sh.u[lane] = u;
   sh.given[lane] = given;
   if (lane == 0) sh.listed = l;
+  return l;
 }
 
 // head[i] for the places [first, last): every thread of the work-group takes part
@@ -322,9 +325,8 @@ struct Rest {
 // taken before, moved from their own maximum to m.  Rows without a teacher token have loss and
 // gradient 0, rows of weight 0 gradient 0, whatever their logits are.
 template <int PLACES>
-__device__ __forceinline__ Rest finish(const DistillArgs& p, int64_t row, Sum r, bool store, Shared<PLACES>& sh) {
+__device__ __forceinline__ Rest finish(const DistillArgs& p, int64_t row, Listed l, Sum r, bool store, Shared<PLACES>& sh) {
   const int lane = threadIdx.x & 63;
-  const Listed l = sh.listed;
   const double inv = 1.0 / (double)p.temperature;
   const float m = fmaximum(r.m, l.m);
   const double dl = ((double)l.m - (double)m) * inv, dr = ((double)r.m - (double)m) * inv;
@@ -439,7 +441,7 @@ __global__ __launch_bounds__(THREADS) void distill_row_kernel(DistillArgs p) {
   if (t < 64) read_listed<true>(p, r, row, t, sh);
   const Sum a = over_threads<THREADS>(stream_sums<THREADS>(r, 0, r.places(), c, sh), c);
   if (t < 64) {
-    const Rest g = finish(p, row, a, true, sh);
+    const Rest g = finish(p, row, sh.listed, a, true, sh);
     if (t == 0) rest = g;
   }
   if constexpr (GRAD) {
@@ -499,7 +501,7 @@ distill_held_kernel(DistillArgs p) {
   }
   const Sum sum = over_threads<THREADS>(a, c);
   if (t < 64) {
-    const Rest g = finish(p, row, sum, true, sh);
+    const Rest g = finish(p, row, sh.listed, sum, true, sh);
     if (t == 0) rest = g;
   }
   __syncthreads();
@@ -549,17 +551,13 @@ __global__ __launch_bounds__(kThreads) void distill_join_kernel(DistillArgs p, i
   const int part = GRAD ? (int)(blockIdx.x % splits) : 0;
   const float c = kLog2e / p.temperature;
   const Row<T> r(p, row);
-  Sum all{kLow, 0.f};
   if (t < 64) {
-    read_listed<true>(p, r, row, t, sh);
+    const Listed l = read_listed<true>(p, r, row, t, sh);      // kept: no barrier stands between
     Sum a{kLow, 0.f};
     for (int i = t; i < splits; i += 64) a = join(a, parts[row * splits + i], c);
-    all.m = wave_maximum(a.m);
-    all.s = wave_sum(a.s * __builtin_amdgcn_exp2f((a.m - all.m) * c));
-  }
-  __syncthreads();              // what finish reads was left in LDS by one lane
-  if (t < 64) {
-    const Rest g = finish(p, row, all, part == 0, sh);
+    const float m = wave_maximum(a.m);
+    const float sum = wave_sum(a.s * __builtin_amdgcn_exp2f((a.m - m) * c));
+    const Rest g = finish(p, row, l, Sum{m, sum}, part == 0, sh);
     if (t == 0) rest = g;
   }
   if constexpr (GRAD) {
