@@ -11,7 +11,7 @@
 // that nearly cancel, and the gradient over R is one multiple of 2^((z - M) c).  Differences
 // z - M are taken before they are scaled, so logits far from zero lose nothing.  Elements and
 // their sums are fp32; the at most 64 terms of a row's loss, which cancel where the two
-// models agree, are combined in 64 bits by one wave.
+// models agree, and the teacher's shares are worked out in 64 bits by one wave.
 //
 // Which vectors of a row hold listed tokens stands in LDS: a byte for each 16-byte vector,
 // the last listed token in it plus one, with a chain through the others.  All but a few
@@ -208,7 +208,7 @@ __device__ __forceinline__ Listed read_listed(const DistillArgs& p, const Row<T>
     l.sound = l.sum_q < INFINITY;
   } else {
     const float top = wave_maximum(t);
-    lq = (double)(t - top) * inv;
+    lq = ((double)t - (double)top) * inv;
     q = there ? exp(lq) : 0.0;
     const double sum = wave_sum(q);
     q /= sum;

@@ -110,3 +110,20 @@ def test_gradients_at_extreme_temperatures(n, v, T):
             g, top = grad.cpu().double(), torch.stack([best, ids[:, 0].long()], 1)
             assert (g[same] == 0).all() and ((g != 0).sum(1)[other] == 2).all() and other.any()
             assert torch.allclose(g.gather(1, top)[other], torch.tensor([1 / T, -1 / T], dtype=torch.float64), rtol=2.0 ** -20)
+
+
+@pytest.mark.parametrize("T", [0.25, 0.7, 3.0])
+@pytest.mark.parametrize("n,v", [(6, 1200), (3, 70001), (300, 9000)])
+def test_the_teachers_shares_are_exact_to_fp32(n, v, T):
+    """Listed tokens that the student gives probability e^-1000: their gradients are -q_j / T, with q
+    worked out in 64 bits and rounded once (2^-24, and as much for all else)."""
+    g = torch.Generator().manual_seed(v)
+    z = torch.randn(n, v, generator=g)
+    ids = torch.stack([torch.randperm(v, generator=g)[:12] for _ in range(n)]).to(torch.int32)
+    z.scatter_(1, ids.long(), -1000.0 * T - 10)
+    lp = -torch.rand(n, 12, generator=g) * 12 * T
+    T = float(torch.tensor(T))                           # a C float; 0.7's rounding alone moves e^-12 by 3 2^-24
+    q = torch.softmax(lp.double() / T, 1)
+    _, grad = G.gptq_distill_loss(z.cuda(), ids.cuda(), lp.cuda(), T, False, want_grad=True)
+    got = grad.double().cpu().gather(1, ids.long())
+    assert ((got + q / T).abs() <= 2.0 ** -23 * q / T).all(), float(((got * T / q + 1).abs() * 2 ** 24).max())
